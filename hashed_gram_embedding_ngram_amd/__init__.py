@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -43,6 +44,24 @@ class _Launch(ctypes.Structure):
 class _Pool(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("row_scale", ctypes.c_void_p), ("slot_of_row", ctypes.c_void_p),
                 ("pool_rows", ctypes.c_int64), ("cached", ctypes.c_int64)]
+
+
+class _Fp8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("block_rows", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("rng_offset", ctypes.c_int64), ("p_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32),
+                ("state", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _AdamWStep(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint64)]
 
 
 _P = ctypes.c_void_p
@@ -89,6 +108,18 @@ _SIGNATURES = {
     "ngram_grad_gate_noalloc_max_elements": (ctypes.c_int64, []),
     "ngram_grad_gate_noalloc": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _P, _P]),
     "ngram_select_hot_rows": (ctypes.c_int, [_P, _I64, _I64, _P, ctypes.POINTER(ctypes.c_int64), _P, _I64, _P]),
+    "ngram_fp8_code_bytes": (ctypes.c_int64, [_I64, _I64]),
+    "ngram_fp8_scale_bytes": (ctypes.c_int64, [_I64, _I64, _I32]),
+    "ngram_quant_fp8": (ctypes.c_int, [_P, _I32, _I64, _I32, ctypes.POINTER(_Fp8), ctypes.POINTER(_Fp8), _P]),
+    "ngram_add_norm": (ctypes.c_int, [_P, _I32, _P, _I64, _I32, _P, ctypes.c_float, _P, _P, ctypes.POINTER(_Fp8), _P,
+                                      _P]),
+    "ngram_add_norm_grad_workspace_bytes": (ctypes.c_int64, [_I64, _I32]),
+    "ngram_add_norm_grad": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _I64, _I32, _P, _P, _P, _I64, _P]),
+    "ngram_project_fp8_workspace_bytes": (ctypes.c_int64, [_I64, _I64, _I64]),
+    "ngram_project_fp8": (ctypes.c_int, [ctypes.POINTER(_Fp8), ctypes.POINTER(_Fp8), _P, _I32, _P, _I64, _P]),
+    "ngram_adamw": (ctypes.c_int, [ctypes.POINTER(_AdamWTensor), _I32, ctypes.POINTER(_AdamWStep), _P]),
+    "ngram_adamw_rows": (ctypes.c_int, [ctypes.POINTER(_AdamWTensor), _I64, _I32, _P, _I64, _P,
+                                        ctypes.POINTER(_AdamWStep), _P]),
 }
 
 _lib = None
@@ -657,3 +688,250 @@ def ngram_grad_gate_noalloc(rows, dout, eN, grad_Wg_out=None, stream=None):
     _check(lib().ngram_grad_gate_noalloc(_ptr(rows), _ptr(dout), _ptr(eN), n, d, _ptr(grad_Wg_out), _stream(stream)),
            "ngram_grad_gate_noalloc")
     return grad_Wg_out
+
+
+F32 = 0
+BF16 = 1
+STATE_F32 = 0
+STATE_FP8 = 1
+FP8_BLOCK = 128
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+_BYTES = (torch.uint8, torch.float8_e8m0fnu)
+_VALUES = (torch.float32,) + _BF16
+
+
+def _value(t):
+    """The ngram_value of a tensor that _dev has checked against _VALUES."""
+    return F32 if t.dtype == torch.float32 else BF16
+
+
+class Fp8:
+    """An 8-bit matrix: E4M3 ``codes`` [rows][128 ceil(cols / 128)] and E8M0
+    ``scales``, one byte per 128 columns of a row (``block_rows`` 1) or of 128
+    rows (128); see "8-bit matrices" in ngram.h."""
+
+    def __init__(self, codes, scales, rows: int, cols: int, block_rows: int = 1):
+        self.rows, self.cols, self.block_rows = int(rows), int(cols), int(block_rows)
+        need_codes = lib().ngram_fp8_code_bytes(self.rows, self.cols)
+        need_scales = lib().ngram_fp8_scale_bytes(self.rows, self.cols, self.block_rows)
+        if need_codes < 0 or need_scales < 0:
+            raise NgramError(f"no 8-bit matrix has rows={rows}, cols={cols}, block_rows={block_rows}")
+        _dev(codes, _CODES, "codes")
+        _dev(scales, _BYTES, "scales")
+        _need(codes, need_codes, "codes")
+        _need(scales, need_scales, "scales")
+        self.codes, self.scales = codes, scales
+        self._c = _Fp8(codes.data_ptr(), scales.data_ptr(), self.rows, self.cols, self.block_rows, 0)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda:0") -> "Fp8":
+        need = lib().ngram_fp8_code_bytes(int(rows), int(cols))
+        scale = lib().ngram_fp8_scale_bytes(int(rows), int(cols), int(block_rows))
+        if need < 0 or scale < 0:
+            raise NgramError(f"no 8-bit matrix has rows={rows}, cols={cols}, block_rows={block_rows}")
+        srows = int(rows) if block_rows == 1 else -(-int(rows) // FP8_BLOCK)
+        codes = torch.empty((int(rows), -(-int(cols) // FP8_BLOCK) * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=device)
+        scales = torch.empty((srows, scale // max(srows, 1)), dtype=torch.uint8, device=device)
+        return cls(codes, scales, rows, cols, block_rows)
+
+    @property
+    def c(self):
+        return ctypes.byref(self._c)
+
+
+def _fp8_c(q):
+    return None if q is None else q.c
+
+
+def ngram_quant_fp8(x, rows=True, transposed=False, block_rows: int = 1, q=None, qt=None, stream=None):
+    """x [n][d] (fp32 or bf16) in 8 bits: (q, qt), with None for the one that
+    is not wanted.  ``rows``: q, n x d; ``transposed``: qt, d x n; or pass
+    the Fp8 to fill.  See ngram_quant_fp8 in ngram.h."""
+    _dev(x, _VALUES, "x")
+    if x.dim() != 2:
+        raise NgramError("x must be [n][d]")
+    n, d = x.shape
+    if q is None and rows:
+        q = Fp8.empty(n, d, block_rows, x.device)
+    if qt is None and transposed:
+        qt = Fp8.empty(d, n, block_rows, x.device)
+    _check(lib().ngram_quant_fp8(_ptr(x), _value(x), n, d, _fp8_c(q), _fp8_c(qt), _stream(stream)), "ngram_quant_fp8")
+    return q, qt
+
+
+class NormOut(NamedTuple):
+    """ngram_add_norm's outputs; None for those not asked for."""
+    sum: Optional[torch.Tensor]
+    y: Optional[torch.Tensor]
+    q: Optional[Fp8]
+    r: Optional[torch.Tensor]
+
+
+def ngram_add_norm(x, gamma, eps, residual=None, sum_out=None, y_out=None, q_out=None, r_out=None, quantise=True,
+                   keep_y=False, keep_r=False, stream=None) -> NormOut:
+    """s = bf16(residual + x), y = s / rms(s) * gamma, and y in 8 bits, in one
+    pass (see ngram_add_norm in ngram.h).  ``sum_out`` receives s and may be
+    ``residual``; q, y (bf16) and r = 1 / rms are made where ``quantise``,
+    ``keep_y`` and ``keep_r`` ask for them or a buffer is passed."""
+    _dev(x, _VALUES, "x")
+    _dev(gamma, _F32, "gamma")
+    if x.dim() != 2:
+        raise NgramError("x must be [n][d]")
+    n, d = x.shape
+    if q_out is None and quantise:
+        q_out = Fp8.empty(n, d, 1, x.device)
+    if y_out is None and keep_y:
+        y_out = torch.empty((n, d), dtype=torch.bfloat16, device=x.device)
+    if r_out is None and keep_r:
+        r_out = torch.empty(n, dtype=torch.float32, device=x.device)
+    _dev(residual, _BF16, "residual", allow_none=True)
+    _dev(sum_out, _BF16, "sum_out", allow_none=True)
+    _dev(y_out, _BF16, "y_out", allow_none=True)
+    _dev(r_out, _F32, "r_out", allow_none=True)
+    _need(gamma, d, "gamma")
+    for t, name in ((residual, "residual"), (sum_out, "sum_out"), (y_out, "y_out")):
+        _need(t, n * d, name)
+    _need(r_out, n, "r_out")
+    _check(lib().ngram_add_norm(_ptr(x), _value(x), _ptr(residual), n, d, _ptr(gamma), float(eps), _ptr(sum_out),
+                                _ptr(y_out), _fp8_c(q_out), _ptr(r_out), _stream(stream)), "ngram_add_norm")
+    return NormOut(sum_out, y_out, q_out, r_out)
+
+
+def add_norm_grad_workspace(n: int, d: int, device="cuda:0"):
+    nbytes = int(lib().ngram_add_norm_grad_workspace_bytes(int(n), int(d)))
+    if nbytes < 0:
+        raise NgramError(f"no norm gradient has n={n}, d={d}")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def ngram_add_norm_grad(dy, sum, r, gamma, dsum=None, dx_out=None, dgamma_out=None, workspace=None, stream=None):
+    """(dx [n][d] bf16, dgamma [d] fp32) from dL/dy (fp32 or bf16) and the
+    forward's sum and r; ``dsum`` is the gradient that reaches the sum along
+    the residual stream (see ngram_add_norm_grad in ngram.h)."""
+    _dev(dy, _VALUES, "dy")
+    _dev(sum, _BF16, "sum")
+    _dev(r, _F32, "r")
+    _dev(gamma, _F32, "gamma")
+    _dev(dsum, _BF16, "dsum", allow_none=True)
+    if dy.dim() != 2:
+        raise NgramError("dy must be [n][d]")
+    n, d = dy.shape
+    dx_out = torch.empty((n, d), dtype=torch.bfloat16, device=dy.device) if dx_out is None else dx_out
+    dgamma_out = torch.empty(d, dtype=torch.float32, device=dy.device) if dgamma_out is None else dgamma_out
+    _dev(dx_out, _BF16, "dx_out")
+    _dev(dgamma_out, _F32, "dgamma_out")
+    for t, name in ((sum, "sum"), (dsum, "dsum"), (dx_out, "dx_out")):
+        _need(t, n * d, name)
+    _need(r, n, "r")
+    _need(gamma, d, "gamma")
+    _need(dgamma_out, d, "dgamma_out")
+    workspace = add_norm_grad_workspace(n, d, dy.device) if workspace is None else workspace
+    _check(lib().ngram_add_norm_grad(_ptr(dy), _value(dy), _ptr(sum), _ptr(r), _ptr(gamma), _ptr(dsum), n, d,
+                                     _ptr(dx_out), _ptr(dgamma_out), *_ws_args(workspace), _stream(stream)),
+           "ngram_add_norm_grad")
+    return dx_out, dgamma_out
+
+
+def project_fp8_workspace(m: int, n: int, k: int, device="cuda:0"):
+    """Workspace of ngram_project_fp8 for C [m][n] over k columns, or None
+    where the call needs none."""
+    nbytes = int(lib().ngram_project_fp8_workspace_bytes(int(m), int(n), int(k)))
+    if nbytes < 0:
+        raise NgramError(f"no 8-bit product has m={m}, n={n}, k={k}")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def ngram_project_fp8(a: Fp8, b: Fp8, out=None, dtype=torch.bfloat16, workspace=None, stream=None):
+    """out [a.rows][b.rows] (fp32 or bf16) = a b^T over their common columns
+    (see ngram_project_fp8 in ngram.h)."""
+    if out is None:
+        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
+    _dev(out, _VALUES, "out")
+    _need(out, a.rows * b.rows, "out")
+    if workspace is None:
+        workspace = project_fp8_workspace(a.rows, b.rows, a.cols, a.codes.device)
+    ws = (None, 0) if workspace is None else _ws_args(workspace)
+    _check(lib().ngram_project_fp8(a.c, b.c, _ptr(out), _value(out), *ws, _stream(stream)), "ngram_project_fp8")
+    return out
+
+
+def _step_c(step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed):
+    return _AdamWStep(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), float(grad_scale), int(step),
+                      int(seed) & 0xFFFFFFFFFFFFFFFF)
+
+
+def _adamw_tensor(p, g, m, v, m_scale, v_scale, rng_offset, name, g_numel=None, scale_rows=None):
+    _dev(p, _VALUES, f"{name}: p")
+    _dev(g, _VALUES, f"{name}: g")
+    n = p.numel()
+    _need(g, n if g_numel is None else g_numel, f"{name}: g")
+    if m.dtype == torch.float32:
+        if m_scale is not None or v_scale is not None:
+            raise NgramError(f"{name}: fp32 moments have no scales")
+        kinds, state = _F32, STATE_F32
+    else:
+        kinds, state = _CODES, STATE_FP8
+        need = -(-n // FP8_BLOCK) if scale_rows is None else scale_rows
+        for t, what in ((m_scale, "m_scale"), (v_scale, "v_scale")):
+            _dev(t, _BYTES, f"{name}: {what}")
+            _need(t, need, f"{name}: {what}")
+    for t, what in ((m, "m"), (v, "v")):
+        _dev(t, kinds, f"{name}: {what}")
+        _need(t, n, f"{name}: {what}")
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    return _AdamWTensor(at(p), at(g), at(m), at(v), at(m_scale), at(v_scale), n, int(rng_offset), _value(p), _value(g),
+                        state, 0)
+
+
+class AdamWTensors:
+    """The tensors of ngram_adamw: equal-length lists of parameters (fp32 or
+    bf16), gradients (fp32 or bf16) and moments, fp32 or 8-bit codes with
+    ``m_scales`` and ``v_scales`` (uint8, one byte per 128 elements).  Keeps
+    the tensors alive; build it again when one of them is another tensor.
+    ``rng_offsets``: each tensor's place in the random sequence (by default
+    one after the other, each at a multiple of 128)."""
+
+    def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, rng_offsets=None):
+        count = len(params)
+        none = [None] * count
+        m_scales, v_scales = m_scales or none, v_scales or none
+        if rng_offsets is None:
+            rng_offsets, at = [], 0
+            for p in params:
+                rng_offsets.append(at)
+                at += -(-p.numel() // FP8_BLOCK) * FP8_BLOCK
+        lists = (params, grads, m, v, m_scales, v_scales, rng_offsets)
+        if any(len(x) != count for x in lists):
+            raise NgramError("the lists must have one entry for each parameter")
+        self.tensors = [tuple(x) for x in zip(*lists[:6])]
+        self.count = count
+        self._c = (_AdamWTensor * max(count, 1))(*[_adamw_tensor(*x, name=f"tensor {i}") for i, x in enumerate(zip(*lists))])
+
+
+def ngram_adamw(tensors: AdamWTensors, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=1.0,
+                seed=0, stream=None):
+    """One AdamW step on every tensor, in place; ``step`` counts from 1 (see
+    ngram_adamw in ngram.h)."""
+    h = _step_c(step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed)
+    _check(lib().ngram_adamw(tensors._c, tensors.count, ctypes.byref(h), _stream(stream)), "ngram_adamw")
+
+
+def ngram_adamw_rows(p, m, v, rows, g, n_rows=None, m_scale=None, v_scale=None, *, lr, step, beta1=0.9, beta2=0.999,
+                     eps=1e-8, weight_decay=0.0, grad_scale=1.0, seed=0, stream=None):
+    """One AdamW step on rows ``rows`` of the table p [R][d] from the sparse
+    gradient (rows, g [max_rows][d], n_rows [1] int64 on the device) that
+    ngram_grad_table and ngram_grad_e1 return (see ngram_adamw_rows in
+    ngram.h)."""
+    if p.dim() != 2:
+        raise NgramError("p must be [R][d]")
+    R, d = p.shape
+    _dev(rows, _I32T, "rows")
+    max_rows = rows.numel()
+    if n_rows is not None:
+        _dev(n_rows, (torch.int64,), "n_rows")
+        _need(n_rows, 1, "n_rows")
+    t = _adamw_tensor(p, g, m, v, m_scale, v_scale, 0, "table", g_numel=max_rows * d, scale_rows=R * -(-d // FP8_BLOCK))
+    h = _step_c(step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed)
+    _check(lib().ngram_adamw_rows(ctypes.byref(t), R, d, _ptr(rows), max_rows, _ptr(n_rows), ctypes.byref(h),
+                                  _stream(stream)), "ngram_adamw_rows")

@@ -1,0 +1,663 @@
+// Residual addition, root-mean-square norm and 8-bit quantisation for MI355X
+// (gfx950): ngram_add_norm, ngram_add_norm_grad, ngram_quant_fp8 and the
+// layout helpers of the 8-bit matrices.  The formulas are in
+// include/ngram.h.  All of these are bound by HBM bandwidth.
+#include "common8.h"
+
+#include <algorithm>
+#include <cmath>
+
+namespace ng8 {
+
+int fail(int status, const char* fmt, ...) {
+    // ngram_last_error() returns the start of the calling thread's own
+    // 512-byte message buffer, a plain char array: writing it from here keeps
+    // one buffer for the whole library.
+    char* const buffer = const_cast<char*>(ngram_last_error());
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buffer, 512, fmt, ap);
+    va_end(ap);
+    return status;
+}
+
+int hip_status(const char* what) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(NGRAM_EHIP, "%s: %s", what, hipGetErrorString(e));
+    return NGRAM_OK;
+}
+
+int check_fp8(const ngram_fp8* q, const char* what) {
+    if (!q) return fail(NGRAM_EINVAL, "%s is NULL", what);
+    if (q->rows < 0 || q->cols < 0) return fail(NGRAM_EINVAL, "%s has a negative size", what);
+    if (q->rows > NGRAM_FP8_MAX || q->cols > NGRAM_FP8_MAX)
+        return fail(NGRAM_ERANGE, "%s: rows=%lld or cols=%lld above %lld", what, (long long)q->rows, (long long)q->cols,
+                    (long long)NGRAM_FP8_MAX);
+    if (q->block_rows != 1 && q->block_rows != kBlock)
+        return fail(NGRAM_EINVAL, "%s: block_rows=%d must be 1 or %d", what, q->block_rows, kBlock);
+    if (q->rows > 0 && q->cols > 0) {
+        if (!q->codes || !q->scales) return fail(NGRAM_EINVAL, "%s: codes or scales is NULL", what);
+        if (!aligned(q->codes, 16) || !aligned(q->scales, 4))
+            return fail(NGRAM_EALIGN, "%s: codes must be 16-byte and scales 4-byte aligned", what);
+    }
+    return NGRAM_OK;
+}
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Residual addition and norm.
+//
+// A row of d columns is cut in chunks of 512: lane l of a wavefront holds
+// columns 512 c + 8 l .. +7 of its chunks, so every load and store of a
+// chunk is one 16-byte (bf16) or 8-byte (codes) access per lane over
+// consecutive addresses, and a scale block of 128 columns is one group of 16
+// lanes.  A wavefront keeps C chunks of gamma in registers and walks over
+// rows; with WIDE, the wavefronts of a workgroup share each row (wavefront w
+// has chunks w C .. w C + C - 1) and join the sums of squares in LDS.
+struct NormArgs {
+    const void* x;
+    const uint16_t* residual;
+    const float* gamma;
+    uint16_t* sum_out;
+    uint16_t* y_out;
+    uint8_t* codes;
+    uint8_t* scales;
+    float* r_out;
+    int64_t n;
+    int32_t d;
+    int32_t ld;         // code columns
+    int32_t sld;        // scale bytes per row
+    float eps;
+    float inv_d;
+};
+
+constexpr int kMaxWaves = 16;
+
+template <int C, bool F32, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_kernel(const NormArgs a) {
+    __shared__ float part[2][kMaxWaves];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6;
+    const int c0 = WIDE ? wave * C : 0;
+    int64_t row = WIDE ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * waves + wave;
+    const int64_t stride = WIDE ? gridDim.x : static_cast<int64_t>(gridDim.x) * waves;
+    float gam[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = (c0 + c) * kSlice + lane * kVec;
+        Raw8<true> g;
+        if (col < a.d) g.load(a.gamma, col); else g.zero();
+        g.get(gam[c]);
+    }
+    for (int it = 0; row < a.n; row += stride, ++it) {
+        Raw8<F32> x[C];
+        Raw8<false> res[C];
+        const int64_t at = row * a.d;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = (c0 + c) * kSlice + lane * kVec;
+            if (col < a.d) {
+                x[c].load(a.x, at + col);
+                if (a.residual) res[c].load(a.residual, at + col); else res[c].zero();
+            } else {
+                x[c].zero();
+                res[c].zero();
+            }
+        }
+        float s[C][8];
+        float total = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = (c0 + c) * kSlice + lane * kVec;
+            float u[8], v[8];
+            x[c].get(u);
+            res[c].get(v);
+            u32x4 packed;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) packed[k] = bf16_pair(u[2 * k] + v[2 * k], u[2 * k + 1] + v[2 * k + 1]);
+            // the norm reads the rounded sum, so that the backward, which has
+            // only the stored sum, differentiates what was computed
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                s[c][2 * k] = bf16_lo(packed[k]);
+                s[c][2 * k + 1] = bf16_hi(packed[k]);
+            }
+            if (a.sum_out && col < a.d) *reinterpret_cast<u32x4*>(a.sum_out + at + col) = packed;
+            float t = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t = fmaf(s[c][k], s[c][k], t);
+            total += t;
+        }
+        total = wave_sum(total);
+        if (WIDE) {
+            // two buffers in turn: a wavefront writes one while a slower one
+            // still reads the other, so one barrier a row is enough
+            float* const p = part[it & 1];
+            if (lane == 0) p[wave] = total;
+            __syncthreads();
+            total = 0.0f;
+            for (int w = 0; w < waves; ++w) total += p[w];
+        }
+        const float r = 1.0f / sqrtf(total * a.inv_d + a.eps);
+        if (a.r_out && lane == 0 && wave == (WIDE ? 0 : wave)) a.r_out[row] = r;
+        uint32_t bytes = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = (c0 + c) * kSlice + lane * kVec;
+            float y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = s[c][k] * r * gam[c][k];
+            if (a.y_out && col < a.d) {
+                u32x4 packed;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) packed[k] = bf16_pair(y[2 * k], y[2 * k + 1]);
+                *reinterpret_cast<u32x4*>(a.y_out + at + col) = packed;
+            }
+            if (a.codes) {
+                if (col >= a.d) {       // past the row: zero codes, also where r is not finite
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = 0.0f;
+                }
+                const uint32_t byte = block_scale16(y);
+                const float inv = inverse_scale(byte);
+                if (col < a.ld) {
+                    u32x2 q;
+                    q[0] = codes4(y[0], y[1], y[2], y[3], inv);
+                    q[1] = codes4(y[4], y[5], y[6], y[7], inv);
+                    *reinterpret_cast<u32x2*>(a.codes + row * a.ld + col) = q;
+                }
+                const uint32_t b0 = __builtin_amdgcn_readlane(byte, 0), b1 = __builtin_amdgcn_readlane(byte, 16);
+                const uint32_t b2 = __builtin_amdgcn_readlane(byte, 32), b3 = __builtin_amdgcn_readlane(byte, 48);
+                const uint32_t word = b0 | b1 << 8 | b2 << 16 | b3 << 24;
+                bytes = lane == c ? word : bytes;
+            }
+        }
+        // chunk c's four scale bytes sit in lane c
+        if (a.codes && lane < C && (c0 + lane) * 4 < a.sld)
+            *reinterpret_cast<uint32_t*>(a.scales + row * a.sld + (c0 + lane) * 4) = bytes;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients of the norm: with h = gamma dy,
+//   dx = r h - s (r^3 / d) sum(h s) + dsum,   dgamma = sum over rows of dy s r.
+// The same walk over rows; a wavefront adds its rows' dgamma terms in
+// registers, a workgroup its wavefronts' in LDS, and one row of partial sums
+// per workgroup goes to the workspace for the kernel below.
+struct NormGradArgs {
+    const void* dy;
+    const uint16_t* sum;
+    const float* r;
+    const float* gamma;
+    const uint16_t* dsum;
+    uint16_t* dx;
+    float* partial;     // [workgroups][d]
+    int64_t n;
+    int32_t d;
+    float inv_d;
+};
+
+template <int C, bool F32, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_grad_kernel(const NormGradArgs a) {
+    __shared__ float part[2][kMaxWaves];
+    extern __shared__ __attribute__((aligned(16))) float sums[];      // not WIDE: [waves][C * 512]
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6;
+    const int c0 = WIDE ? wave * C : 0;
+    int64_t row = WIDE ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * waves + wave;
+    const int64_t stride = WIDE ? gridDim.x : static_cast<int64_t>(gridDim.x) * waves;
+    float gam[C][8], acc[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = (c0 + c) * kSlice + lane * kVec;
+        Raw8<true> g;
+        if (col < a.d) g.load(a.gamma, col); else g.zero();
+        g.get(gam[c]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[c][k] = 0.0f;
+    }
+    for (int it = 0; row < a.n; row += stride, ++it) {
+        Raw8<F32> dy[C];
+        Raw8<false> s[C], ds[C];
+        const int64_t at = row * a.d;
+        const float r = a.r[row];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = (c0 + c) * kSlice + lane * kVec;
+            if (col < a.d) {
+                dy[c].load(a.dy, at + col);
+                s[c].load(a.sum, at + col);
+                if (a.dsum) ds[c].load(a.dsum, at + col); else ds[c].zero();
+            } else {
+                dy[c].zero();
+                s[c].zero();
+                ds[c].zero();
+            }
+        }
+        float dot = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            float u[8], v[8];
+            dy[c].get(u);
+            s[c].get(v);
+            float t = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                t = fmaf(u[k] * gam[c][k], v[k], t);
+                acc[c][k] = fmaf(u[k], v[k] * r, acc[c][k]);
+            }
+            dot += t;
+        }
+        dot = wave_sum(dot);
+        if (WIDE) {
+            float* const p = part[it & 1];
+            if (lane == 0) p[wave] = dot;
+            __syncthreads();
+            dot = 0.0f;
+            for (int w = 0; w < waves; ++w) dot += p[w];
+        }
+        const float f = dot * r * r * r * a.inv_d;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = (c0 + c) * kSlice + lane * kVec;
+            float u[8], v[8], w[8];
+            dy[c].get(u);
+            s[c].get(v);
+            ds[c].get(w);
+            u32x4 packed;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float o[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int j = 2 * k + q;
+                    o[q] = (u[j] * gam[c][j] * r - v[j] * f) + w[j];
+                }
+                packed[k] = bf16_pair(o[0], o[1]);
+            }
+            if (col < a.d) *reinterpret_cast<u32x4*>(a.dx + at + col) = packed;
+        }
+    }
+    float* const out = a.partial + static_cast<int64_t>(blockIdx.x) * a.d;
+    if (WIDE) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int col = (c0 + c) * kSlice + lane * kVec;
+            if (col < a.d) {
+                *reinterpret_cast<f32x4*>(out + col) = f32x4{acc[c][0], acc[c][1], acc[c][2], acc[c][3]};
+                *reinterpret_cast<f32x4*>(out + col + 4) = f32x4{acc[c][4], acc[c][5], acc[c][6], acc[c][7]};
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        float* const p = sums + wave * (C * kSlice) + c * kSlice + lane * kVec;
+        *reinterpret_cast<f32x4*>(p) = f32x4{acc[c][0], acc[c][1], acc[c][2], acc[c][3]};
+        *reinterpret_cast<f32x4*>(p + 4) = f32x4{acc[c][4], acc[c][5], acc[c][6], acc[c][7]};
+    }
+    __syncthreads();
+    for (int col = threadIdx.x; col < a.d; col += blockDim.x) {
+        float t = 0.0f;
+        for (int w = 0; w < waves; ++w) t += sums[w * (C * kSlice) + col];
+        out[col] = t;
+    }
+}
+
+// dgamma[col] = the sum of `rows` rows of partial sums: 64 columns per
+// workgroup, 16 wavefronts that take every 16th row, joined in LDS.
+__global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ partial, int rows, int d,
+                                                          float* __restrict__ out) {
+    __shared__ float part[16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int col = blockIdx.x * 64 + lane;
+    float t = 0.0f;
+    if (col < d) {
+#pragma unroll 8
+        for (int r = wave; r < rows; r += 16) t += partial[static_cast<int64_t>(r) * d + col];
+    }
+    part[wave][lane] = t;
+    __syncthreads();
+    if (wave == 0 && col < d) {
+        t = 0.0f;
+        for (int w = 0; w < 16; ++w) t += part[w][lane];
+        out[col] = t;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Quantisation of a matrix x[n][d]: codes and scales of its rows (a scale per
+// 128 columns), of its transpose (a scale per 128 rows of x), or both from
+// one read; with TILE one scale serves a 128 x 128 tile and both layouts.
+//
+// A workgroup owns a 128 x 128 tile.  Thread t holds the 8 x 8 patch of rows
+// 8 (t >> 4) .. +7 and columns 8 (t & 15) .. +7: a row's 128 columns are a
+// group of 16 lanes (row scales by lane moves), and the patch transposes in
+// registers.  Column maxima go through LDS; so do the transposed codes, which
+// then leave as whole 128-byte lines.
+struct QuantArgs {
+    const void* x;
+    uint8_t *q, *qs, *qt, *qts;
+    int64_t n;
+    int32_t d;
+    int64_t q_ld, q_sld, qt_ld, qt_sld;
+    int32_t tiles_d;
+    int32_t tile_scale;
+};
+
+template <bool F32>
+__global__ void __launch_bounds__(256) quant_kernel(const QuantArgs a) {
+    __shared__ uint32_t cmax[4][128];
+    __shared__ __attribute__((aligned(16))) uint8_t codes[128 * 144];   // [column][128 rows + 16]: 16-byte rows that start on shifting banks
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int tr = t >> 4, tc = t & 15;
+    const int64_t tile_r = blockIdx.x / a.tiles_d;
+    const int tile_c = blockIdx.x - tile_r * a.tiles_d;
+    const int64_t r0 = tile_r * 128 + 8 * tr;
+    const int c0 = tile_c * 128 + 8 * tc;
+    float x[8][8];
+    {
+        Raw8<F32> raw[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (r0 + i < a.n && c0 < a.d) raw[i].load(a.x, (r0 + i) * a.d + c0); else raw[i].zero();
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) raw[i].get(x[i]);
+    }
+    uint32_t tile_byte = 0;
+    if (a.tile_scale) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, finite_amax_bits(x[i]));
+        m = max16(m);
+        m = max(max(__builtin_amdgcn_readlane(m, 0), __builtin_amdgcn_readlane(m, 16)),
+                max(__builtin_amdgcn_readlane(m, 32), __builtin_amdgcn_readlane(m, 48)));
+        if (lane == 0) cmax[wave][0] = m;
+        __syncthreads();
+        tile_byte = scale_byte(max(max(cmax[0][0], cmax[1][0]), max(cmax[2][0], cmax[3][0])));
+    }
+    if (a.q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t byte = a.tile_scale ? tile_byte : block_scale16(x[i]);
+            const float inv = inverse_scale(byte);
+            if (r0 + i < a.n) {
+                u32x2 c;
+                c[0] = codes4(x[i][0], x[i][1], x[i][2], x[i][3], inv);
+                c[1] = codes4(x[i][4], x[i][5], x[i][6], x[i][7], inv);
+                *reinterpret_cast<u32x2*>(a.q + (r0 + i) * a.q_ld + c0) = c;
+                if (!a.tile_scale && tc == 0) a.qs[(r0 + i) * a.q_sld + tile_c] = static_cast<uint8_t>(byte);
+                if (!a.tile_scale && tile_c == a.tiles_d - 1 && tc > 0 && tile_c + tc < a.q_sld)
+                    a.qs[(r0 + i) * a.q_sld + tile_c + tc] = kUnitScale;
+            }
+        }
+        if (a.tile_scale && t == 0) a.qs[tile_r * a.q_sld + tile_c] = static_cast<uint8_t>(tile_byte);
+        if (a.tile_scale && tile_c == a.tiles_d - 1 && t > 0 && tile_c + t < a.q_sld)
+            a.qs[tile_r * a.q_sld + tile_c + t] = kUnitScale;
+    }
+    if (!a.qt) return;
+    uint32_t byte[8];
+    if (a.tile_scale) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) byte[k] = tile_byte;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t u = __float_as_uint(x[i][k]) & 0x7FFFFFFFu;
+                m = max(m, u < kInfBits ? u : 0u);
+            }
+            m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
+            m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
+            if (lane < 16) cmax[wave][8 * tc + k] = m;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int c = 8 * tc + k;
+            byte[k] = scale_byte(max(max(cmax[0][c], cmax[1][c]), max(cmax[2][c], cmax[3][c])));
+        }
+    }
+    const int64_t last_r = (a.n - 1) / 128;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float inv = inverse_scale(byte[k]);
+        u32x2 c;
+        c[0] = codes4(x[0][k], x[1][k], x[2][k], x[3][k], inv);
+        c[1] = codes4(x[4][k], x[5][k], x[6][k], x[7][k], inv);
+        *reinterpret_cast<u32x2*>(codes + (8 * tc + k) * 144 + 8 * tr) = c;
+        if (c0 + k < a.d && !a.tile_scale) {
+            if (tr == 0) a.qts[static_cast<int64_t>(c0 + k) * a.qt_sld + tile_r] = static_cast<uint8_t>(byte[k]);
+            if (tile_r == last_r && tr > 0 && tile_r + tr < a.qt_sld)
+                a.qts[static_cast<int64_t>(c0 + k) * a.qt_sld + tile_r + tr] = kUnitScale;
+        }
+    }
+    if (a.tile_scale) {
+        if (t == 0) a.qts[tile_c * a.qt_sld + tile_r] = static_cast<uint8_t>(tile_byte);
+        if (tile_r == last_r && t > 0 && tile_r + t < a.qt_sld) a.qts[tile_c * a.qt_sld + tile_r + t] = kUnitScale;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = 32 * i + (t >> 3), part = t & 7;      // a column's 128 bytes by eight lanes
+        const int64_t col = static_cast<int64_t>(tile_c) * 128 + c;
+        if (col < a.d)
+            *reinterpret_cast<u32x4*>(a.qt + col * a.qt_ld + tile_r * 128 + 16 * part) =
+                *reinterpret_cast<const u32x4*>(codes + c * 144 + 16 * part);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launch shapes.
+
+// Chunks per wavefront and wavefronts per row.  Many rows: a wavefront takes
+// a whole row of up to 5 chunks (gamma and the row stay in registers), wider
+// rows are shared.  Few rows: one chunk per wavefront, so that a row's loads
+// are all in flight at once on as many wavefronts as there are chunks.
+struct RowShape {
+    int chunks;     // per wavefront
+    int waves;      // per workgroup
+    bool wide;
+    int64_t grid;
+};
+
+RowShape row_shape(int64_t n, int d, int64_t max_grid, int wide_chunks) {
+    const int total = (d + kSlice - 1) / kSlice;
+    RowShape s;
+    if (n >= 2048 && total <= 5) {
+        s.chunks = total;
+        s.waves = 4;
+        s.wide = false;
+        s.grid = std::min<int64_t>((n + 3) / 4, max_grid);
+    } else {
+        const int want = n >= 2048 ? wide_chunks : 1;
+        s.waves = std::min(kMaxWaves, (total + want - 1) / want);
+        s.chunks = (total + s.waves - 1) / s.waves;
+        s.waves = (total + s.chunks - 1) / s.chunks;
+        s.wide = true;
+        s.grid = std::min<int64_t>(n, max_grid);
+    }
+    return s;
+}
+
+template <bool F32, bool WIDE>
+void launch_norm(int chunks, dim3 grid, dim3 block, hipStream_t st, const NormArgs& a) {
+#define NG8_CASE(C) case C: hipLaunchKernelGGL((add_norm_kernel<C, F32, WIDE>), grid, block, 0, st, a); break
+    switch (chunks) { NG8_CASE(1); NG8_CASE(2); NG8_CASE(3); NG8_CASE(4); NG8_CASE(5); default:
+        if constexpr (WIDE) switch (chunks) { NG8_CASE(6); NG8_CASE(7); default: NG8_CASE(8); } }
+#undef NG8_CASE
+}
+
+template <bool F32, bool WIDE>
+void launch_norm_grad(int chunks, dim3 grid, dim3 block, size_t lds, hipStream_t st, const NormGradArgs& a) {
+#define NG8_CASE(C) case C: hipLaunchKernelGGL((add_norm_grad_kernel<C, F32, WIDE>), grid, block, lds, st, a); break
+    switch (chunks) { NG8_CASE(1); NG8_CASE(2); NG8_CASE(3); NG8_CASE(4); NG8_CASE(5); default:
+        if constexpr (WIDE) switch (chunks) { NG8_CASE(6); NG8_CASE(7); default: NG8_CASE(8); } }
+#undef NG8_CASE
+}
+
+constexpr int64_t kNormGrid = 2048;         // 256 compute units x 8 workgroups of 4 wavefronts
+constexpr int64_t kNormGradGrid = 512;      // rows of partial sums
+
+int check_rows(int64_t n, int32_t d) {
+    if (n < 0) return fail(NGRAM_EINVAL, "n=%lld is negative", (long long)n);
+    if (d <= 0 || d % kVec != 0) return fail(NGRAM_EINVAL, "d=%d must be a positive multiple of %d", d, kVec);
+    if (d > NGRAM_MAX_D) return fail(NGRAM_ERANGE, "d=%d above %d", d, NGRAM_MAX_D);
+    if (n > NGRAM_FP8_MAX) return fail(NGRAM_ERANGE, "n=%lld above %lld", (long long)n, (long long)NGRAM_FP8_MAX);
+    return NGRAM_OK;
+}
+
+int check_value(int dtype, const char* what) {
+    if (dtype != NGRAM_F32 && dtype != NGRAM_BF16) return fail(NGRAM_EINVAL, "%s=%d is not an ngram_value", what, dtype);
+    return NGRAM_OK;
+}
+
+int64_t norm_grad_grid(int64_t n, int d) { return std::max<int64_t>(1, row_shape(n, d, kNormGradGrid, 2).grid); }
+
+}  // namespace
+}  // namespace ng8
+
+using namespace ng8;
+
+extern "C" {
+
+int64_t ngram_fp8_code_bytes(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols < 0 || rows > NGRAM_FP8_MAX || cols > NGRAM_FP8_MAX) return -1;
+    return rows * code_ld(cols);
+}
+
+int64_t ngram_fp8_scale_bytes(int64_t rows, int64_t cols, int32_t block_rows) {
+    if (rows < 0 || cols < 0 || rows > NGRAM_FP8_MAX || cols > NGRAM_FP8_MAX) return -1;
+    if (block_rows != 1 && block_rows != kBlock) return -1;
+    return (block_rows == 1 ? rows : blocks_of(rows)) * scale_ld(cols);
+}
+
+int ngram_add_norm(const void* x, int32_t x_dtype, const uint16_t* residual, int64_t n, int32_t d, const float* gamma,
+                   float eps, uint16_t* sum_out, uint16_t* y_out, const ngram_fp8* q_out, float* r_out,
+                   ngram_stream_t stream) {
+    fail(NGRAM_OK, "%s", "");
+    int rc = check_rows(n, d);
+    if (rc) return rc;
+    if ((rc = check_value(x_dtype, "x_dtype"))) return rc;
+    if (!(eps >= 0.0f) || std::isinf(eps)) return fail(NGRAM_EINVAL, "eps must be finite and not negative");
+    if (q_out) {
+        if ((rc = check_fp8(q_out, "q_out"))) return rc;
+        if (q_out->rows != n || q_out->cols != d || q_out->block_rows != 1)
+            return fail(NGRAM_EINVAL, "q_out must be %lld x %d with block_rows 1", (long long)n, d);
+    }
+    if (!gamma) return fail(NGRAM_EINVAL, "gamma is NULL");
+    if (n == 0) return NGRAM_OK;
+    if (!x) return fail(NGRAM_EINVAL, "x is NULL");
+    if (!sum_out && !y_out && !q_out && !r_out) return fail(NGRAM_EINVAL, "no output is asked for");
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(gamma, 16) || !aligned(sum_out, 16) || !aligned(y_out, 16))
+        return fail(NGRAM_EALIGN, "x, residual, gamma, sum_out and y_out must be 16-byte aligned");
+    if (!aligned(r_out, 4)) return fail(NGRAM_EALIGN, "r_out must be 4-byte aligned");
+    NormArgs a;
+    a.x = x; a.residual = residual; a.gamma = gamma; a.sum_out = sum_out; a.y_out = y_out;
+    a.codes = q_out ? q_out->codes : nullptr;
+    a.scales = q_out ? q_out->scales : nullptr;
+    a.r_out = r_out; a.n = n; a.d = d;
+    a.ld = static_cast<int32_t>(code_ld(d));
+    a.sld = static_cast<int32_t>(scale_ld(d));
+    a.eps = eps;
+    a.inv_d = 1.0f / static_cast<float>(d);
+    const RowShape s = row_shape(n, d, kNormGrid, 4);
+    const dim3 grid(static_cast<unsigned>(s.grid)), block(64 * s.waves);
+    if (x_dtype == NGRAM_F32) {
+        if (s.wide) launch_norm<true, true>(s.chunks, grid, block, stream, a);
+        else launch_norm<true, false>(s.chunks, grid, block, stream, a);
+    } else {
+        if (s.wide) launch_norm<false, true>(s.chunks, grid, block, stream, a);
+        else launch_norm<false, false>(s.chunks, grid, block, stream, a);
+    }
+    return hip_status("ngram_add_norm launch");
+}
+
+int64_t ngram_add_norm_grad_workspace_bytes(int64_t n, int32_t d) {
+    if (n < 0 || n > NGRAM_FP8_MAX || d <= 0 || d % kVec != 0 || d > NGRAM_MAX_D) return -1;
+    return norm_grad_grid(n, d) * d * 4;
+}
+
+int ngram_add_norm_grad(const void* dy, int32_t dy_dtype, const uint16_t* sum, const float* r, const float* gamma,
+                        const uint16_t* dsum, int64_t n, int32_t d, uint16_t* dx_out, float* dgamma_out,
+                        void* workspace, int64_t workspace_bytes, ngram_stream_t stream) {
+    fail(NGRAM_OK, "%s", "");
+    int rc = check_rows(n, d);
+    if (rc) return rc;
+    if ((rc = check_value(dy_dtype, "dy_dtype"))) return rc;
+    if (!gamma || !dgamma_out) return fail(NGRAM_EINVAL, "gamma or dgamma_out is NULL");
+    if (n > 0 && (!dy || !sum || !r || !dx_out)) return fail(NGRAM_EINVAL, "dy, sum, r or dx_out is NULL");
+    if (!aligned(dy, 16) || !aligned(sum, 16) || !aligned(gamma, 16) || !aligned(dsum, 16) || !aligned(dx_out, 16) ||
+        !aligned(dgamma_out, 4) || !aligned(r, 4))
+        return fail(NGRAM_EALIGN, "dy, sum, gamma, dsum and dx_out must be 16-byte aligned, r and dgamma_out 4-byte");
+    const int64_t need = ngram_add_norm_grad_workspace_bytes(n, d);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+        return fail(NGRAM_EINVAL, "workspace must hold %lld bytes, 16-byte aligned", (long long)need);
+    NormGradArgs a;
+    a.dy = dy; a.sum = sum; a.r = r; a.gamma = gamma; a.dsum = dsum; a.dx = dx_out;
+    a.partial = static_cast<float*>(workspace);
+    a.n = n; a.d = d;
+    a.inv_d = 1.0f / static_cast<float>(d);
+    RowShape s = row_shape(n, d, kNormGradGrid, 2);
+    s.grid = norm_grad_grid(n, d);      // no rows: one workgroup writes a row of zeros
+    const dim3 grid(static_cast<unsigned>(s.grid)), block(64 * s.waves);
+    const size_t lds = s.wide ? 0 : static_cast<size_t>(s.waves) * s.chunks * kSlice * 4;
+    if (dy_dtype == NGRAM_F32) {
+        if (s.wide) launch_norm_grad<true, true>(s.chunks, grid, block, lds, stream, a);
+        else launch_norm_grad<true, false>(s.chunks, grid, block, lds, stream, a);
+    } else {
+        if (s.wide) launch_norm_grad<false, true>(s.chunks, grid, block, lds, stream, a);
+        else launch_norm_grad<false, false>(s.chunks, grid, block, lds, stream, a);
+    }
+    hipLaunchKernelGGL(column_sum_kernel, dim3((d + 63) / 64), dim3(1024), 0, stream, a.partial,
+                       static_cast<int>(s.grid), d, dgamma_out);
+    return hip_status("ngram_add_norm_grad launch");
+}
+
+int ngram_quant_fp8(const void* x, int32_t x_dtype, int64_t n, int32_t d, const ngram_fp8* q, const ngram_fp8* qt,
+                    ngram_stream_t stream) {
+    fail(NGRAM_OK, "%s", "");
+    int rc = check_rows(n, d);
+    if (rc) return rc;
+    if ((rc = check_value(x_dtype, "x_dtype"))) return rc;
+    if (!q && !qt) return fail(NGRAM_EINVAL, "q and qt are both NULL");
+    if (q) {
+        if ((rc = check_fp8(q, "q"))) return rc;
+        if (q->rows != n || q->cols != d) return fail(NGRAM_EINVAL, "q must be %lld x %d", (long long)n, d);
+    }
+    if (qt) {
+        if ((rc = check_fp8(qt, "qt"))) return rc;
+        if (qt->rows != d || qt->cols != n) return fail(NGRAM_EINVAL, "qt must be %d x %lld", d, (long long)n);
+    }
+    if (q && qt && q->block_rows != qt->block_rows)
+        return fail(NGRAM_EINVAL, "q and qt must have the same block_rows");
+    if (n == 0) return NGRAM_OK;
+    if (!x) return fail(NGRAM_EINVAL, "x is NULL");
+    if (!aligned(x, 16)) return fail(NGRAM_EALIGN, "x must be 16-byte aligned");
+    QuantArgs a;
+    a.x = x;
+    a.q = q ? q->codes : nullptr;
+    a.qs = q ? q->scales : nullptr;
+    a.qt = qt ? qt->codes : nullptr;
+    a.qts = qt ? qt->scales : nullptr;
+    a.n = n; a.d = d;
+    a.q_ld = code_ld(d); a.q_sld = scale_ld(d);
+    a.qt_ld = code_ld(n); a.qt_sld = scale_ld(n);
+    a.tiles_d = static_cast<int32_t>(blocks_of(d));
+    a.tile_scale = (q ? q : qt)->block_rows == kBlock;
+    const int64_t tiles = blocks_of(n) * a.tiles_d;
+    if (tiles > INT32_MAX) return fail(NGRAM_ERANGE, "n=%lld too large for one launch", (long long)n);
+    if (x_dtype == NGRAM_F32)
+        hipLaunchKernelGGL((quant_kernel<true>), dim3(static_cast<unsigned>(tiles)), dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((quant_kernel<false>), dim3(static_cast<unsigned>(tiles)), dim3(256), 0, stream, a);
+    return hip_status("ngram_quant_fp8 launch");
+}
+
+}  // extern "C"

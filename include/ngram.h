@@ -396,6 +396,161 @@ int64_t ngram_grad_gate_noalloc_max_elements(void);
 int ngram_grad_gate_noalloc(const int32_t* rows, const uint16_t* dout, const float* eN, int64_t n, int32_t d,
                             float* grad_Wg_out, ngram_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Training and serving the projected layer in 8 bits: the norm behind the
+ * residual stream with an 8-bit output, the product that reads it, their
+ * gradients, and the optimiser step that applies the table's and the dense
+ * gradients.  The pages name none of these in a form to follow; the formulas
+ * are fixed here.
+ *
+ * 8-bit matrices.  Elements are OCP E4M3 codes (largest finite value 448)
+ * with one E8M0 scale (a power of two, byte e + 127 for 2^e) for each block of
+ * 128 consecutive columns of a row (block_rows = 1), or of 128 rows
+ * (block_rows = 128).  Value = code * 2^e.  e is the smallest exponent >= -126 for which no
+ * finite value of the block exceeds 448 * 2^e, and 0 for a block without a
+ * finite nonzero value; codes round to nearest, ties to even; infinities and
+ * NaN become the NaN code.  Power-of-two scales cost at most one bit of E4M3's
+ * range, nothing of its precision, and the matrix cores apply them.
+ *   codes  [rows][128 ceil(cols / 128)] bytes, zero from cols on, 16-byte aligned;
+ *   scales [rows, or ceil(rows / 128)][4 ceil(ceil(cols / 128) / 4)] bytes,
+ *     127 from block ceil(cols / 128) on, 4-byte aligned.
+ * rows, cols <= NGRAM_FP8_MAX.  The *_bytes calls give the sizes (-1 for sizes
+ * out of range). */
+#define NGRAM_FP8_BLOCK 128
+#define NGRAM_FP8_MAX 1073741824       /* 2^30 */
+
+typedef enum { NGRAM_F32 = 0, NGRAM_BF16 = 1 } ngram_value;
+
+typedef struct {
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t rows;
+    int64_t cols;
+    int32_t block_rows;    /* 1 or 128 */
+    int32_t reserved;
+} ngram_fp8;
+
+int64_t ngram_fp8_code_bytes(int64_t rows, int64_t cols);
+int64_t ngram_fp8_scale_bytes(int64_t rows, int64_t cols, int32_t block_rows);
+
+/* Quantise x[n][d] (fp32 or bf16, device, 16-byte aligned; d a multiple of 8)
+ * to q (n x d), to qt (d x n, its transpose), or to both from one read of x;
+ * either may be NULL.  block_rows = 1: a scale per 128 columns of x for q and
+ * per 128 rows of x for qt (a product that sums over the rows needs its
+ * blocks along them); block_rows = 128: one scale per 128 x 128 tile, the
+ * same in both.  Errors: EINVAL, EALIGN, ERANGE. */
+int ngram_quant_fp8(const void* x, int32_t x_dtype, int64_t n, int32_t d, const ngram_fp8* q, const ngram_fp8* qt,
+                    ngram_stream_t stream);
+
+/* Residual addition, root-mean-square norm and quantisation in one pass.  Per row:
+ *   s[j] = bf16(residual[j] + x[j])                  (the new residual stream)
+ *   r    = 1 / sqrt(sum over j of s[j]^2 / d + eps)
+ *   y[j] = s[j] r gamma[j]
+ * s is rounded before the norm, so that the stored sum is what was normed.
+ * All in fp32; the sum's order is fixed.  x[n][d] fp32 or bf16,
+ * residual[n][d] bf16 or NULL (s = bf16(x)), gamma[d] fp32.  Outputs, each
+ * NULL if not wanted, one at least: sum_out[n][d] bf16 (may equal residual,
+ * or a bf16 x), y_out[n][d] bf16 (y rounded to nearest, ties to even),
+ * q_out (n x d, block_rows 1, quantised from the fp32 y), r_out[n] fp32.
+ * d a multiple of 8; device pointers, 16-byte aligned (r_out 4).  eps finite,
+ * >= 0.  n = 0 launches nothing. */
+int ngram_add_norm(const void* x, int32_t x_dtype, const uint16_t* residual, int64_t n, int32_t d, const float* gamma,
+                   float eps, uint16_t* sum_out, uint16_t* y_out, const ngram_fp8* q_out, float* r_out,
+                   ngram_stream_t stream);
+
+/* Gradients of the norm, the roundings passed straight through.  From
+ * dy = dL/dy[n][d] (fp32 or bf16), the forward's sum s and r, and optionally
+ * dsum[n][d] bf16 (the gradient that reaches s along the residual stream):
+ *   dx[j]     = r gamma[j] dy[j] - s[j] (r^3 / d) sum over k of gamma[k] dy[k] s[k] + dsum[j]
+ *   dgamma[j] = sum over rows of dy[j] s[j] r
+ * dx_out[n][d] bf16 is the gradient of both x and residual (and may equal
+ * dsum, or a bf16 dy); dgamma_out[d] fp32 sums in a fixed order with no
+ * atomics.  n = 0 gives dgamma 0.  workspace: device, 16-byte aligned,
+ * ngram_add_norm_grad_workspace_bytes(n, d) bytes. */
+int64_t ngram_add_norm_grad_workspace_bytes(int64_t n, int32_t d);
+int ngram_add_norm_grad(const void* dy, int32_t dy_dtype, const uint16_t* sum, const float* r, const float* gamma,
+                        const uint16_t* dsum, int64_t n, int32_t d, uint16_t* dx_out, float* dgamma_out,
+                        void* workspace, int64_t workspace_bytes, ngram_stream_t stream);
+
+/* Product of 8-bit matrices: C[i][o] = sum over j of A[i][j] B[o][j] (values,
+ * scales included), fp32 accumulation in an order that is fixed for given
+ * sizes.  A is m x k, B is n x k (n a multiple of 8), C[m][n] fp32 or bf16
+ * (rounded once), 16-byte aligned.  Either operand may have block_rows 1 or
+ * 128.  The layer y = P x is A = x, B = P (n x k = d_out x d_in); its
+ * gradients are dx: A = dy, B = P transposed (ngram_quant_fp8's qt, its tile
+ * scales the same), and dP: A = dy transposed, B = x transposed, both with
+ * their blocks along the tokens.  k <= 2^23.  A NaN code gives NaN in its row or column
+ * of C.  workspace: device, 16-byte aligned,
+ * ngram_project_fp8_workspace_bytes(m, n, k) bytes (0 for many sizes: then it
+ * may be NULL).  Errors: EINVAL, EALIGN, ERANGE; m = 0 launches nothing. */
+int64_t ngram_project_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c_dtype, void* workspace,
+                      int64_t workspace_bytes, ngram_stream_t stream);
+
+/* AdamW with decoupled weight decay.  Per element, in fp32, from the gradient
+ * g (times grad_scale):
+ *   m' = beta1 m + (1 - beta1) g,    v' = beta2 v + (1 - beta2) g^2
+ *   p' = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m' / (sqrt(v') / sqrt(1 - beta2^step) + eps)
+ * p fp32 or bf16, g fp32 or bf16, moments in fp32 (NGRAM_STATE_F32) or in 8
+ * bits (NGRAM_STATE_FP8): m and sqrt(v) as E4M3 codes with an E8M0 scale per
+ * 128 consecutive elements of the tensor (of the row, in a table).
+ * In few bits rounding to nearest would lose the step: beta2 = 0.999 moves
+ * sqrt(v) by 0.05% where E4M3's neighbours lie 6 to 12% apart, and an
+ * update of a bf16 parameter is often below half its last place.  So 8-bit moments and bf16
+ * parameters round up or down at random, with the probabilities that make the
+ * expected value exact, and a positive sqrt(v) never becomes zero.  The
+ * random bits of element i are half (even i: low) of
+ * splitmix64(key + (rng_offset + i) / 2), key = splitmix64(splitmix64(seed) +
+ * step): m takes bits 0..19, sqrt(v) bits 12..31, p bits 8..23.  Equal inputs
+ * give equal bits.
+ *
+ * One tensor: numel elements; p, g, fp32 moments 16-byte aligned, codes
+ * 8-byte; m_scale, v_scale: ceil(numel / 128) bytes (NULL for fp32 moments).
+ * rng_offset: a multiple of 8; give each tensor a range of its own. */
+typedef enum { NGRAM_STATE_F32 = 0, NGRAM_STATE_FP8 = 1 } ngram_state;
+
+typedef struct {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    uint8_t* m_scale;
+    uint8_t* v_scale;
+    int64_t numel;
+    int64_t rng_offset;
+    int32_t p_dtype;       /* ngram_value */
+    int32_t g_dtype;       /* ngram_value */
+    int32_t state;         /* ngram_state */
+    int32_t reserved;
+} ngram_adamw_tensor;
+
+typedef struct {
+    double lr;
+    double beta1;
+    double beta2;
+    double eps;            /* > 0 */
+    double weight_decay;
+    double grad_scale;     /* 1 to take gradients as they are */
+    int64_t step;          /* from 1 */
+    uint64_t seed;
+} ngram_adamw_step;
+
+/* The step on tensors[0 .. count) (a HOST array, read before the call
+ * returns), in place; tensors must not overlap.  One launch for up to 48
+ * tensors of one combination of types.  Errors: EINVAL, EALIGN, ERANGE. */
+int ngram_adamw(const ngram_adamw_tensor* tensors, int32_t count, const ngram_adamw_step* step, ngram_stream_t stream);
+
+/* The step on the touched rows of a table, from a sparse gradient as
+ * ngram_grad_table and ngram_grad_e1 write it: table->p, m, v [R][d]
+ * (numel = R d, rng_offset 0), scales [R][ceil(d / 128)]; row rows[u] takes
+ * the gradient row table->g [max_rows][d], u < min(*n_rows, max_rows).  n_rows
+ * (device int64; NULL: max_rows) is read on the device, so the number of rows
+ * need not come back to the host.  Rows must be distinct; ids outside [0, R)
+ * are skipped.  Rows not listed keep their parameters and moments (their
+ * decay is not made up for later). */
+int ngram_adamw_rows(const ngram_adamw_tensor* table, int64_t R, int32_t d, const int32_t* rows, int64_t max_rows,
+                     const int64_t* n_rows, const ngram_adamw_step* step, ngram_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
