@@ -115,7 +115,7 @@ _SIGNATURES = {
                                       _P]),
     "ngram_add_norm_grad_workspace_bytes": (ctypes.c_int64, [_I64, _I32]),
     "ngram_add_norm_grad": (ctypes.c_int, [_P, _I32, _P, _P, _P, _P, _I64, _I32, _P, _P, _P, _I64, _P]),
-    "ngram_project_fp8_workspace_bytes": (ctypes.c_int64, [_I64, _I64, _I64]),
+    "ngram_project_fp8_workspace_bytes": (ctypes.c_int64, [_I64, _I64, _I64, _I32]),
     "ngram_project_fp8": (ctypes.c_int, [ctypes.POINTER(_Fp8), ctypes.POINTER(_Fp8), _P, _I32, _P, _I64, _P]),
     "ngram_adamw": (ctypes.c_int, [ctypes.POINTER(_AdamWTensor), _I32, ctypes.POINTER(_AdamWStep), _P]),
     "ngram_adamw_rows": (ctypes.c_int, [ctypes.POINTER(_AdamWTensor), _I64, _I32, _P, _I64, _P,
@@ -833,10 +833,10 @@ def ngram_add_norm_grad(dy, sum, r, gamma, dsum=None, dx_out=None, dgamma_out=No
     return dx_out, dgamma_out
 
 
-def project_fp8_workspace(m: int, n: int, k: int, device="cuda:0"):
-    """Workspace of ngram_project_fp8 for C [m][n] over k columns, or None
-    where the call needs none."""
-    nbytes = int(lib().ngram_project_fp8_workspace_bytes(int(m), int(n), int(k)))
+def project_fp8_workspace(m: int, n: int, k: int, dtype=torch.float32, device="cuda:0"):
+    """Workspace of ngram_project_fp8 for C [m][n] of ``dtype`` over k
+    columns, or None where the call needs none."""
+    nbytes = int(lib().ngram_project_fp8_workspace_bytes(int(m), int(n), int(k), F32 if dtype == torch.float32 else BF16))
     if nbytes < 0:
         raise NgramError(f"no 8-bit product has m={m}, n={n}, k={k}")
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
@@ -850,7 +850,7 @@ def ngram_project_fp8(a: Fp8, b: Fp8, out=None, dtype=torch.bfloat16, workspace=
     _dev(out, _VALUES, "out")
     _need(out, a.rows * b.rows, "out")
     if workspace is None:
-        workspace = project_fp8_workspace(a.rows, b.rows, a.cols, a.codes.device)
+        workspace = project_fp8_workspace(a.rows, b.rows, a.cols, out.dtype, a.codes.device)
     ws = (None, 0) if workspace is None else _ws_args(workspace)
     _check(lib().ngram_project_fp8(a.c, b.c, _ptr(out), _value(out), *ws, _stream(stream)), "ngram_project_fp8")
     return out

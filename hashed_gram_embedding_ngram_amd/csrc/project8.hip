@@ -48,8 +48,11 @@ struct ProjArgs {
     int32_t splits;
     int32_t ntiles_n;
     int32_t ntiles;
+    int32_t band;           // tile rows walked together
+    int32_t stride;         // items from one of a workgroup to its next
 };
 
+// acc + x y, each scaled by the lowest byte of its word.
 __device__ __forceinline__ f32x4 mfma_scaled(i32x8 x, i32x8 y, f32x4 acc, uint32_t xs, uint32_t ys) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, acc, 0, 0, 0, static_cast<int>(xs), 0, static_cast<int>(ys));
 }
@@ -94,160 +97,451 @@ __device__ __forceinline__ void store4(void* c, int64_t at, f32x4 v) {
 
 // ---------------------------------------------------------------------------
 // Tiled kernel: a workgroup of WM x WN wavefronts owns a tile of 16 TM WM rows
-// of A by 16 TN WN rows of B and walks K in steps of 128 through two LDS
-// buffers, filled straight from global memory.
+// of A by 16 TN WN rows of B and walks K in steps of 128 through NS LDS
+// buffers, filled straight from global memory (no registers on the way).
 //
 // LDS rows are 128 bytes (eight 16-byte chunks); chunk c of row r sits at
-// position c ^ ((r >> 1) & 7), so the 16 rows that a group of 16 lanes reads
-// fall on 16 different 16-byte bank groups.  A load instruction fills 8 rows.
-// Scale words (four steps' bytes of a row) go through LDS too.
-__device__ __forceinline__ uint32_t chunk_pos(int row, int c) {
-    return static_cast<uint32_t>(row) * kStep + (static_cast<uint32_t>(c ^ ((row >> 1) & 7)) << 4);
-}
-
-template <int TM, int TN, int WM, int WN>
+// position c ^ ((r >> 1) & 7).  A fragment read takes chunks g and g + 4 in
+// lane group g = lane >> 4: the LDS serves 16 lanes at a time, 0-3 with 12-15 and
+// 20-27 and so on, and in this order they fall on 16 different 16-byte bank
+// groups (no conflicts counted; chunks 2 g and 2 g + 1 had one for every read).  A load instruction
+// fills 8 rows.
+//
+// Scales go through LDS as well: a row's word of four steps' bytes with the
+// first of the four, and a byte read for each fragment and step.
+template <int TM_, int TN_, int WM_, int WN_, int NS_, bool F32_>
 struct Tile {
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, NS = NS_;
+    static constexpr bool F32 = F32_;
     static constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN, Waves = WM * WN, Threads = 64 * Waves;
-    static constexpr int Stage = (BM + BN) * kStep;             // bytes of one operand buffer
-    static constexpr int ScaleStage = (BM + BN) * 4;            // bytes of one scale buffer
-    static constexpr int Lds = 2 * Stage + 2 * ScaleStage;
-    static constexpr int Groups = (BM + BN) / 8 / Waves;        // load instructions per wavefront and step
-    static constexpr int ScaleLoads = (BM + BN) / 64;           // wavefronts that load scales
-    static_assert(BM % 64 == 0 && BN % 64 == 0 && (BM / 8) % Groups == 0 && ScaleLoads <= Waves, "tile shape");
+    static constexpr int Rows = BM + BN;
+    static constexpr int Stage = Rows * kStep;                  // bytes of one operand buffer
+    static constexpr int ScaleStage = Rows * 4;                 // bytes of one scale buffer: four steps
+    static constexpr int ScaleBuffers = 4;      // the item's steps, NS ahead at most, touch no more groups of four
+    static constexpr int Lds = NS * Stage + ScaleBuffers * ScaleStage;
+    static constexpr int LoadsA = BM / 8 / Waves, LoadsB = BN / 8 / Waves, Loads = LoadsA + LoadsB;     // instructions per wavefront and step
+    static_assert(BM % 64 == 0 && BN % 64 == 0 && LoadsA % 2 == 0 && LoadsB % 2 == 0 && Rows / 64 <= Waves, "tile shape");
+    static_assert(TM % 2 == 0 && TN % 2 == 0, "fragments are stored in pairs");
+    static_assert(NS >= 2 && NS <= 4 && Lds <= 160 * 1024, "buffers");
 };
 
-// XCD-aware tile order: workgroup b runs on XCD b mod 8, and the tiles of an
-// XCD are a contiguous run of the row-tile-major order, so that one row tile's
-// A stays in that XCD's L2; a run of whole tile rows is walked column by
-// column, so that its concurrent tiles share one B tile.
-__device__ __forceinline__ bool tile_of(int b, int ntiles, int ntiles_n, int* mt, int* nt) {
-    const int per = (ntiles + 7) / 8, xcd = b & 7, slot = b >> 3;
-    const int full = ntiles - 8 * (per - 1);
+// Work item w of the launch's order: workgroup b runs on XCD b mod 8 and takes
+// items b, b + stride, ... (the stride is a multiple of 8), and the items of an XCD
+// are a contiguous run of the order: split by split, and in a split bands of `band` tile
+// rows, each walked column by column.  The tiles that an XCD has in flight
+// then share band tiles of A and a few of B at the same place of K, which
+// its L2 holds: 4 + 8 tiles for 32 workgroups, where whole columns would
+// want 32 + 1.
+struct Item {
+    int32_t mt, nt, split, valid;
+};
+__device__ __forceinline__ Item item_of(int w, const ProjArgs& a) {
+    const int total = a.ntiles * a.splits;
+    const int per = (total + 7) / 8, xcd = w & 7, slot = w >> 3;
+    const int full = total - 8 * (per - 1);
     const int count = xcd < full ? per : per - 1;
-    if (slot >= count) return false;
-    const int base = xcd < full ? xcd * per : full * per + (xcd - full) * (per - 1);
-    if (base % ntiles_n == 0 && count % ntiles_n == 0) {
-        const int rows_x = count / ntiles_n;
-        *nt = slot / rows_x;
-        *mt = base / ntiles_n + (slot - *nt * rows_x);
-    } else {
-        const int tile = base + slot;
-        *mt = tile / ntiles_n;
-        *nt = tile - *mt * ntiles_n;
-    }
-    return true;
+    const int idx = (xcd < full ? xcd * per : full * per + (xcd - full) * (per - 1)) + slot;
+    const int split = idx / a.ntiles, tile = idx - split * a.ntiles;
+    const int first = tile / (a.band * a.ntiles_n) * a.band;             // the band's first row
+    const int rows = min(a.band, a.ntiles / a.ntiles_n - first);
+    const int r = tile - first * a.ntiles_n, nt = r / max(rows, 1);
+    return Item{__builtin_amdgcn_readfirstlane(first + r - nt * rows), __builtin_amdgcn_readfirstlane(nt),
+                __builtin_amdgcn_readfirstlane(split), __builtin_amdgcn_readfirstlane(slot < count ? 1 : 0)};
 }
 
-template <int TM, int TN, int WM, int WN, bool F32>
-__global__ void __launch_bounds__(64 * WM * WN, 1) project_fp8_kernel(const ProjArgs a) {
-    using T = Tile<TM, TN, WM, WN>;
-    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int split = blockIdx.y;
-    int mt, nt;
-    if (!tile_of(blockIdx.x, a.ntiles, a.ntiles_n, &mt, &nt)) return;
-    const int64_t m0 = static_cast<int64_t>(mt) * T::BM, n0 = static_cast<int64_t>(nt) * T::BN;
-    const int wm = (wave / WN) * 16 * TM, wn = (wave % WN) * 16 * TN;
-    const int k_begin = split * a.split_steps;
-    const int k_end = min(k_begin + a.split_steps, a.steps);
+// Keeps the products of a group where they are written: the compiler would
+// otherwise gather all of a step's reads in front of the barrier and all its
+// products behind it.
+template <int N>
+__device__ __forceinline__ void pin(f32x4* acc) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) __asm__ volatile("" : "+v"(acc[j]));
+    __builtin_amdgcn_sched_barrier(0);
+}
 
-    // Operand loads: wavefront w fills row groups w Groups .. of [A tile | B
-    // tile].  Rows past M or N are clamped: their results are never stored.
-    const bool of_a = wave * T::Groups < T::BM / 8;
-    const int64_t tile0 = of_a ? m0 : n0, last = (of_a ? a.m : a.n) - 1;
-    const uint8_t* src = (of_a ? a.a : a.b) + tile0 * a.ld + static_cast<int64_t>(k_begin) * kStep;
-    uint32_t off[T::Groups];
-#pragma unroll
-    for (int q = 0; q < T::Groups; ++q) {
-        const int r = 8 * (wave * T::Groups + q - (of_a ? 0 : T::BM / 8)) + (lane >> 3);
-        const int rr = static_cast<int>(min(tile0 + r, last) - tile0);
-        off[q] = static_cast<uint32_t>(rr) * static_cast<uint32_t>(a.ld) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
-    }
-    // Scale loads: wavefront w < ScaleLoads fills 64 rows of [A | B].
-    const uint8_t* ssrc = a.as;
-    if (wave < T::ScaleLoads) {
-        const bool sa = wave * 64 < T::BM;
-        const int64_t row = sa ? min(m0 + wave * 64 + lane, a.m - 1) : min(n0 + wave * 64 - T::BM + lane, a.n - 1);
-        ssrc = (sa ? a.as : a.bs) + (row >> (sa ? a.ash : a.bsh)) * a.sld + k_begin;
-    }
-    auto issue = [&](int i) {       // step k_begin + i into buffer i & 1
-        uint8_t* const buf = lds + (i & 1) * T::Stage;
-#pragma unroll
-        for (int q = 0; q < T::Groups; ++q)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src + static_cast<int64_t>(i) * kStep + off[q]),
-                                             (__attribute__((address_space(3))) void*)(buf + (wave * T::Groups + q) * 1024), 16, 0, 0);
-        if ((i & 3) == 0 && wave < T::ScaleLoads)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(ssrc + i),
-                                             (__attribute__((address_space(3))) void*)(lds + 2 * T::Stage + ((i >> 2) & 1) * T::ScaleStage + wave * 256), 4, 0, 0);
-    };
-
-    f32x4 acc[TM][TN];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    uint32_t sa[TM], sb[TN];
-    const int steps = k_end - k_begin;
-    const int lr = lane & 15, lc = (lane >> 4) * 2;
-    issue(0);
-    for (int i = 0; i < steps; ++i) {
-        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (i + 1 < steps) issue(i + 1);
-        const uint8_t* const at = lds + (i & 1) * T::Stage;
-        const uint8_t* const bt = at + T::BM * kStep;
-        if ((i & 3) == 0) {
-            const uint32_t* const sc = reinterpret_cast<const uint32_t*>(lds + 2 * T::Stage + ((i >> 2) & 1) * T::ScaleStage);
-#pragma unroll
-            for (int s = 0; s < TM; ++s) sa[s] = sc[wm + 16 * s + lr];
-#pragma unroll
-            for (int s = 0; s < TN; ++s) sb[s] = sc[T::BM + wn + 16 * s + lr];
-        }
-        const auto frag = [&](const uint8_t* base, int r) {
-            return join(*reinterpret_cast<const u32x4*>(base + chunk_pos(r, lc)), *reinterpret_cast<const u32x4*>(base + chunk_pos(r, lc + 1)));
-        };
-        if constexpr (F32) {
-            Wide fb[TN];
-#pragma unroll
-            for (int s = 0; s < TN; ++s) fb[s] = widen(frag(bt, wn + 16 * s + lr), sb[s]);
-#pragma unroll
-            for (int s = 0; s < TM; ++s) {
-                const Wide fa = widen(frag(at, wm + 16 * s + lr), sa[s]);
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[s][j] = mfma_wide(fb[j], fa, acc[s][j]);
-            }
-        } else {
-            i32x8 fb[TN];
-#pragma unroll
-            for (int s = 0; s < TN; ++s) fb[s] = frag(bt, wn + 16 * s + lr);
-#pragma unroll
-            for (int s = 0; s < TM; ++s) {
-                const i32x8 fa = frag(at, wm + 16 * s + lr);
-#pragma unroll
-                for (int j = 0; j < TN; ++j) acc[s][j] = mfma_scaled(fb[j], fa, acc[s][j], sb[j], sa[s]);
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < TM; ++s) sa[s] >>= 8;
-#pragma unroll
-        for (int s = 0; s < TN; ++s) sb[s] >>= 8;
-    }
-    // The B fragment is the instruction's row operand, so lane l holds, of
-    // each 16 x 16 tile, row l & 15 of A and four consecutive rows
-    // 4 (l >> 4) .. +3 of B: four consecutive outputs.
+// The B fragment is the instruction's row operand, so lane l holds, of each
+// 16 x 16 tile, row l & 15 of A and four consecutive rows 4 (l >> 4) .. +3 of
+// B: four consecutive outputs, 16 bytes of fp32.  In bf16 that is 8, so two
+// neighbouring tiles' values are exchanged between lane groups 0 and 1, 2 and
+// 3: then a lane has eight consecutive outputs of one of the two, and a store
+// writes 64 consecutive bytes of 16 rows (32-byte pieces took 8% of the whole
+// product's time at 32768 x 2560 x 2560).
+template <int TM, int TN, bool F32>
+__device__ __forceinline__ void store_tile(const ProjArgs& a, const f32x4 (&acc)[TM][TN], int64_t m0, int64_t n0, int split, int lane) {
+    const int lr = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int s = 0; s < TM; ++s) {
-        const int64_t row = m0 + wm + 16 * s + lr;
+        const int64_t row = m0 + 16 * s + lr;
+        if (F32 || a.splits > 1) {
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int64_t col = n0 + wn + 16 * j + 4 * (lane >> 4);
-            if (row < a.m && col < a.n) {
-                if (a.splits > 1) store4<true>(a.partial, (split * a.m + row) * a.n + col, acc[s][j]);
-                else store4<F32>(a.c, row * a.n + col, acc[s][j]);
+            for (int j = 0; j < TN; ++j) {
+                const int64_t col = n0 + 16 * j + 4 * g;
+                if (row < a.m && col < a.n) {
+                    if (a.splits > 1) store4<true>(a.partial, (split * a.m + row) * a.n + col, acc[s][j]);
+                    else store4<F32>(a.c, row * a.n + col, acc[s][j]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < TN; j += 2) {
+                const f32x4 x = acc[s][j], y = acc[s][j + 1];
+                const auto p = __builtin_amdgcn_permlane16_swap(bf16_pair(x[0], x[1]), bf16_pair(y[0], y[1]), false, false);
+                const auto q = __builtin_amdgcn_permlane16_swap(bf16_pair(x[2], x[3]), bf16_pair(y[2], y[3]), false, false);
+                const int64_t col = n0 + 16 * j + 16 * (g & 1) + 8 * (g >> 1);
+                if (row < a.m && col < a.n)
+                    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.c) + row * a.n + col) = u32x4{p[0], q[0], p[1], q[1]};
             }
         }
     }
+}
+
+template <class T>
+__global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjArgs a) {
+    constexpr int TM = T::TM, TN = T::TN, NS = T::NS;
+    constexpr bool F32 = T::F32, Two = NS == 2;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int t = threadIdx.x, lane = t & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int wm = (wave / T::WN) * 16 * TM, wn = (wave % T::WN) * 16 * TN;
+    int w = blockIdx.x, lw = w;
+    Item now = item_of(w, a);
+    if (!now.valid) return;
+
+    // Loads run ahead of the products, through the end of an item into the next.
+    //
+    // Operands: wavefront v fills row groups v LoadsA .. of the A tile and v
+    // LoadsB .. of the B tile, 8 rows an instruction; every other group has
+    // the same swizzle.  Rows past M or N are clamped to the last row (their
+    // results are never stored): the limit is that row's offset.  Scales:
+    // thread t < Rows brings the word of row t of [A tile | B tile].
+    const uint32_t ld = static_cast<uint32_t>(a.ld);
+    const uint32_t chunk0 = 16u * ((lane & 7) ^ (lane >> 4)), flip = (chunk0 ^ 64u) - chunk0;
+    const uint32_t off_a = (8 * wave * T::LoadsA + (lane >> 3)) * ld + chunk0, off_b = (8 * wave * T::LoadsB + (lane >> 3)) * ld + chunk0;
+    uint8_t* const sbuf = lds + NS * T::Stage;
+    const uint8_t *pa, *pb, *ps;        // the load step's first rows; the thread's scale byte of it
+    uint32_t last_a, last_b;            // offsets of the tiles' last rows
+    int ahead, left;                    // the load step in its item, steps left with it
+    int put_to = -1;                    // the scale buffer loaded last
+    const auto steps_of = [&](const Item& it) { return min(a.split_steps, a.steps - it.split * a.split_steps); };
+    const auto load_from = [&](const Item& it) {
+        const int64_t m0 = static_cast<int64_t>(it.mt) * T::BM, n0 = static_cast<int64_t>(it.nt) * T::BN;
+        const int64_t k0 = static_cast<int64_t>(it.split) * a.split_steps;
+        last_a = (static_cast<uint32_t>(min(a.m - m0, static_cast<int64_t>(T::BM))) - 1) * ld;
+        last_b = (static_cast<uint32_t>(min(a.n - n0, static_cast<int64_t>(T::BN))) - 1) * ld;
+        pa = a.a + m0 * a.ld + k0 * kStep;
+        pb = a.b + n0 * a.ld + k0 * kStep;
+        const bool sa = t < T::BM;
+        const int64_t row = sa ? min(m0 + t, a.m - 1) : min(n0 + t - T::BM, a.n - 1);
+        ps = (sa ? a.as : a.bs) + (row >> (sa ? a.ash : a.bsh)) * a.sld + k0;
+        ahead = 0;
+        left = steps_of(it);
+    };
+    const auto step_on = [&] {          // after a step's loads
+        if (--left > 0) {
+            pa += kStep;
+            pb += kStep;
+            ps += 1;
+            ++ahead;
+            return;
+        }
+        lw += a.stride;
+        const Item it = item_of(lw, a);
+        if (it.valid) {
+            load_from(it);
+        } else {                        // nothing follows: the last step again, never read
+            lw -= a.stride;
+            left = 1;
+        }
+    };
+    const auto load = [&](const uint8_t* s, uint32_t off, uint32_t last, uint8_t* to, int q) {
+        const uint32_t at = min(off + 8 * q * ld, last + chunk0) + (q & 1 ? flip : 0u);     // modulo 2^32: flip may be -64
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(s + at),
+                                         (__attribute__((address_space(3))) void*)(to + q * 1024), 16, 0, 0);
+    };
+    const auto load_a = [&](int buffer, int q) { load(pa, off_a, last_a, lds + buffer * T::Stage + wave * T::LoadsA * 1024, q); };
+    const auto load_b = [&](int buffer, int q) {
+        load(pb, off_b, last_b, lds + buffer * T::Stage + T::BM * kStep + wave * T::LoadsB * 1024, q);
+    };
+    const auto load_scales = [&] {      // ahead of a step's other loads
+        if ((ahead & 3) != 0) return;
+        put_to = (put_to + 1) & (T::ScaleBuffers - 1);
+        if (wave < T::Rows / 64)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)ps,
+                                             (__attribute__((address_space(3))) void*)(sbuf + put_to * T::ScaleStage + wave * 256), 4, 0, 0);
+    };
+
+    // A lane reads chunks g and g + 4 (g = lane >> 4) of its fragment rows.
+    // Rows 16 s + lr of a fragment share the swizzle of lr, so one lane
+    // offset per chunk serves them all.
+    const int lr = lane & 15, g = lane >> 4;
+    const uint32_t lo = lr * kStep + ((g ^ ((lr >> 1) & 7)) << 4), hi = lo ^ 64u;
+    const auto frag = [&](const uint8_t* rows, int s) {
+        return join(*reinterpret_cast<const u32x4*>(rows + s * 16 * kStep + lo), *reinterpret_cast<const u32x4*>(rows + s * 16 * kStep + hi));
+    };
+    const uint32_t a_row = wm * kStep, b_row = (T::BM + wn) * kStep;
+    uint32_t sa[TM], sb[TN];
+    const auto scales = [&](int i, int buffer) {        // step i's bytes of this wavefront's rows
+        const uint8_t* const p = sbuf + buffer * T::ScaleStage + (i & 3) + lr * 4;
+#pragma unroll
+        for (int s = 0; s < TM; ++s) sa[s] = p[(wm + 16 * s) * 4];
+#pragma unroll
+        for (int s = 0; s < TN; ++s) sb[s] = p[(T::BM + wn + 16 * s) * 4];
+    };
+    f32x4 acc[TM][TN];
+    const auto clear = [&] {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    i32x8 fb[TN], fa, next;     // codes; the bf16 instruction's operands are widened from them when they are used
+    Wide wb[F32 ? TN : 1];
+    const auto times = [&](int s, int j, const i32x8& x, const Wide& xw, uint32_t xs, uint32_t ys) {
+        if constexpr (F32) acc[s][j] = mfma_wide(wb[j], xw, acc[s][j]);
+        else acc[s][j] = mfma_scaled(fb[j], x, acc[s][j], ys, xs);
+    };
+    const auto wide = [&](const i32x8& x, uint32_t scale) {
+        Wide v{};
+        if constexpr (F32) v = widen(x, scale);
+        return v;
+    };
+    // Before the loop: step 0, and the loads of the steps after it (with two
+    // buffers, A's of step 1).
+    load_from(now);
+#pragma unroll
+    for (int s = 0; s < (Two ? 1 : NS); ++s) {
+        load_scales();
+#pragma unroll
+        for (int q = 0; q < T::LoadsA; ++q) load_a(s, q);
+#pragma unroll
+        for (int q = 0; q < T::LoadsB; ++q) load_b(s, q);
+        step_on();
+    }
+    __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(Two ? 0 : (NS - 1) * T::Loads) : "memory");
+    __syncthreads();
+    if (Two) {
+        load_scales();
+#pragma unroll
+        for (int q = 0; q < T::LoadsA; ++q) load_a(1, q);
+    }
+    scales(0, 0);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb[j] = frag(lds + b_row, j);
+    fa = frag(lds + a_row, 0);
+    clear();
+    int i = 0, steps = steps_of(now), read_from = 0;
+    for (int buffer = 0;;) {
+        const int after = buffer + 1 == NS ? 0 : buffer + 1;
+        const uint8_t* const at = lds + buffer * T::Stage + a_row;
+        if constexpr (F32)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) wb[j] = widen(fb[j], sb[j]);
+        // Rows 0 .. TM - 3.  A load instruction takes the wavefront's turn
+        // for as long as the CU's one load path needs for it (16 cycles or
+        // more), so the large tile's loads are spread: A's over the tail of
+        // the step that frees the buffer, B's over the head of the next.
+        i32x8 over;
+#pragma unroll
+        for (int s = 0; s < TM - 2; ++s) {
+            next = frag(at, s + 1);
+            if (s == TM - 3) over = frag(at, TM - 1);
+            const Wide xw = wide(fa, sa[s]);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) times(s, j, fa, xw, sa[s], sb[j]);
+            fa = next;
+            // the first product waits for this group's reads; the next
+            // group's are issued behind it
+            if (!F32) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                if (s == TM - 3) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+                else __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, TN - 1, 0);
+            }
+            pin<TN>(acc[s]);
+            if (Two && s < 2)
+#pragma unroll
+                for (int q = s * T::LoadsB / 2; q < (s + 1) * T::LoadsB / 2; ++q) load_b(after, q);
+        }
+        if (TM == 2) over = frag(at, 1);
+        if (Two) step_on();
+        // the next step's loads have landed: NS - 2 later steps' may be in flight
+        __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((NS - 2) * T::Loads) : "memory");
+        __builtin_amdgcn_s_barrier();
+        __asm__ volatile("" ::: "memory");
+        const uint32_t tx = sa[TM - 2], ty = sa[TM - 1];
+        uint32_t tb[TN];
+#pragma unroll
+        for (int s = 0; s < TN; ++s) tb[s] = sb[s];
+        const int to = ++i < steps ? i : 0;
+        if ((to & 3) == 0) read_from = (read_from + 1) & (T::ScaleBuffers - 1);
+        scales(to, read_from);
+        // A step's last two row fragments (fa, over) are multiplied after
+        // the barrier that ends its reads, while the next step's first
+        // fragments are on their way.
+        const uint8_t* const nt = lds + after * T::Stage;
+        const i32x8 first = frag(nt + a_row, 0);
+        const Wide xw = wide(fa, tx), yw = wide(over, ty);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            times(TM - 2, j, fa, xw, tx, tb[j]);
+            times(TM - 1, j, over, yw, ty, tb[j]);
+            fb[j] = frag(nt + b_row, j);
+            pin<1>(&acc[TM - 2][j]);
+            pin<1>(&acc[TM - 1][j]);
+            if (j == 0) load_scales();
+#pragma unroll
+            for (int q = j * T::LoadsA / TN; q < (j + 1) * T::LoadsA / TN; ++q) load_a(buffer, q);
+            if (!Two)
+#pragma unroll
+                for (int q = j * T::LoadsB / TN; q < (j + 1) * T::LoadsB / TN; ++q) load_b(buffer, q);
+        }
+        if (!Two) step_on();
+        fa = first;
+        buffer = after;
+        if (i < steps) continue;
+        store_tile<TM, TN, F32>(a, acc, static_cast<int64_t>(now.mt) * T::BM + wm, static_cast<int64_t>(now.nt) * T::BN + wn, now.split, lane);
+        w += a.stride;
+        now = item_of(w, a);
+        if (!now.valid) break;
+        i = 0;
+        steps = steps_of(now);
+        clear();
+    }
+    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");        // loads into LDS end before the workgroup does
+}
+
+// Small results, where a step is over long before the next one's loads have
+// landed: a workgroup's G groups of WM x WN wavefronts each take every G-th
+// step of K of one tile, so that G steps' loads are in flight and the chain of
+// waits is G times shorter, and join their accumulators in LDS at the end.
+// Same LDS layout and fragments as above; a scale word is loaded with every
+// G steps.
+template <int TM_, int TN_, int WM_, int WN_, int G_, bool F32_>
+struct SmallTile {
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, G = G_;
+    static constexpr bool F32 = F32_;
+    static constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN, Waves = WM * WN, Threads = 64 * Waves * G;
+    static constexpr int Rows = BM + BN;
+    static constexpr int Part = Rows * kStep;                   // bytes of one group's operand buffer
+    static constexpr int Stage = G * Part + Rows * 4;           // of a stage: the groups' operands, then the scale words
+    static constexpr int Lds = 2 * Stage;
+    static constexpr int LoadsA = BM / 8 / Waves, LoadsB = BN / 8 / Waves;
+    static_assert(BM % 64 == 0 && BN % 64 == 0 && LoadsA % 2 == 0 && LoadsB % 2 == 0 && Rows / 64 <= Waves * G, "tile shape");
+    static_assert(4 % G == 0 && TM % 2 == 0 && TN % 2 == 0 && Lds <= 160 * 1024 && (G - 1) * BM * BN * 4 <= Lds, "groups");
+};
+
+template <class T>
+__global__ void __launch_bounds__(T::Threads, 1) project_fp8_small_kernel(const ProjArgs a) {
+    constexpr int TM = T::TM, TN = T::TN, G = T::G;
+    constexpr bool F32 = T::F32;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int t = threadIdx.x, lane = t & 63;
+    const int all = __builtin_amdgcn_readfirstlane(t >> 6), group = all / T::Waves, wave = all % T::Waves;
+    const int wm = (wave / T::WN) * 16 * TM, wn = (wave % T::WN) * 16 * TN;
+    const Item it = item_of(blockIdx.x, a);
+    if (!it.valid) return;
+    const int64_t m0 = static_cast<int64_t>(it.mt) * T::BM, n0 = static_cast<int64_t>(it.nt) * T::BN;
+    const int k0 = it.split * a.split_steps, k1 = min(k0 + a.split_steps, a.steps);
+    const int rounds = (k1 - k0 + G - 1) / G;
+
+    const uint32_t ld = static_cast<uint32_t>(a.ld);
+    const uint32_t chunk0 = 16u * ((lane & 7) ^ (lane >> 4)), flip = (chunk0 ^ 64u) - chunk0;
+    const uint32_t off_a = (8 * wave * T::LoadsA + (lane >> 3)) * ld + chunk0, off_b = (8 * wave * T::LoadsB + (lane >> 3)) * ld + chunk0;
+    const uint32_t last_a = (static_cast<uint32_t>(min(a.m - m0, static_cast<int64_t>(T::BM))) - 1) * ld + chunk0;
+    const uint32_t last_b = (static_cast<uint32_t>(min(a.n - n0, static_cast<int64_t>(T::BN))) - 1) * ld + chunk0;
+    const uint8_t* const pa = a.a + m0 * a.ld;
+    const uint8_t* const pb = a.b + n0 * a.ld;
+    const bool sa_row = t < T::BM;
+    const int64_t srow = sa_row ? min(m0 + t, a.m - 1) : min(n0 + t - T::BM, a.n - 1);
+    const uint8_t* const ps = (sa_row ? a.as : a.bs) + (srow >> (sa_row ? a.ash : a.bsh)) * a.sld;
+    const auto issue = [&](int r) {     // round r: this group's step, the last one again where there is none
+        uint8_t* const stage = lds + (r & 1) * T::Stage;
+        uint8_t* const to = stage + group * T::Part;
+        const int64_t k = static_cast<int64_t>(min(k0 + r * G + group, k1 - 1)) * kStep;
+        if (all < T::Rows / 64)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(ps + ((k0 + r * G) & ~3)),
+                                             (__attribute__((address_space(3))) void*)(stage + G * T::Part + all * 256), 4, 0, 0);
+#pragma unroll
+        for (int q = 0; q < T::LoadsA; ++q) {
+            const uint32_t at = min(off_a + 8 * q * ld, last_a) + (q & 1 ? flip : 0u);      // modulo 2^32: flip may be -64
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(pa + k + at),
+                                             (__attribute__((address_space(3))) void*)(to + (wave * T::LoadsA + q) * 1024), 16, 0, 0);
+        }
+#pragma unroll
+        for (int q = 0; q < T::LoadsB; ++q) {
+            const uint32_t at = min(off_b + 8 * q * ld, last_b) + (q & 1 ? flip : 0u);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(pb + k + at),
+                                             (__attribute__((address_space(3))) void*)(to + T::BM * kStep + (wave * T::LoadsB + q) * 1024), 16, 0, 0);
+        }
+    };
+    const int lr = lane & 15, g = lane >> 4;
+    const uint32_t lo = lr * kStep + ((g ^ ((lr >> 1) & 7)) << 4), hi = lo ^ 64u;
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int s = 0; s < TM; ++s)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[s][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    issue(0);
+    for (int r = 0; r < rounds; ++r) {
+        __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        __asm__ volatile("" ::: "memory");
+        if (r + 1 < rounds) issue(r + 1);
+        const int step = k0 + r * G + group;
+        if (step >= k1) continue;       // the whole wavefront; it comes back to the barrier
+        const uint8_t* const stage = lds + (r & 1) * T::Stage;
+        const uint8_t* const at = stage + group * T::Part + wm * kStep;
+        const uint8_t* const bt = stage + group * T::Part + (T::BM + wn) * kStep;
+        const uint8_t* const sc = stage + G * T::Part + (step & 3) + lr * 4;
+        uint32_t sa[TM], sb[TN];
+        i32x8 fa[TM], fb[TN];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            sb[j] = sc[(T::BM + wn + 16 * j) * 4];
+            fb[j] = join(*reinterpret_cast<const u32x4*>(bt + j * 16 * kStep + lo), *reinterpret_cast<const u32x4*>(bt + j * 16 * kStep + hi));
+        }
+#pragma unroll
+        for (int s = 0; s < TM; ++s) {
+            sa[s] = sc[(wm + 16 * s) * 4];
+            fa[s] = join(*reinterpret_cast<const u32x4*>(at + s * 16 * kStep + lo), *reinterpret_cast<const u32x4*>(at + s * 16 * kStep + hi));
+        }
+        if constexpr (F32) {
+            Wide wb[TN];
+#pragma unroll
+            for (int j = 0; j < TN; ++j) wb[j] = widen(fb[j], sb[j]);
+#pragma unroll
+            for (int s = 0; s < TM; ++s) {
+                const Wide wa = widen(fa[s], sa[s]);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[s][j] = mfma_wide(wb[j], wa, acc[s][j]);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < TM; ++s)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[s][j] = mfma_scaled(fb[j], fa[s], acc[s][j], sb[j], sa[s]);
+        }
+    }
+    if (G > 1) {
+        __syncthreads();                // every read of the operands is done
+        f32x4* const part = reinterpret_cast<f32x4*>(lds);
+        constexpr int PerWave = TM * TN * 64;
+        if (group > 0) {
+#pragma unroll
+            for (int s = 0; s < TM; ++s)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) part[((group - 1) * T::Waves + wave) * PerWave + (s * TN + j) * 64 + lane] = acc[s][j];
+        }
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int o = 0; o < G - 1; ++o)
+#pragma unroll
+            for (int s = 0; s < TM; ++s)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[s][j] += part[(o * T::Waves + wave) * PerWave + (s * TN + j) * 64 + lane];
+    }
+    store_tile<TM, TN, F32>(a, acc, m0 + wm, n0 + wn, it.split, lane);
 }
 
 // The sum of the splits' partial products, in their order.
@@ -313,39 +607,73 @@ __global__ void __launch_bounds__(512) project_fp8_rows_kernel(const ProjArgs a)
 // ---------------------------------------------------------------------------
 // Which kernel, tile and split.
 struct Plan {
-    int kind;           // 0: few rows; 1: 64 x 64; 2: 128 x 128; 3: 256 x 256
+    int kind;           // 0: few rows; 1: 64 x 64; 2: 128 x 128; 3: 256 x 256 (fp32: 256 x 128)
     int splits;
-    int split_steps;
+    int split_steps;    // a multiple of 4
 };
 
 constexpr int kUnits = 256;     // compute units
+constexpr int64_t kRows = 64;   // most rows of A for the few-rows kernel
 
-Plan plan_of(int64_t m, int64_t n, int64_t k) {
+// The tile kernels run one workgroup per compute unit, so a product takes
+// ceil(items / 256) rounds of one item's time, and an item's time is nearly a fixed
+// part plus a part per step.  Measured on MI355X at 16 to 32768 rows (us, bf16 /
+// fp32 result): 64 x 64: 3 + 0.23 / 0.32 a step; 128 x 128: 4 + 0.53 / 0.9;
+// the large tile 8 + 1.4 / 1.5.  At 2560 x 2560 the large tile wins from about 4000
+// rows (36 against 45 us), 128 x 128 from about 600 (1024 rows: 16 against 24).  Splitting K
+// pays where tiles are few and K is long; it costs a second launch and the
+// partial sums' way through memory.
+Plan plan_of(int64_t m, int64_t n, int64_t k, bool f32) {
     const int steps = static_cast<int>(blocks_of(k));
-    Plan p{0, 1, (steps + 3) / 4 * 4};
-    if (m <= 64) return p;
-    const auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
-    p.kind = tiles(256) >= kUnits ? 3 : tiles(128) >= kUnits ? 2 : 1;
-    // long K over few tiles (the weight gradient): larger tiles, K split
-    if (p.kind < 3 && steps >= 32) p.kind = tiles(256) >= 32 ? 3 : 2;
-    const int64_t have = tiles(p.kind == 3 ? 256 : p.kind == 2 ? 128 : 64);
-    const int64_t want = (p.kind == 3 ? 1 : 2) * kUnits;
-    int64_t splits = std::min<int64_t>(std::max<int64_t>(1, want / std::max<int64_t>(1, have)), std::max(1, steps / 16));
-    p.split_steps = static_cast<int>(((steps + splits - 1) / splits + 3) / 4 * 4);
-    p.splits = (steps + p.split_steps - 1) / p.split_steps;
-    return p;
+    Plan best{0, 1, (steps + 3) / 4 * 4};
+    if (m <= kRows) return best;
+    const double fixed[3] = {3, 4, 8}, step16[3] = {0.23, 0.53, 1.4}, step32[3] = {0.32, 0.9, 1.5};
+    const int64_t rows[3] = {64, 128, 256}, cols[3] = {64, 128, f32 ? 128 : 256};
+    double least = 0;
+    for (int kind = 1; kind <= 3; ++kind) {
+        const int64_t tiles = ((m + rows[kind - 1] - 1) / rows[kind - 1]) * ((n + cols[kind - 1] - 1) / cols[kind - 1]);
+        int before = 0;
+        for (int want = 1; want <= 32; ++want) {
+            const int per = ((steps + want - 1) / want + 3) / 4 * 4, splits = (steps + per - 1) / per;
+            if (splits == before || (splits > 1 && per < 16)) continue;
+            before = splits;
+            const double rounds = static_cast<double>((tiles * splits + kUnits - 1) / kUnits);
+            double us = rounds * (fixed[kind - 1] + (f32 ? step32 : step16)[kind - 1] * std::min(per, steps));
+            if (splits > 1) us += 4 + 8e-6 * static_cast<double>(splits) * static_cast<double>(m) * static_cast<double>(n) / 4;
+            if (best.kind == 0 || us < least) {
+                least = us;
+                best = Plan{kind, splits, per};
+            }
+        }
+    }
+    return best;
 }
 
-template <int TM, int TN, int WM, int WN>
-int launch_tile(ProjArgs& a, bool f32, hipStream_t st) {
-    using T = Tile<TM, TN, WM, WN>;
-    const int64_t mt = (a.m + T::BM - 1) / T::BM, nt = (a.n + T::BN - 1) / T::BN;
-    if (mt * nt > INT32_MAX / 16) return fail(NGRAM_ERANGE, "%lld x %lld too large for one launch", (long long)a.m, (long long)a.n);
+template <class T>
+int launch_tile(ProjArgs& a, hipStream_t st) {
+    const int64_t mt = (a.m + T::BM - 1) / T::BM, nt = (a.n + T::BN - 1) / T::BN, items = mt * nt * a.splits;
+    if (items > INT32_MAX / 2) return fail(NGRAM_ERANGE, "%lld x %lld too large for one launch", (long long)a.m, (long long)a.n);
     a.ntiles_n = static_cast<int32_t>(nt);
     a.ntiles = static_cast<int32_t>(mt * nt);
-    const dim3 grid(8 * ((a.ntiles + 7) / 8), a.splits), block(T::Threads);
-    if (f32) hipLaunchKernelGGL((project_fp8_kernel<TM, TN, WM, WN, true>), grid, block, T::Lds, st, a);
-    else hipLaunchKernelGGL((project_fp8_kernel<TM, TN, WM, WN, false>), grid, block, T::Lds, st, a);
+    a.band = T::BM >= 256 ? 2 : 8;
+    // as many workgroups as the chip holds at once, each with every stride-th
+    // item; where an item has fewer steps than there are buffers, an item each
+    const int64_t room = kUnits * std::max(1, 160 * 1024 / T::Lds);
+    const int64_t least = std::min<int64_t>(a.split_steps, a.steps - (a.splits - 1) * a.split_steps);     // the last split's steps
+    const dim3 grid(static_cast<unsigned>(least < 4 ? (items + 7) / 8 * 8 : std::min((items + 7) / 8 * 8, room))), block(T::Threads);
+    a.stride = static_cast<int32_t>(grid.x);
+    hipLaunchKernelGGL((project_fp8_kernel<T>), grid, block, T::Lds, st, a);
+    return NGRAM_OK;
+}
+
+template <class T>
+int launch_small(ProjArgs& a, hipStream_t st) {
+    const int64_t mt = (a.m + T::BM - 1) / T::BM, nt = (a.n + T::BN - 1) / T::BN, items = mt * nt * a.splits;
+    if (items > INT32_MAX / 2) return fail(NGRAM_ERANGE, "%lld x %lld too large for one launch", (long long)a.m, (long long)a.n);
+    a.ntiles_n = static_cast<int32_t>(nt);
+    a.ntiles = static_cast<int32_t>(mt * nt);
+    a.band = 8;
+    hipLaunchKernelGGL((project_fp8_small_kernel<T>), dim3(static_cast<unsigned>((items + 7) / 8 * 8)), dim3(T::Threads), T::Lds, st, a);
     return NGRAM_OK;
 }
 
@@ -371,9 +699,9 @@ using namespace ng8;
 
 extern "C" {
 
-int64_t ngram_project_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k) {
-    if (!sizes_ok(m, n, k)) return -1;
-    const Plan p = plan_of(m, n, k);
+int64_t ngram_project_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t c_dtype) {
+    if (!sizes_ok(m, n, k) || (c_dtype != NGRAM_F32 && c_dtype != NGRAM_BF16)) return -1;
+    const Plan p = plan_of(m, n, k, c_dtype == NGRAM_F32);
     return p.splits > 1 ? 4 * p.splits * m * n : 0;
 }
 
@@ -392,8 +720,9 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
     if (A->rows == 0) return NGRAM_OK;
     if (!C) return fail(NGRAM_EINVAL, "C is NULL");
     if (!aligned(C, 16)) return fail(NGRAM_EALIGN, "C must be 16-byte aligned");
-    const Plan p = plan_of(A->rows, B->rows, A->cols);
-    const int64_t need = ngram_project_fp8_workspace_bytes(A->rows, B->rows, A->cols);
+    const bool f32 = c_dtype == NGRAM_F32;
+    const Plan p = plan_of(A->rows, B->rows, A->cols, f32);
+    const int64_t need = p.splits > 1 ? 4 * p.splits * A->rows * B->rows : 0;
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return fail(NGRAM_EINVAL, "workspace must hold %lld bytes, 16-byte aligned", (long long)need);
     ProjArgs a;
@@ -404,8 +733,7 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
     a.bsh = B->block_rows == kBlock ? 7 : 0;
     a.steps = static_cast<int32_t>(blocks_of(A->cols));
     a.split_steps = p.split_steps; a.splits = p.splits;
-    a.ntiles_n = a.ntiles = 0;
-    const bool f32 = c_dtype == NGRAM_F32;
+    a.ntiles_n = a.ntiles = a.band = a.stride = 0;
     rc = NGRAM_OK;
     if (p.kind == 0) {
         if ((a.n + 15) / 16 > INT32_MAX) return fail(NGRAM_ERANGE, "B too large for one launch");
@@ -413,11 +741,11 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
         else if (a.m <= 32) launch_rows<2>(a, f32, stream);
         else launch_rows<4>(a, f32, stream);
     } else if (p.kind == 1) {
-        rc = launch_tile<2, 2, 2, 2>(a, f32, stream);
+        rc = f32 ? launch_small<SmallTile<2, 2, 2, 2, 4, true>>(a, stream) : launch_small<SmallTile<2, 2, 2, 2, 4, false>>(a, stream);
     } else if (p.kind == 2) {
-        rc = launch_tile<4, 4, 2, 2>(a, f32, stream);
+        rc = f32 ? launch_small<SmallTile<4, 2, 2, 4, 2, true>>(a, stream) : launch_small<SmallTile<4, 2, 2, 4, 2, false>>(a, stream);
     } else {
-        rc = launch_tile<8, 4, 2, 4>(a, f32, stream);
+        rc = f32 ? launch_tile<Tile<4, 4, 4, 2, 3, true>>(a, stream) : launch_tile<Tile<8, 4, 2, 4, 2, false>>(a, stream);
     }
     if (rc) return rc;
     if (a.splits > 1) {

@@ -474,16 +474,16 @@ int ngram_add_norm_grad(const void* dy, int32_t dy_dtype, const uint16_t* sum, c
 
 /* Product of 8-bit matrices: C[i][o] = sum over j of A[i][j] B[o][j] (values,
  * scales included), fp32 accumulation in an order that is fixed for given
- * sizes.  A is m x k, B is n x k (n a multiple of 8), C[m][n] fp32 or bf16
+ * sizes and result type.  A is m x k, B is n x k (n a multiple of 8), C[m][n] fp32 or bf16
  * (rounded once), 16-byte aligned.  Either operand may have block_rows 1 or
  * 128.  The layer y = P x is A = x, B = P (n x k = d_out x d_in); its
  * gradients are dx: A = dy, B = P transposed (ngram_quant_fp8's qt, its tile
  * scales the same), and dP: A = dy transposed, B = x transposed, both with
  * their blocks along the tokens.  k <= 2^23.  A NaN code gives NaN in its row or column
  * of C.  workspace: device, 16-byte aligned,
- * ngram_project_fp8_workspace_bytes(m, n, k) bytes (0 for many sizes: then it
- * may be NULL).  Errors: EINVAL, EALIGN, ERANGE; m = 0 launches nothing. */
-int64_t ngram_project_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k);
+ * ngram_project_fp8_workspace_bytes(m, n, k, c_dtype) bytes (0 for many
+ * sizes: then it may be NULL).  Errors: EINVAL, EALIGN, ERANGE; m = 0 launches nothing. */
+int64_t ngram_project_fp8_workspace_bytes(int64_t m, int64_t n, int64_t k, int32_t c_dtype);
 int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c_dtype, void* workspace,
                       int64_t workspace_bytes, ngram_stream_t stream);
 

@@ -26,8 +26,8 @@ def test_sizes():
     assert L.ngram_fp8_scale_bytes(5, 5, 64) == -1
     assert L.ngram_add_norm_grad_workspace_bytes(5, 12) == -1 and L.ngram_add_norm_grad_workspace_bytes(-1, 8) == -1
     assert L.ngram_add_norm_grad_workspace_bytes(5, 65544) == -1 and L.ngram_add_norm_grad_workspace_bytes(0, 64) > 0
-    assert L.ngram_project_fp8_workspace_bytes(5, 12, 64) == -1 and L.ngram_project_fp8_workspace_bytes(5, 8, (1 << 23) + 1) == -1
-    assert L.ngram_project_fp8_workspace_bytes(4, 2560, 2560) >= 0
+    assert L.ngram_project_fp8_workspace_bytes(5, 12, 64, 0) == -1 and L.ngram_project_fp8_workspace_bytes(5, 8, (1 << 23) + 1, 0) == -1
+    assert L.ngram_project_fp8_workspace_bytes(4, 2560, 2560, 1) >= 0 and L.ngram_project_fp8_workspace_bytes(4, 8, 8, 2) == -1
 
 
 def norm(x=A, xt=1, res=A, n=4, d=64, gamma=A, eps=1e-6, s=A, y=A, q=None, r=None):
