@@ -695,15 +695,47 @@ BF16 = 1
 STATE_F32 = 0
 STATE_FP8 = 1
 FP8_BLOCK = 128
+FP8_MAX = 1 << 30
 
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _BYTES = (torch.uint8, torch.float8_e8m0fnu)
 _VALUES = (torch.float32,) + _BF16
 
+# The calls below are short on the GPU at decode sizes (a few microseconds), so
+# their marshalling is kept short too: tensors go through one check each, and
+# raw pointers, as ints, straight to ctypes.
+
+
+def _arg(t, dtypes, count, name):
+    """The pointer of a required contiguous device tensor of at least
+    ``count`` elements."""
+    if t is None or t.dtype not in dtypes or not t.is_cuda or not t.is_contiguous() or t.numel() < count:
+        _dev(t, dtypes, name)
+        _need(t, count, name)
+    return t.data_ptr()
+
+
+def _opt(t, dtypes, count, name):
+    """The same for an optional one: None stays None."""
+    return None if t is None else _arg(t, dtypes, count, name)
+
+
+def _raw_stream(stream):
+    """The HIP stream handle of ``stream``, by default the current device's
+    current stream."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
+
 
 def _value(t):
-    """The ngram_value of a tensor that _dev has checked against _VALUES."""
-    return F32 if t.dtype == torch.float32 else BF16
+    """The ngram_value of a tensor that has been checked against _VALUES."""
+    return F32 if t.dtype is torch.float32 else BF16
+
+
+def _matrix(t, name):
+    """(rows, columns) of a matrix argument."""
+    if t is None or t.dim() != 2:
+        raise NgramError(f"{name} must have two dimensions")
+    return t.shape
 
 
 class Fp8:
@@ -711,33 +743,32 @@ class Fp8:
     ``scales``, one byte per 128 columns of a row (``block_rows`` 1) or of 128
     rows (128); see "8-bit matrices" in ngram.h."""
 
+    __slots__ = ("codes", "scales", "rows", "cols", "block_rows", "c")
+
     def __init__(self, codes, scales, rows: int, cols: int, block_rows: int = 1):
-        self.rows, self.cols, self.block_rows = int(rows), int(cols), int(block_rows)
-        need_codes = lib().ngram_fp8_code_bytes(self.rows, self.cols)
-        need_scales = lib().ngram_fp8_scale_bytes(self.rows, self.cols, self.block_rows)
-        if need_codes < 0 or need_scales < 0:
-            raise NgramError(f"no 8-bit matrix has rows={rows}, cols={cols}, block_rows={block_rows}")
-        _dev(codes, _CODES, "codes")
-        _dev(scales, _BYTES, "scales")
-        _need(codes, need_codes, "codes")
-        _need(scales, need_scales, "scales")
+        ld, srows, sld = _fp8_shape(rows, cols, block_rows)
+        self.rows, self.cols, self.block_rows = rows, cols, block_rows
         self.codes, self.scales = codes, scales
-        self._c = _Fp8(codes.data_ptr(), scales.data_ptr(), self.rows, self.cols, self.block_rows, 0)
+        self.c = _Fp8(_arg(codes, _CODES, rows * ld, "codes"), _arg(scales, _BYTES, srows * sld, "scales"), rows, cols, block_rows, 0)
 
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda:0") -> "Fp8":
-        need = lib().ngram_fp8_code_bytes(int(rows), int(cols))
-        scale = lib().ngram_fp8_scale_bytes(int(rows), int(cols), int(block_rows))
-        if need < 0 or scale < 0:
-            raise NgramError(f"no 8-bit matrix has rows={rows}, cols={cols}, block_rows={block_rows}")
-        srows = int(rows) if block_rows == 1 else -(-int(rows) // FP8_BLOCK)
-        codes = torch.empty((int(rows), -(-int(cols) // FP8_BLOCK) * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=device)
-        scales = torch.empty((srows, scale // max(srows, 1)), dtype=torch.uint8, device=device)
-        return cls(codes, scales, rows, cols, block_rows)
+        ld, srows, sld = _fp8_shape(rows, cols, block_rows)
+        codes = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device)
+        scales = torch.empty((srows, sld), dtype=torch.uint8, device=device)
+        self = cls.__new__(cls)
+        self.rows, self.cols, self.block_rows, self.codes, self.scales = rows, cols, block_rows, codes, scales
+        self.c = _Fp8(codes.data_ptr(), scales.data_ptr(), rows, cols, block_rows, 0)
+        return self
 
-    @property
-    def c(self):
-        return ctypes.byref(self._c)
+
+def _fp8_shape(rows, cols, block_rows):
+    """(code bytes a row, scale rows, scale bytes a row), as
+    ngram_fp8_code_bytes and ngram_fp8_scale_bytes count them."""
+    if not (0 <= rows <= FP8_MAX and 0 <= cols <= FP8_MAX) or block_rows not in (1, FP8_BLOCK):
+        raise NgramError(f"no 8-bit matrix has rows={rows}, cols={cols}, block_rows={block_rows}")
+    nb = (cols + FP8_BLOCK - 1) // FP8_BLOCK
+    return nb * FP8_BLOCK, rows if block_rows == 1 else (rows + FP8_BLOCK - 1) // FP8_BLOCK, (nb + 3) // 4 * 4
 
 
 def _fp8_c(q):
@@ -748,15 +779,15 @@ def ngram_quant_fp8(x, rows=True, transposed=False, block_rows: int = 1, q=None,
     """x [n][d] (fp32 or bf16) in 8 bits: (q, qt), with None for the one that
     is not wanted.  ``rows``: q, n x d; ``transposed``: qt, d x n; or pass
     the Fp8 to fill.  See ngram_quant_fp8 in ngram.h."""
-    _dev(x, _VALUES, "x")
-    if x.dim() != 2:
-        raise NgramError("x must be [n][d]")
-    n, d = x.shape
+    n, d = _matrix(x, "x")
+    px = _arg(x, _VALUES, n * d, "x")
     if q is None and rows:
         q = Fp8.empty(n, d, block_rows, x.device)
     if qt is None and transposed:
         qt = Fp8.empty(d, n, block_rows, x.device)
-    _check(lib().ngram_quant_fp8(_ptr(x), _value(x), n, d, _fp8_c(q), _fp8_c(qt), _stream(stream)), "ngram_quant_fp8")
+    rc = lib().ngram_quant_fp8(px, _value(x), n, d, _fp8_c(q), _fp8_c(qt), _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_quant_fp8")
     return q, qt
 
 
@@ -774,32 +805,26 @@ def ngram_add_norm(x, gamma, eps, residual=None, sum_out=None, y_out=None, q_out
     pass (see ngram_add_norm in ngram.h).  ``sum_out`` receives s and may be
     ``residual``; q, y (bf16) and r = 1 / rms are made where ``quantise``,
     ``keep_y`` and ``keep_r`` ask for them or a buffer is passed."""
-    _dev(x, _VALUES, "x")
-    _dev(gamma, _F32, "gamma")
-    if x.dim() != 2:
-        raise NgramError("x must be [n][d]")
-    n, d = x.shape
+    n, d = _matrix(x, "x")
+    count = n * d
+    px = _arg(x, _VALUES, count, "x")
+    pg = _arg(gamma, _F32, d, "gamma")
     if q_out is None and quantise:
         q_out = Fp8.empty(n, d, 1, x.device)
     if y_out is None and keep_y:
         y_out = torch.empty((n, d), dtype=torch.bfloat16, device=x.device)
     if r_out is None and keep_r:
         r_out = torch.empty(n, dtype=torch.float32, device=x.device)
-    _dev(residual, _BF16, "residual", allow_none=True)
-    _dev(sum_out, _BF16, "sum_out", allow_none=True)
-    _dev(y_out, _BF16, "y_out", allow_none=True)
-    _dev(r_out, _F32, "r_out", allow_none=True)
-    _need(gamma, d, "gamma")
-    for t, name in ((residual, "residual"), (sum_out, "sum_out"), (y_out, "y_out")):
-        _need(t, n * d, name)
-    _need(r_out, n, "r_out")
-    _check(lib().ngram_add_norm(_ptr(x), _value(x), _ptr(residual), n, d, _ptr(gamma), float(eps), _ptr(sum_out),
-                                _ptr(y_out), _fp8_c(q_out), _ptr(r_out), _stream(stream)), "ngram_add_norm")
+    rc = lib().ngram_add_norm(px, _value(x), _opt(residual, _BF16, count, "residual"), n, d, pg, eps,
+                              _opt(sum_out, _BF16, count, "sum_out"), _opt(y_out, _BF16, count, "y_out"), _fp8_c(q_out),
+                              _opt(r_out, _F32, n, "r_out"), _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_add_norm")
     return NormOut(sum_out, y_out, q_out, r_out)
 
 
 def add_norm_grad_workspace(n: int, d: int, device="cuda:0"):
-    nbytes = int(lib().ngram_add_norm_grad_workspace_bytes(int(n), int(d)))
+    nbytes = lib().ngram_add_norm_grad_workspace_bytes(n, d)
     if nbytes < 0:
         raise NgramError(f"no norm gradient has n={n}, d={d}")
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
@@ -809,34 +834,25 @@ def ngram_add_norm_grad(dy, sum, r, gamma, dsum=None, dx_out=None, dgamma_out=No
     """(dx [n][d] bf16, dgamma [d] fp32) from dL/dy (fp32 or bf16) and the
     forward's sum and r; ``dsum`` is the gradient that reaches the sum along
     the residual stream (see ngram_add_norm_grad in ngram.h)."""
-    _dev(dy, _VALUES, "dy")
-    _dev(sum, _BF16, "sum")
-    _dev(r, _F32, "r")
-    _dev(gamma, _F32, "gamma")
-    _dev(dsum, _BF16, "dsum", allow_none=True)
-    if dy.dim() != 2:
-        raise NgramError("dy must be [n][d]")
-    n, d = dy.shape
+    n, d = _matrix(dy, "dy")
+    count = n * d
+    pdy = _arg(dy, _VALUES, count, "dy")
+    ps, pr, pg = _arg(sum, _BF16, count, "sum"), _arg(r, _F32, n, "r"), _arg(gamma, _F32, d, "gamma")
     dx_out = torch.empty((n, d), dtype=torch.bfloat16, device=dy.device) if dx_out is None else dx_out
     dgamma_out = torch.empty(d, dtype=torch.float32, device=dy.device) if dgamma_out is None else dgamma_out
-    _dev(dx_out, _BF16, "dx_out")
-    _dev(dgamma_out, _F32, "dgamma_out")
-    for t, name in ((sum, "sum"), (dsum, "dsum"), (dx_out, "dx_out")):
-        _need(t, n * d, name)
-    _need(r, n, "r")
-    _need(gamma, d, "gamma")
-    _need(dgamma_out, d, "dgamma_out")
     workspace = add_norm_grad_workspace(n, d, dy.device) if workspace is None else workspace
-    _check(lib().ngram_add_norm_grad(_ptr(dy), _value(dy), _ptr(sum), _ptr(r), _ptr(gamma), _ptr(dsum), n, d,
-                                     _ptr(dx_out), _ptr(dgamma_out), *_ws_args(workspace), _stream(stream)),
-           "ngram_add_norm_grad")
+    rc = lib().ngram_add_norm_grad(pdy, _value(dy), ps, pr, pg, _opt(dsum, _BF16, count, "dsum"), n, d,
+                                   _arg(dx_out, _BF16, count, "dx_out"), _arg(dgamma_out, _F32, d, "dgamma_out"),
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_add_norm_grad")
     return dx_out, dgamma_out
 
 
 def project_fp8_workspace(m: int, n: int, k: int, dtype=torch.float32, device="cuda:0"):
     """Workspace of ngram_project_fp8 for C [m][n] of ``dtype`` over k
     columns, or None where the call needs none."""
-    nbytes = int(lib().ngram_project_fp8_workspace_bytes(int(m), int(n), int(k), F32 if dtype == torch.float32 else BF16))
+    nbytes = lib().ngram_project_fp8_workspace_bytes(m, n, k, F32 if dtype is torch.float32 else BF16)
     if nbytes < 0:
         raise NgramError(f"no 8-bit product has m={m}, n={n}, k={k}")
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
@@ -845,43 +861,37 @@ def project_fp8_workspace(m: int, n: int, k: int, dtype=torch.float32, device="c
 def ngram_project_fp8(a: Fp8, b: Fp8, out=None, dtype=torch.bfloat16, workspace=None, stream=None):
     """out [a.rows][b.rows] (fp32 or bf16) = a b^T over their common columns
     (see ngram_project_fp8 in ngram.h)."""
+    m, n = a.rows, b.rows
     if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=dtype, device=a.codes.device)
-    _dev(out, _VALUES, "out")
-    _need(out, a.rows * b.rows, "out")
+        out = torch.empty((m, n), dtype=dtype, device=a.codes.device)
+    po = _arg(out, _VALUES, m * n, "out")
     if workspace is None:
-        workspace = project_fp8_workspace(a.rows, b.rows, a.cols, out.dtype, a.codes.device)
-    ws = (None, 0) if workspace is None else _ws_args(workspace)
-    _check(lib().ngram_project_fp8(a.c, b.c, _ptr(out), _value(out), *ws, _stream(stream)), "ngram_project_fp8")
+        workspace = project_fp8_workspace(m, n, a.cols, out.dtype, out.device)
+    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    rc = lib().ngram_project_fp8(a.c, b.c, po, _value(out), ws, ws_bytes, _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_project_fp8")
     return out
 
 
 def _step_c(step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed):
-    return _AdamWStep(float(lr), float(beta1), float(beta2), float(eps), float(weight_decay), float(grad_scale), int(step),
-                      int(seed) & 0xFFFFFFFFFFFFFFFF)
+    return _AdamWStep(lr, beta1, beta2, eps, weight_decay, grad_scale, step, seed & 0xFFFFFFFFFFFFFFFF)
 
 
-def _adamw_tensor(p, g, m, v, m_scale, v_scale, rng_offset, name, g_numel=None, scale_rows=None):
-    _dev(p, _VALUES, f"{name}: p")
-    _dev(g, _VALUES, f"{name}: g")
+def _adamw_tensor(p, g, m, v, m_scale, v_scale, rng_offset, name, g_numel=None, scale_bytes=None):
     n = p.numel()
-    _need(g, n if g_numel is None else g_numel, f"{name}: g")
-    if m.dtype == torch.float32:
+    pp = _arg(p, _VALUES, n, f"{name}: p")
+    pg = _arg(g, _VALUES, n if g_numel is None else g_numel, f"{name}: g")
+    if m.dtype is torch.float32:
         if m_scale is not None or v_scale is not None:
             raise NgramError(f"{name}: fp32 moments have no scales")
-        kinds, state = _F32, STATE_F32
+        kinds, state, pms, pvs = _F32, STATE_F32, None, None
     else:
         kinds, state = _CODES, STATE_FP8
-        need = -(-n // FP8_BLOCK) if scale_rows is None else scale_rows
-        for t, what in ((m_scale, "m_scale"), (v_scale, "v_scale")):
-            _dev(t, _BYTES, f"{name}: {what}")
-            _need(t, need, f"{name}: {what}")
-    for t, what in ((m, "m"), (v, "v")):
-        _dev(t, kinds, f"{name}: {what}")
-        _need(t, n, f"{name}: {what}")
-    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    return _AdamWTensor(at(p), at(g), at(m), at(v), at(m_scale), at(v_scale), n, int(rng_offset), _value(p), _value(g),
-                        state, 0)
+        need = -(-n // FP8_BLOCK) if scale_bytes is None else scale_bytes
+        pms, pvs = _arg(m_scale, _BYTES, need, f"{name}: m_scale"), _arg(v_scale, _BYTES, need, f"{name}: v_scale")
+    return _AdamWTensor(pp, pg, _arg(m, kinds, n, f"{name}: m"), _arg(v, kinds, n, f"{name}: v"), pms, pvs, n, rng_offset,
+                        _value(p), _value(g), state, 0)
 
 
 class AdamWTensors:
@@ -906,15 +916,17 @@ class AdamWTensors:
             raise NgramError("the lists must have one entry for each parameter")
         self.tensors = [tuple(x) for x in zip(*lists[:6])]
         self.count = count
-        self._c = (_AdamWTensor * max(count, 1))(*[_adamw_tensor(*x, name=f"tensor {i}") for i, x in enumerate(zip(*lists))])
+        self.c = (_AdamWTensor * max(count, 1))(*[_adamw_tensor(*x, name=f"tensor {i}") for i, x in enumerate(zip(*lists))])
 
 
 def ngram_adamw(tensors: AdamWTensors, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=1.0,
                 seed=0, stream=None):
     """One AdamW step on every tensor, in place; ``step`` counts from 1 (see
     ngram_adamw in ngram.h)."""
-    h = _step_c(step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed)
-    _check(lib().ngram_adamw(tensors._c, tensors.count, ctypes.byref(h), _stream(stream)), "ngram_adamw")
+    rc = lib().ngram_adamw(tensors.c, tensors.count, _step_c(step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed),
+                           _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_adamw")
 
 
 def ngram_adamw_rows(p, m, v, rows, g, n_rows=None, m_scale=None, v_scale=None, *, lr, step, beta1=0.9, beta2=0.999,
@@ -923,15 +935,11 @@ def ngram_adamw_rows(p, m, v, rows, g, n_rows=None, m_scale=None, v_scale=None, 
     gradient (rows, g [max_rows][d], n_rows [1] int64 on the device) that
     ngram_grad_table and ngram_grad_e1 return (see ngram_adamw_rows in
     ngram.h)."""
-    if p.dim() != 2:
-        raise NgramError("p must be [R][d]")
-    R, d = p.shape
-    _dev(rows, _I32T, "rows")
-    max_rows = rows.numel()
-    if n_rows is not None:
-        _dev(n_rows, (torch.int64,), "n_rows")
-        _need(n_rows, 1, "n_rows")
-    t = _adamw_tensor(p, g, m, v, m_scale, v_scale, 0, "table", g_numel=max_rows * d, scale_rows=R * -(-d // FP8_BLOCK))
-    h = _step_c(step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed)
-    _check(lib().ngram_adamw_rows(ctypes.byref(t), R, d, _ptr(rows), max_rows, _ptr(n_rows), ctypes.byref(h),
-                                  _stream(stream)), "ngram_adamw_rows")
+    R, d = _matrix(p, "p")
+    max_rows = 0 if rows is None else rows.numel()
+    pr, pn = _arg(rows, _I32T, 0, "rows"), _opt(n_rows, (torch.int64,), 1, "n_rows")
+    t = _adamw_tensor(p, g, m, v, m_scale, v_scale, 0, "table", g_numel=max_rows * d, scale_bytes=R * -(-d // FP8_BLOCK))
+    rc = lib().ngram_adamw_rows(t, R, d, pr, max_rows, pn, _step_c(step, lr, beta1, beta2, eps, weight_decay, grad_scale, seed),
+                                _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_adamw_rows")
