@@ -114,12 +114,13 @@ struct Raw8 {
 // without a finite nonzero value has e = 0.  Infinities and NaN become the
 // NaN code and do not count for e.
 
-// The largest |x| of x[0..7] as bits.
+// The largest |x| of x[0..7], NaN left out, as bits (v_max_f32 returns its
+// other operand where one is NaN).
 __device__ __forceinline__ uint32_t amax_bits(const float x[8]) {
-    uint32_t m = 0;
+    float m = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7FFFFFFFu);
-    return m;
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(x[k]));
+    return __float_as_uint(m);
 }
 // The same over finite values only.
 __device__ __forceinline__ uint32_t finite_amax_bits(const float x[8]) {
@@ -139,21 +140,19 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
 __device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }     // 2^e, e >= -126
 __device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254 - byte) << 23); }   // 2^-e
 // The scale byte of the lane's block of 128 (its group of 16 lanes, eight
-// elements each).  A block that holds an infinity or a NaN takes a second
-// look at its finite values; the wavefront branches only where one does.
+// elements each).  A block that holds an infinity takes a second look at
+// its finite values; the wavefront branches only where one does.
 __device__ __forceinline__ uint32_t block_scale16(const float x[8]) {
     uint32_t m = max16(amax_bits(x));
     if (__builtin_expect(__ballot(m >= kInfBits) != 0, 0)) m = max16(finite_amax_bits(x));
     return scale_byte(m);
 }
 // Four codes: E4M3 nearest-even of x * inv (exact scaling: inv is a power of
-// two).  Callers pass |x * inv| <= 448 for finite x.
-__device__ __forceinline__ float nan_if_inf(float x) {
-    return (__float_as_uint(x) & 0x7FFFFFFFu) == kInfBits ? __uint_as_float(0x7FC00000u) : x;
-}
+// two).  Callers pass |x * inv| <= 448 for finite x; the conversion gives the
+// NaN code for infinities and NaN.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float inv) {
-    int r = __builtin_amdgcn_cvt_pk_fp8_f32(nan_if_inf(a * inv), nan_if_inf(b * inv), 0, false);
-    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(nan_if_inf(c * inv), nan_if_inf(d * inv), r, true));
+    const int r = __builtin_amdgcn_cvt_pk_fp8_f32(a * inv, b * inv, 0, false);
+    return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c * inv, d * inv, r, true));
 }
 __device__ __forceinline__ void codes8_to_f32(u32x2 c, float v[8]) {
     typedef float f2 __attribute__((ext_vector_type(2)));

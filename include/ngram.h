@@ -498,7 +498,8 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
  * sqrt(v) by 0.05% where E4M3's neighbours lie 6 to 12% apart, and an
  * update of a bf16 parameter is often below half its last place.  So 8-bit moments and bf16
  * parameters round up or down at random, with the probabilities that make the
- * expected value exact, and a positive sqrt(v) never becomes zero.  The
+ * expected value exact, and a positive sqrt(v) never becomes zero (a v' below
+ * 2^-126 counts as zero).  The
  * random bits of element i are half (even i: low) of
  * splitmix64(key + (rng_offset + i) / 2), key = splitmix64(splitmix64(seed) +
  * step): m takes bits 0..19, sqrt(v) bits 12..31, p bits 8..23.  Equal inputs
@@ -528,7 +529,7 @@ typedef struct {
     double lr;
     double beta1;
     double beta2;
-    double eps;            /* > 0 */
+    double eps;            /* >= 2^-126 */
     double weight_decay;
     double grad_scale;     /* 1 to take gradients as they are */
     int64_t step;          /* from 1 */
