@@ -74,118 +74,121 @@ struct NormArgs {
 
 constexpr int kMaxWaves = 16;
 
+// A store past the caches' usual keeping (STREAM: outputs of many rows, which
+// are gone from L2 before anyone reads them; 106 -> 101 us at 32768 x 2560), or
+// a plain one.
+template <bool STREAM, typename V, typename P>
+__device__ __forceinline__ void put(P* to, V v) {
+    if (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<V*>(to));
+    else *reinterpret_cast<V*>(to) = v;
+}
+
 template <int C, bool F32, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_kernel(const NormArgs a) {
-    __shared__ float part[2][kMaxWaves];
+    __shared__ float part[kMaxWaves];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
     const int c0 = WIDE ? wave * C : 0;
-    int64_t row = WIDE ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * waves + wave;
-    const int64_t stride = WIDE ? gridDim.x : static_cast<int64_t>(gridDim.x) * waves;
-    float gam[C][8];
+    const int64_t row = WIDE ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * waves + wave;
+    if (row >= a.n) return;
+    Raw8<true> gam[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int col = (c0 + c) * kSlice + lane * kVec;
-        Raw8<true> g;
-        if (col < a.d) g.load(a.gamma, col); else g.zero();
-        g.get(gam[c]);
+        if (col < a.d) gam[c].load(a.gamma, col); else gam[c].zero();
     }
-    for (int it = 0; row < a.n; row += stride, ++it) {
-        Raw8<F32> x[C];
-        Raw8<false> res[C];
-        const int64_t at = row * a.d;
+    Raw8<F32> x[C];
+    Raw8<false> res[C];
+    const int64_t at = row * a.d;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int col = (c0 + c) * kSlice + lane * kVec;
-            if (col < a.d) {
-                x[c].load(a.x, at + col);
-                if (a.residual) res[c].load(a.residual, at + col); else res[c].zero();
-            } else {
-                x[c].zero();
-                res[c].zero();
-            }
+    for (int c = 0; c < C; ++c) {
+        const int col = (c0 + c) * kSlice + lane * kVec;
+        if (col < a.d) {
+            x[c].load(a.x, at + col);
+            if (a.residual) res[c].load(a.residual, at + col); else res[c].zero();
+        } else {
+            x[c].zero();
+            res[c].zero();
         }
-        float s[C][8];
-        float total = 0.0f;
+    }
+    float s[C][8];
+    float total = 0.0f;
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int col = (c0 + c) * kSlice + lane * kVec;
-            float u[8], v[8];
-            x[c].get(u);
-            res[c].get(v);
+    for (int c = 0; c < C; ++c) {
+        const int col = (c0 + c) * kSlice + lane * kVec;
+        float u[8], v[8];
+        x[c].get(u);
+        res[c].get(v);
+        u32x4 packed;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) packed[k] = bf16_pair(u[2 * k] + v[2 * k], u[2 * k + 1] + v[2 * k + 1]);
+        // the norm reads the rounded sum, so that the backward, which has
+        // only the stored sum, differentiates what was computed
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            s[c][2 * k] = bf16_lo(packed[k]);
+            s[c][2 * k + 1] = bf16_hi(packed[k]);
+        }
+        if (a.sum_out && col < a.d) put<!WIDE>(a.sum_out + at + col, packed);
+        float t = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t = fmaf(s[c][k], s[c][k], t);
+        total += t;
+    }
+    total = wave_sum(total);
+    if (WIDE) {
+        if (lane == 0) part[wave] = total;
+        __syncthreads();
+        total = 0.0f;
+        for (int w = 0; w < waves; ++w) total += part[w];
+    }
+    const float r = 1.0f / sqrtf(total * a.inv_d + a.eps);
+    if (a.r_out && lane == 0 && wave == (WIDE ? 0 : wave)) a.r_out[row] = r;
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int col = (c0 + c) * kSlice + lane * kVec;
+        float y[8], gv[8];
+        gam[c].get(gv);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] = s[c][k] * r * gv[k];
+        if (a.y_out && col < a.d) {
             u32x4 packed;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) packed[k] = bf16_pair(u[2 * k] + v[2 * k], u[2 * k + 1] + v[2 * k + 1]);
-            // the norm reads the rounded sum, so that the backward, which has
-            // only the stored sum, differentiates what was computed
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                s[c][2 * k] = bf16_lo(packed[k]);
-                s[c][2 * k + 1] = bf16_hi(packed[k]);
-            }
-            if (a.sum_out && col < a.d) *reinterpret_cast<u32x4*>(a.sum_out + at + col) = packed;
-            float t = 0.0f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) t = fmaf(s[c][k], s[c][k], t);
-            total += t;
+            for (int k = 0; k < 4; ++k) packed[k] = bf16_pair(y[2 * k], y[2 * k + 1]);
+            put<!WIDE>(a.y_out + at + col, packed);
         }
-        total = wave_sum(total);
-        if (WIDE) {
-            // two buffers in turn: a wavefront writes one while a slower one
-            // still reads the other, so one barrier a row is enough
-            float* const p = part[it & 1];
-            if (lane == 0) p[wave] = total;
-            __syncthreads();
-            total = 0.0f;
-            for (int w = 0; w < waves; ++w) total += p[w];
-        }
-        const float r = 1.0f / sqrtf(total * a.inv_d + a.eps);
-        if (a.r_out && lane == 0 && wave == (WIDE ? 0 : wave)) a.r_out[row] = r;
-        uint32_t bytes = 0;
+        if (a.codes) {
+            if (col >= a.d) {       // past the row: zero codes, also where r is not finite
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int col = (c0 + c) * kSlice + lane * kVec;
-            float y[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = s[c][k] * r * gam[c][k];
-            if (a.y_out && col < a.d) {
-                u32x4 packed;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) packed[k] = bf16_pair(y[2 * k], y[2 * k + 1]);
-                *reinterpret_cast<u32x4*>(a.y_out + at + col) = packed;
+                for (int k = 0; k < 8; ++k) y[k] = 0.0f;
             }
-            if (a.codes) {
-                if (col >= a.d) {       // past the row: zero codes, also where r is not finite
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] = 0.0f;
-                }
-                const uint32_t byte = block_scale16(y);
-                const float inv = inverse_scale(byte);
-                if (col < a.ld) {
-                    u32x2 q;
-                    q[0] = codes4(y[0], y[1], y[2], y[3], inv);
-                    q[1] = codes4(y[4], y[5], y[6], y[7], inv);
-                    *reinterpret_cast<u32x2*>(a.codes + row * a.ld + col) = q;
-                }
-                const uint32_t b0 = __builtin_amdgcn_readlane(byte, 0), b1 = __builtin_amdgcn_readlane(byte, 16);
-                const uint32_t b2 = __builtin_amdgcn_readlane(byte, 32), b3 = __builtin_amdgcn_readlane(byte, 48);
-                const uint32_t word = b0 | b1 << 8 | b2 << 16 | b3 << 24;
-                bytes = lane == c ? word : bytes;
+            const uint32_t byte = block_scale16(y);
+            const float inv = inverse_scale(byte);
+            if (col < a.ld) {
+                u32x2 q;
+                q[0] = codes4(y[0], y[1], y[2], y[3], inv);
+                q[1] = codes4(y[4], y[5], y[6], y[7], inv);
+                put<!WIDE>(a.codes + row * a.ld + col, q);
             }
+            const uint32_t b0 = __builtin_amdgcn_readlane(byte, 0), b1 = __builtin_amdgcn_readlane(byte, 16);
+            const uint32_t b2 = __builtin_amdgcn_readlane(byte, 32), b3 = __builtin_amdgcn_readlane(byte, 48);
+            const uint32_t word = b0 | b1 << 8 | b2 << 16 | b3 << 24;
+            bytes = lane == c ? word : bytes;
         }
-        // chunk c's four scale bytes sit in lane c
-        if (a.codes && lane < C && (c0 + lane) * 4 < a.sld)
-            *reinterpret_cast<uint32_t*>(a.scales + row * a.sld + (c0 + lane) * 4) = bytes;
     }
+    // chunk c's four scale bytes sit in lane c
+    if (a.codes && lane < C && (c0 + lane) * 4 < a.sld)
+        *reinterpret_cast<uint32_t*>(a.scales + row * a.sld + (c0 + lane) * 4) = bytes;
 }
 
 // ---------------------------------------------------------------------------
 // Gradients of the norm: with h = gamma dy,
 //   dx = r h - s (r^3 / d) sum(h s) + dsum,   dgamma = sum over rows of dy s r.
-// The same walk over rows; a wavefront adds its rows' dgamma terms in
-// registers, a workgroup its wavefronts' in LDS, and one row of partial sums
-// per workgroup goes to the workspace for the kernel below.
+// A workgroup walks over rows, its wavefronts sharing each as in the wide
+// forward; a lane adds its columns' dgamma terms in registers, and one row of
+// partial sums per workgroup goes to the workspace for the kernel below.
 struct NormGradArgs {
     const void* dy;
     const uint16_t* sum;
@@ -199,16 +202,13 @@ struct NormGradArgs {
     float inv_d;
 };
 
-template <int C, bool F32, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_grad_kernel(const NormGradArgs a) {
+template <int C, bool F32>
+__global__ void __launch_bounds__(64 * kMaxWaves) add_norm_grad_kernel(const NormGradArgs a) {
     __shared__ float part[2][kMaxWaves];
-    extern __shared__ __attribute__((aligned(16))) float sums[];      // not WIDE: [waves][C * 512]
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6;
-    const int c0 = WIDE ? wave * C : 0;
-    int64_t row = WIDE ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * waves + wave;
-    const int64_t stride = WIDE ? gridDim.x : static_cast<int64_t>(gridDim.x) * waves;
+    const int c0 = wave * C;
     float gam[C][8], acc[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_grad_ker
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[c][k] = 0.0f;
     }
-    for (int it = 0; row < a.n; row += stride, ++it) {
+    int it = 0;
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, ++it) {
         Raw8<F32> dy[C];
         Raw8<false> s[C], ds[C];
         const int64_t at = row * a.d;
@@ -252,13 +253,13 @@ __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_grad_ker
             dot += t;
         }
         dot = wave_sum(dot);
-        if (WIDE) {
-            float* const p = part[it & 1];
-            if (lane == 0) p[wave] = dot;
-            __syncthreads();
-            dot = 0.0f;
-            for (int w = 0; w < waves; ++w) dot += p[w];
-        }
+        // two buffers in turn: a wavefront writes one while a slower one
+        // still reads the other, so one barrier a row is enough
+        float* const p = part[it & 1];
+        if (lane == 0) p[wave] = dot;
+        __syncthreads();
+        dot = 0.0f;
+        for (int w = 0; w < waves; ++w) dot += p[w];
         const float f = dot * r * r * r * a.inv_d;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -278,32 +279,17 @@ __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_grad_ker
                 }
                 packed[k] = bf16_pair(o[0], o[1]);
             }
-            if (col < a.d) *reinterpret_cast<u32x4*>(a.dx + at + col) = packed;
+            if (col < a.d) put<true>(a.dx + at + col, packed);
         }
     }
     float* const out = a.partial + static_cast<int64_t>(blockIdx.x) * a.d;
-    if (WIDE) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int col = (c0 + c) * kSlice + lane * kVec;
-            if (col < a.d) {
-                *reinterpret_cast<f32x4*>(out + col) = f32x4{acc[c][0], acc[c][1], acc[c][2], acc[c][3]};
-                *reinterpret_cast<f32x4*>(out + col + 4) = f32x4{acc[c][4], acc[c][5], acc[c][6], acc[c][7]};
-            }
-        }
-        return;
-    }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        float* const p = sums + wave * (C * kSlice) + c * kSlice + lane * kVec;
-        *reinterpret_cast<f32x4*>(p) = f32x4{acc[c][0], acc[c][1], acc[c][2], acc[c][3]};
-        *reinterpret_cast<f32x4*>(p + 4) = f32x4{acc[c][4], acc[c][5], acc[c][6], acc[c][7]};
-    }
-    __syncthreads();
-    for (int col = threadIdx.x; col < a.d; col += blockDim.x) {
-        float t = 0.0f;
-        for (int w = 0; w < waves; ++w) t += sums[w * (C * kSlice) + col];
-        out[col] = t;
+        const int col = (c0 + c) * kSlice + lane * kVec;
+        if (col < a.d) {
+            *reinterpret_cast<f32x4*>(out + col) = f32x4{acc[c][0], acc[c][1], acc[c][2], acc[c][3]};
+            *reinterpret_cast<f32x4*>(out + col + 4) = f32x4{acc[c][4], acc[c][5], acc[c][6], acc[c][7]};
+        }
     }
 }
 
@@ -456,10 +442,10 @@ __global__ void __launch_bounds__(256) quant_kernel(const QuantArgs a) {
 // ---------------------------------------------------------------------------
 // Launch shapes.
 
-// Chunks per wavefront and wavefronts per row.  Many rows: a wavefront takes
-// a whole row of up to 5 chunks (gamma and the row stay in registers), wider
-// rows are shared.  Few rows: one chunk per wavefront, so that a row's loads
-// are all in flight at once on as many wavefronts as there are chunks.
+// Forward.  Many rows: a wavefront takes a whole row of up to 5 chunks, wider
+// rows are shared by wavefronts of 4 chunks.  Few rows: one chunk per
+// wavefront, so that a row's loads are all in flight at once on as many
+// wavefronts as there are chunks.
 struct RowShape {
     int chunks;     // per wavefront
     int waves;      // per workgroup
@@ -467,22 +453,36 @@ struct RowShape {
     int64_t grid;
 };
 
-RowShape row_shape(int64_t n, int d, int64_t max_grid, int wide_chunks) {
+RowShape row_shape(int64_t n, int d) {
     const int total = (d + kSlice - 1) / kSlice;
     RowShape s;
-    if (n >= 2048 && total <= 5) {
+    s.wide = n < 2048 || total > 5;
+    if (!s.wide) {
         s.chunks = total;
         s.waves = 4;
-        s.wide = false;
-        s.grid = std::min<int64_t>((n + 3) / 4, max_grid);
+        s.grid = (n + 3) / 4;
     } else {
-        const int want = n >= 2048 ? wide_chunks : 1;
+        const int want = n < 2048 ? 1 : 4;
         s.waves = std::min(kMaxWaves, (total + want - 1) / want);
         s.chunks = (total + s.waves - 1) / s.waves;
         s.waves = (total + s.chunks - 1) / s.chunks;
-        s.wide = true;
-        s.grid = std::min<int64_t>(n, max_grid);
+        s.grid = n;
     }
+    return s;
+}
+
+// Gradient.  A row by a workgroup, one chunk per wavefront up to 16: at 32768
+// x 2560, 119 us against 128 with two chunks and 132 with a wavefront to a
+// row (fewer registers, more wavefronts).  512 workgroups walk over the rows (1024: 132
+// us: more partial sums; 256: slower in every shape).
+RowShape grad_shape(int64_t n, int d) {
+    const int total = (d + kSlice - 1) / kSlice;
+    RowShape s;
+    s.wide = true;
+    s.waves = std::min(kMaxWaves, total);
+    s.chunks = (total + s.waves - 1) / s.waves;
+    s.waves = (total + s.chunks - 1) / s.chunks;
+    s.grid = std::max<int64_t>(1, std::min<int64_t>(n, 512));   // no rows: one workgroup writes a row of zeros
     return s;
 }
 
@@ -494,16 +494,12 @@ void launch_norm(int chunks, dim3 grid, dim3 block, hipStream_t st, const NormAr
 #undef NG8_CASE
 }
 
-template <bool F32, bool WIDE>
-void launch_norm_grad(int chunks, dim3 grid, dim3 block, size_t lds, hipStream_t st, const NormGradArgs& a) {
-#define NG8_CASE(C) case C: hipLaunchKernelGGL((add_norm_grad_kernel<C, F32, WIDE>), grid, block, lds, st, a); break
-    switch (chunks) { NG8_CASE(1); NG8_CASE(2); NG8_CASE(3); NG8_CASE(4); NG8_CASE(5); default:
-        if constexpr (WIDE) switch (chunks) { NG8_CASE(6); NG8_CASE(7); default: NG8_CASE(8); } }
+template <bool F32>
+void launch_norm_grad(int chunks, dim3 grid, dim3 block, hipStream_t st, const NormGradArgs& a) {
+#define NG8_CASE(C) case C: hipLaunchKernelGGL((add_norm_grad_kernel<C, F32>), grid, block, 0, st, a); break
+    switch (chunks) { NG8_CASE(1); NG8_CASE(2); NG8_CASE(3); NG8_CASE(4); NG8_CASE(5); NG8_CASE(6); NG8_CASE(7); default: NG8_CASE(8); }
 #undef NG8_CASE
 }
-
-constexpr int64_t kNormGrid = 2048;         // 256 compute units x 8 workgroups of 4 wavefronts
-constexpr int64_t kNormGradGrid = 512;      // rows of partial sums
 
 int check_rows(int64_t n, int32_t d) {
     if (n < 0) return fail(NGRAM_EINVAL, "n=%lld is negative", (long long)n);
@@ -518,7 +514,6 @@ int check_value(int dtype, const char* what) {
     return NGRAM_OK;
 }
 
-int64_t norm_grad_grid(int64_t n, int d) { return std::max<int64_t>(1, row_shape(n, d, kNormGradGrid, 2).grid); }
 
 }  // namespace
 }  // namespace ng8
@@ -567,7 +562,7 @@ int ngram_add_norm(const void* x, int32_t x_dtype, const uint16_t* residual, int
     a.sld = static_cast<int32_t>(scale_ld(d));
     a.eps = eps;
     a.inv_d = 1.0f / static_cast<float>(d);
-    const RowShape s = row_shape(n, d, kNormGrid, 4);
+    const RowShape s = row_shape(n, d);
     const dim3 grid(static_cast<unsigned>(s.grid)), block(64 * s.waves);
     if (x_dtype == NGRAM_F32) {
         if (s.wide) launch_norm<true, true>(s.chunks, grid, block, stream, a);
@@ -581,7 +576,7 @@ int ngram_add_norm(const void* x, int32_t x_dtype, const uint16_t* residual, int
 
 int64_t ngram_add_norm_grad_workspace_bytes(int64_t n, int32_t d) {
     if (n < 0 || n > NGRAM_FP8_MAX || d <= 0 || d % kVec != 0 || d > NGRAM_MAX_D) return -1;
-    return norm_grad_grid(n, d) * d * 4;
+    return grad_shape(n, d).grid * d * 4;
 }
 
 int ngram_add_norm_grad(const void* dy, int32_t dy_dtype, const uint16_t* sum, const float* r, const float* gamma,
@@ -604,17 +599,10 @@ int ngram_add_norm_grad(const void* dy, int32_t dy_dtype, const uint16_t* sum, c
     a.partial = static_cast<float*>(workspace);
     a.n = n; a.d = d;
     a.inv_d = 1.0f / static_cast<float>(d);
-    RowShape s = row_shape(n, d, kNormGradGrid, 2);
-    s.grid = norm_grad_grid(n, d);      // no rows: one workgroup writes a row of zeros
+    const RowShape s = grad_shape(n, d);
     const dim3 grid(static_cast<unsigned>(s.grid)), block(64 * s.waves);
-    const size_t lds = s.wide ? 0 : static_cast<size_t>(s.waves) * s.chunks * kSlice * 4;
-    if (dy_dtype == NGRAM_F32) {
-        if (s.wide) launch_norm_grad<true, true>(s.chunks, grid, block, lds, stream, a);
-        else launch_norm_grad<true, false>(s.chunks, grid, block, lds, stream, a);
-    } else {
-        if (s.wide) launch_norm_grad<false, true>(s.chunks, grid, block, lds, stream, a);
-        else launch_norm_grad<false, false>(s.chunks, grid, block, lds, stream, a);
-    }
+    if (dy_dtype == NGRAM_F32) launch_norm_grad<true>(s.chunks, grid, block, stream, a);
+    else launch_norm_grad<false>(s.chunks, grid, block, stream, a);
     hipLaunchKernelGGL(column_sum_kernel, dim3((d + 63) / 64), dim3(1024), 0, stream, a.partial,
                        static_cast<int>(s.grid), d, dgamma_out);
     return hip_status("ngram_add_norm_grad launch");
