@@ -93,6 +93,10 @@ struct Raw8 {
         }
     }
     __device__ __forceinline__ void zero() { a = u32x4{0, 0, 0, 0}; b = u32x4{0, 0, 0, 0}; }
+    __device__ __forceinline__ float at(int k) const {      // k a constant once unrolled
+        if (F32) return __uint_as_float(k < 4 ? a[k & 3] : b[k & 3]);
+        return k & 1 ? bf16_hi(a[k >> 1]) : bf16_lo(a[k >> 1]);
+    }
     __device__ __forceinline__ void get(float v[8]) const {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {

@@ -335,46 +335,48 @@ struct QuantArgs {
 };
 
 template <bool F32>
-__global__ void __launch_bounds__(256) quant_kernel(const QuantArgs a) {
-    __shared__ uint32_t cmax[4][128];
-    __shared__ __attribute__((aligned(16))) uint8_t codes[128 * 144];   // [column][128 rows + 16]: 16-byte rows that start on shifting banks
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(F32 ? 4 : 6))) quant_kernel(const QuantArgs a) {
+    __shared__ u32x4 cmax[4][32];
+    __shared__ __attribute__((aligned(16))) uint8_t codes[128 * 128];   // transposed
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     const int tr = t >> 4, tc = t & 15;
     const int64_t tile_r = blockIdx.x / a.tiles_d;
     const int tile_c = blockIdx.x - tile_r * a.tiles_d;
     const int64_t r0 = tile_r * 128 + 8 * tr;
     const int c0 = tile_c * 128 + 8 * tc;
-    float x[8][8];
-    {
-        Raw8<F32> raw[8];
+    // kept as loaded and unpacked where used: fewer registers, more tiles in flight
+    Raw8<F32> raw[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (r0 + i < a.n && c0 < a.d) raw[i].load(a.x, (r0 + i) * a.d + c0); else raw[i].zero();
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) raw[i].get(x[i]);
+    for (int i = 0; i < 8; ++i) {
+        if (r0 + i < a.n && c0 < a.d) raw[i].load(a.x, (r0 + i) * a.d + c0); else raw[i].zero();
     }
     uint32_t tile_byte = 0;
     if (a.tile_scale) {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, finite_amax_bits(x[i]));
+        for (int i = 0; i < 8; ++i) {
+            float x[8];
+            raw[i].get(x);
+            m = max(m, finite_amax_bits(x));
+        }
         m = max16(m);
         m = max(max(__builtin_amdgcn_readlane(m, 0), __builtin_amdgcn_readlane(m, 16)),
                 max(__builtin_amdgcn_readlane(m, 32), __builtin_amdgcn_readlane(m, 48)));
-        if (lane == 0) cmax[wave][0] = m;
+        if (lane == 0) cmax[wave][0][0] = m;
         __syncthreads();
-        tile_byte = scale_byte(max(max(cmax[0][0], cmax[1][0]), max(cmax[2][0], cmax[3][0])));
+        tile_byte = scale_byte(max(max(cmax[0][0][0], cmax[1][0][0]), max(cmax[2][0][0], cmax[3][0][0])));
     }
     if (a.q) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t byte = a.tile_scale ? tile_byte : block_scale16(x[i]);
+            float x[8];
+            raw[i].get(x);
+            const uint32_t byte = a.tile_scale ? tile_byte : block_scale16(x);
             const float inv = inverse_scale(byte);
             if (r0 + i < a.n) {
                 u32x2 c;
-                c[0] = codes4(x[i][0], x[i][1], x[i][2], x[i][3], inv);
-                c[1] = codes4(x[i][4], x[i][5], x[i][6], x[i][7], inv);
+                c[0] = codes4(x[0], x[1], x[2], x[3], inv);
+                c[1] = codes4(x[4], x[5], x[6], x[7], inv);
                 *reinterpret_cast<u32x2*>(a.q + (r0 + i) * a.q_ld + c0) = c;
                 if (!a.tile_scale && tc == 0) a.qs[(r0 + i) * a.q_sld + tile_c] = static_cast<uint8_t>(byte);
                 if (!a.tile_scale && tile_c == a.tiles_d - 1 && tc > 0 && tile_c + tc < a.q_sld)
@@ -391,23 +393,34 @@ __global__ void __launch_bounds__(256) quant_kernel(const QuantArgs a) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) byte[k] = tile_byte;
     } else {
+        uint32_t m[8] = {};
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            uint32_t m = 0;
+        for (int i = 0; i < 8; ++i) {
+            float x[8];
+            raw[i].get(x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t u = __float_as_uint(x[i][k]) & 0x7FFFFFFFu;
-                m = max(m, u < kInfBits ? u : 0u);
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t u = __float_as_uint(x[k]) & 0x7FFFFFFFu;
+                m[k] = max(m[k], u < kInfBits ? u : 0u);
             }
-            m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 16)));
-            m = max(m, static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), 32)));
-            if (lane < 16) cmax[wave][8 * tc + k] = m;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {       // over the wavefront's four groups of 16 lanes
+            const auto p = __builtin_amdgcn_permlane16_swap(m[k], m[k], false, false);
+            m[k] = max(p[0], p[1]);
+            const auto q = __builtin_amdgcn_permlane32_swap(m[k], m[k], false, false);
+            m[k] = max(q[0], q[1]);
+        }
+        if (lane < 16) {
+            cmax[wave][2 * tc] = u32x4{m[0], m[1], m[2], m[3]};
+            cmax[wave][2 * tc + 1] = u32x4{m[4], m[5], m[6], m[7]};
         }
         __syncthreads();
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int c = 8 * tc + k;
-            byte[k] = scale_byte(max(max(cmax[0][c], cmax[1][c]), max(cmax[2][c], cmax[3][c])));
+        for (int h = 0; h < 2; ++h) {
+            const u32x4 w0 = cmax[0][2 * tc + h], w1 = cmax[1][2 * tc + h], w2 = cmax[2][2 * tc + h], w3 = cmax[3][2 * tc + h];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) byte[4 * h + k] = scale_byte(max(max(w0[k], w1[k]), max(w2[k], w3[k])));
         }
     }
     const int64_t last_r = (a.n - 1) / 128;
@@ -415,9 +428,11 @@ __global__ void __launch_bounds__(256) quant_kernel(const QuantArgs a) {
     for (int k = 0; k < 8; ++k) {
         const float inv = inverse_scale(byte[k]);
         u32x2 c;
-        c[0] = codes4(x[0][k], x[1][k], x[2][k], x[3][k], inv);
-        c[1] = codes4(x[4][k], x[5][k], x[6][k], x[7][k], inv);
-        *reinterpret_cast<u32x2*>(codes + (8 * tc + k) * 144 + 8 * tr) = c;
+        c[0] = codes4(raw[0].at(k), raw[1].at(k), raw[2].at(k), raw[3].at(k), inv);
+        c[1] = codes4(raw[4].at(k), raw[5].at(k), raw[6].at(k), raw[7].at(k), inv);
+        // column 8 tc + k, rows 8 tr .. +7: 8-byte unit tr ^ tc of LDS row
+        // (8 tc + k) ^ (tc & 1), so that a store's 64 lanes spread over all banks
+        *reinterpret_cast<u32x2*>(codes + ((8 * tc + k) ^ (tc & 1)) * 128 + 8 * (tr ^ tc)) = c;
         if (c0 + k < a.d && !a.tile_scale) {
             if (tr == 0) a.qts[static_cast<int64_t>(c0 + k) * a.qt_sld + tile_r] = static_cast<uint8_t>(byte[k]);
             if (tile_r == last_r && tr > 0 && tile_r + tr < a.qt_sld)
@@ -433,9 +448,10 @@ __global__ void __launch_bounds__(256) quant_kernel(const QuantArgs a) {
     for (int i = 0; i < 4; ++i) {
         const int c = 32 * i + (t >> 3), part = t & 7;      // a column's 128 bytes by eight lanes
         const int64_t col = static_cast<int64_t>(tile_c) * 128 + c;
+        const int from = c >> 3;                            // the column's tc
+        const u32x4 v = *reinterpret_cast<const u32x4*>(codes + (c ^ (from & 1)) * 128 + 16 * (part ^ (from >> 1)));
         if (col < a.d)
-            *reinterpret_cast<u32x4*>(a.qt + col * a.qt_ld + tile_r * 128 + 16 * part) =
-                *reinterpret_cast<const u32x4*>(codes + c * 144 + 16 * part);
+            *reinterpret_cast<u32x4*>(a.qt + col * a.qt_ld + tile_r * 128 + 16 * part) = from & 1 ? u32x4{v[2], v[3], v[0], v[1]} : v;
     }
 }
 

@@ -556,18 +556,21 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const float* __restrict_
 
 // ---------------------------------------------------------------------------
 // Few rows of A (decode): bound by the one read of B.  A workgroup owns 16
-// rows of B; its eight wavefronts take every eighth step of K with operands
+// rows of B; its 16 wavefronts take every 16th step of K with operands
 // straight from global memory (B is read once, A stays in L2), and join their
 // accumulators in LDS.  The matrix cores have time to spare here, so both
-// result types take the exact instruction.
+// result types take the exact instruction.  4 x 2560 x 2560: 4.0 us (8
+// wavefronts 4.9; four steps' loads ahead 5.0, for want of wavefronts), of
+// which an empty launch is about 2.5; 8 x 8192 x 8192: 16.5 us, 4.1 TB/s.
+constexpr int kRowWaves = 16;
+
 template <int MT, bool F32>
-__global__ void __launch_bounds__(512) project_fp8_rows_kernel(const ProjArgs a) {
-    __shared__ f32x4 part[8][MT][64];
+__global__ void __launch_bounds__(64 * kRowWaves) project_fp8_rows_kernel(const ProjArgs a) {
+    __shared__ f32x4 part[kRowWaves][MT][64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * (16 * MT);
     const int64_t br = min(n0 + lr, a.n - 1);
     const uint8_t* const bp = a.b + br * a.ld + 32 * (lane >> 4);
     const uint8_t* const bsp = a.bs + (br >> a.bsh) * a.sld;
@@ -575,15 +578,15 @@ __global__ void __launch_bounds__(512) project_fp8_rows_kernel(const ProjArgs a)
     const uint8_t* asp[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-        const int64_t ar = min(m0 + 16 * t + lr, a.m - 1);
+        const int64_t ar = min(static_cast<int64_t>(16 * t + lr), a.m - 1);
         ap[t] = a.a + ar * a.ld + 32 * (lane >> 4);
         asp[t] = a.as + (ar >> a.ash) * a.sld;
     }
     f32x4 acc[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int kb = wave; kb < a.steps; kb += 8) {
+#pragma unroll 2
+    for (int kb = wave; kb < a.steps; kb += kRowWaves) {
         const u32x4* const p = reinterpret_cast<const u32x4*>(bp + static_cast<int64_t>(kb) * kStep);
         const Wide fb = widen(join(p[0], p[1]), bsp[kb]);
 #pragma unroll
@@ -595,11 +598,11 @@ __global__ void __launch_bounds__(512) project_fp8_rows_kernel(const ProjArgs a)
 #pragma unroll
     for (int t = 0; t < MT; ++t) part[wave][t][lane] = acc[t];
     __syncthreads();
-    for (int t = wave; t < MT; t += 8) {
+    for (int t = wave; t < MT; t += kRowWaves) {
         f32x4 v = part[0][t][lane];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) v += part[w][t][lane];
-        const int64_t row = m0 + 16 * t + lr, col = n0 + 4 * (lane >> 4);
+        for (int w = 1; w < kRowWaves; ++w) v += part[w][t][lane];
+        const int64_t row = 16 * t + lr, col = n0 + 4 * (lane >> 4);
         if (row < a.m && col < a.n) store4<F32>(a.c, row * a.n + col, v);
     }
 }
@@ -613,7 +616,7 @@ struct Plan {
 };
 
 constexpr int kUnits = 256;     // compute units
-constexpr int64_t kRows = 64;   // most rows of A for the few-rows kernel
+constexpr int64_t kRows = 32;   // most rows of A for the few-rows kernel (64 rows: 8.6 us against the small tile's 7.3)
 
 // The tile kernels run one workgroup per compute unit, so a product takes
 // ceil(items / 256) rounds of one item's time, and an item's time is nearly a fixed
@@ -679,7 +682,7 @@ int launch_small(ProjArgs& a, hipStream_t st) {
 
 template <int MT>
 void launch_rows(const ProjArgs& a, bool f32, hipStream_t st) {
-    const dim3 grid(static_cast<unsigned>((a.n + 15) / 16), static_cast<unsigned>((a.m + 16 * MT - 1) / (16 * MT))), block(512);
+    const dim3 grid(static_cast<unsigned>((a.n + 15) / 16)), block(64 * kRowWaves);
     if (f32) hipLaunchKernelGGL((project_fp8_rows_kernel<MT, true>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((project_fp8_rows_kernel<MT, false>), grid, block, 0, st, a);
 }
@@ -736,10 +739,8 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
     a.ntiles_n = a.ntiles = a.band = a.stride = 0;
     rc = NGRAM_OK;
     if (p.kind == 0) {
-        if ((a.n + 15) / 16 > INT32_MAX) return fail(NGRAM_ERANGE, "B too large for one launch");
         if (a.m <= 16) launch_rows<1>(a, f32, stream);
-        else if (a.m <= 32) launch_rows<2>(a, f32, stream);
-        else launch_rows<4>(a, f32, stream);
+        else launch_rows<2>(a, f32, stream);
     } else if (p.kind == 1) {
         rc = f32 ? launch_small<SmallTile<2, 2, 2, 2, 4, true>>(a, stream) : launch_small<SmallTile<2, 2, 2, 2, 4, false>>(a, stream);
     } else if (p.kind == 2) {
