@@ -726,6 +726,14 @@ def _raw_stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
+def _made(t, stream):
+    """A tensor that a call makes for itself or for its caller: the allocator
+    is told of a stream other than the current one that it is used on."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _value(t):
     """The ngram_value of a tensor that has been checked against _VALUES."""
     return F32 if t.dtype is torch.float32 else BF16
@@ -752,10 +760,10 @@ class Fp8:
         self.c = _Fp8(_arg(codes, _CODES, rows * ld, "codes"), _arg(scales, _BYTES, srows * sld, "scales"), rows, cols, block_rows, 0)
 
     @classmethod
-    def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda:0") -> "Fp8":
+    def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda:0", stream=None) -> "Fp8":
         ld, srows, sld = _fp8_shape(rows, cols, block_rows)
-        codes = torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device)
-        scales = torch.empty((srows, sld), dtype=torch.uint8, device=device)
+        codes = _made(torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device), stream)
+        scales = _made(torch.empty((srows, sld), dtype=torch.uint8, device=device), stream)
         self = cls.__new__(cls)
         self.rows, self.cols, self.block_rows, self.codes, self.scales = rows, cols, block_rows, codes, scales
         self.c = _Fp8(codes.data_ptr(), scales.data_ptr(), rows, cols, block_rows, 0)
@@ -782,9 +790,9 @@ def ngram_quant_fp8(x, rows=True, transposed=False, block_rows: int = 1, q=None,
     n, d = _matrix(x, "x")
     px = _arg(x, _VALUES, n * d, "x")
     if q is None and rows:
-        q = Fp8.empty(n, d, block_rows, x.device)
+        q = Fp8.empty(n, d, block_rows, x.device, stream)
     if qt is None and transposed:
-        qt = Fp8.empty(d, n, block_rows, x.device)
+        qt = Fp8.empty(d, n, block_rows, x.device, stream)
     rc = lib().ngram_quant_fp8(px, _value(x), n, d, _fp8_c(q), _fp8_c(qt), _raw_stream(stream))
     if rc:
         _check(rc, "ngram_quant_fp8")
@@ -810,11 +818,11 @@ def ngram_add_norm(x, gamma, eps, residual=None, sum_out=None, y_out=None, q_out
     px = _arg(x, _VALUES, count, "x")
     pg = _arg(gamma, _F32, d, "gamma")
     if q_out is None and quantise:
-        q_out = Fp8.empty(n, d, 1, x.device)
+        q_out = Fp8.empty(n, d, 1, x.device, stream)
     if y_out is None and keep_y:
-        y_out = torch.empty((n, d), dtype=torch.bfloat16, device=x.device)
+        y_out = _made(torch.empty((n, d), dtype=torch.bfloat16, device=x.device), stream)
     if r_out is None and keep_r:
-        r_out = torch.empty(n, dtype=torch.float32, device=x.device)
+        r_out = _made(torch.empty(n, dtype=torch.float32, device=x.device), stream)
     rc = lib().ngram_add_norm(px, _value(x), _opt(residual, _BF16, count, "residual"), n, d, pg, eps,
                               _opt(sum_out, _BF16, count, "sum_out"), _opt(y_out, _BF16, count, "y_out"), _fp8_c(q_out),
                               _opt(r_out, _F32, n, "r_out"), _raw_stream(stream))
@@ -838,9 +846,12 @@ def ngram_add_norm_grad(dy, sum, r, gamma, dsum=None, dx_out=None, dgamma_out=No
     count = n * d
     pdy = _arg(dy, _VALUES, count, "dy")
     ps, pr, pg = _arg(sum, _BF16, count, "sum"), _arg(r, _F32, n, "r"), _arg(gamma, _F32, d, "gamma")
-    dx_out = torch.empty((n, d), dtype=torch.bfloat16, device=dy.device) if dx_out is None else dx_out
-    dgamma_out = torch.empty(d, dtype=torch.float32, device=dy.device) if dgamma_out is None else dgamma_out
-    workspace = add_norm_grad_workspace(n, d, dy.device) if workspace is None else workspace
+    if dx_out is None:
+        dx_out = _made(torch.empty((n, d), dtype=torch.bfloat16, device=dy.device), stream)
+    if dgamma_out is None:
+        dgamma_out = _made(torch.empty(d, dtype=torch.float32, device=dy.device), stream)
+    if workspace is None:
+        workspace = _made(add_norm_grad_workspace(n, d, dy.device), stream)
     rc = lib().ngram_add_norm_grad(pdy, _value(dy), ps, pr, pg, _opt(dsum, _BF16, count, "dsum"), n, d,
                                    _arg(dx_out, _BF16, count, "dx_out"), _arg(dgamma_out, _F32, d, "dgamma_out"),
                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream))
@@ -863,10 +874,12 @@ def ngram_project_fp8(a: Fp8, b: Fp8, out=None, dtype=torch.bfloat16, workspace=
     (see ngram_project_fp8 in ngram.h)."""
     m, n = a.rows, b.rows
     if out is None:
-        out = torch.empty((m, n), dtype=dtype, device=a.codes.device)
+        out = _made(torch.empty((m, n), dtype=dtype, device=a.codes.device), stream)
     po = _arg(out, _VALUES, m * n, "out")
     if workspace is None:
         workspace = project_fp8_workspace(m, n, a.cols, out.dtype, out.device)
+        if workspace is not None:
+            _made(workspace, stream)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     rc = lib().ngram_project_fp8(a.c, b.c, po, _value(out), ws, ws_bytes, _raw_stream(stream))
     if rc:

@@ -413,7 +413,8 @@ int ngram_grad_gate_noalloc(const int32_t* rows, const uint16_t* dout, const flo
  * range, nothing of its precision, and the matrix cores apply them.
  *   codes  [rows][128 ceil(cols / 128)] bytes, zero from cols on, 16-byte aligned;
  *   scales [rows, or ceil(rows / 128)][4 ceil(ceil(cols / 128) / 4)] bytes,
- *     127 from block ceil(cols / 128) on, 4-byte aligned.
+ *     127 from block ceil(cols / 128) on, 4-byte aligned; every byte from 1
+ *     to 254 (what the library writes).
  * rows, cols <= NGRAM_FP8_MAX.  The *_bytes calls give the sizes (-1 for sizes
  * out of range). */
 #define NGRAM_FP8_BLOCK 128
