@@ -2,7 +2,14 @@
 // ngram_adamw_rows over the touched rows of a table, with moments in fp32 or
 // in 8 bits.  The formulas are in include/ngram.h.  Both are bound by HBM
 // bandwidth: 10 bytes an element for bf16 parameters and gradients with 8-bit
-// moments, 28 for everything in fp32.
+// moments, 28 for everything in fp32.  A lane has eight consecutive elements:
+// every access of a wavefront is 512 to 2048 consecutive bytes, and a scale
+// block of 128 is a group of 16 lanes, which finds its largest value by lane
+// moves.  Everything is read and written once, so all of it goes past the
+// caches' usual keeping (260,000 rows of 2560: 1670-1700 us with plain
+// accesses, 1400-1450 so).  Measured: 200M bf16 parameters with 8-bit moments
+// 326 us, 6.1 TB/s; 60M of everything in fp32 322 us, 5.2 TB/s; those rows 5.5
+// TB/s.  A large copy reaches 5.5 TB/s.
 #include "common8.h"
 
 #include <cmath>
@@ -142,10 +149,10 @@ template <bool F32>
 __device__ __forceinline__ void store8(void* p, int64_t i, const Raw8<F32>& x) {
     if (F32) {
         u32x4* const d = reinterpret_cast<u32x4*>(static_cast<float*>(p) + i);
-        d[0] = x.a;
-        d[1] = x.b;
+        __builtin_nontemporal_store(x.a, d);
+        __builtin_nontemporal_store(x.b, d + 1);
     } else {
-        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = x.a;
+        __builtin_nontemporal_store(x.a, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i));
     }
 }
 
@@ -221,14 +228,14 @@ __global__ void __launch_bounds__(256) adamw_kernel(const AdamArgs a) {
     const int64_t left = t.numel - i;
     const int live = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
     if (live == 8) {
-        e.p.load(t.p, i);
-        e.g.load(t.g, i);
+        e.p.load_stream(t.p, i);
+        e.g.load_stream(t.g, i);
         if (S8) {
-            e.mc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(t.m) + i);
-            e.vc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(t.v) + i);
+            e.mc = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(t.m) + i));
+            e.vc = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(t.v) + i));
         } else {
-            e.m.load(t.m, i);
-            e.v.load(t.v, i);
+            e.m.load_stream(t.m, i);
+            e.v.load_stream(t.v, i);
         }
     } else {
         load_some(e.p, t.p, i, live);
@@ -255,8 +262,8 @@ __global__ void __launch_bounds__(256) adamw_kernel(const AdamArgs a) {
     if (live == 8) {
         store8(t.p, i, e.p);
         if (S8) {
-            *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(t.m) + i) = e.mc;
-            *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(t.v) + i) = e.vc;
+            __builtin_nontemporal_store(e.mc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(t.m) + i));
+            __builtin_nontemporal_store(e.vc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(t.v) + i));
         } else {
             store8(t.m, i, e.m);
             store8(t.v, i, e.v);
@@ -316,16 +323,16 @@ __global__ void __launch_bounds__(256) adamw_rows_kernel(const RowsArgs a) {
     const int64_t at = row * a.d + col;
     Eight<P32, G32, S8> e;
     if (live) {
-        e.g.load(a.g, u * a.d + col);
-        e.p.load(a.p, at);
+        e.g.load_stream(a.g, u * a.d + col);
+        e.p.load_stream(a.p, at);
         if (S8) {
-            e.mc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.m) + at);
-            e.vc = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.v) + at);
+            e.mc = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.m) + at));
+            e.vc = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.v) + at));
             e.ms = a.ms[row * a.nb + (col >> 7)];
             e.vs = a.vs[row * a.nb + (col >> 7)];
         } else {
-            e.m.load(a.m, at);
-            e.v.load(a.v, at);
+            e.m.load_stream(a.m, at);
+            e.v.load_stream(a.v, at);
         }
     } else {
         e.g.zero();
@@ -340,8 +347,8 @@ __global__ void __launch_bounds__(256) adamw_rows_kernel(const RowsArgs a) {
     if (!live) return;
     store8(a.p, at, e.p);
     if (S8) {
-        *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.m) + at) = e.mc;
-        *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.v) + at) = e.vc;
+        __builtin_nontemporal_store(e.mc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.m) + at));
+        __builtin_nontemporal_store(e.vc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.v) + at));
         if ((lane & 15) == 0) {
             a.ms[row * a.nb + (col >> 7)] = static_cast<uint8_t>(e.ms);
             a.vs[row * a.nb + (col >> 7)] = static_cast<uint8_t>(e.vs);

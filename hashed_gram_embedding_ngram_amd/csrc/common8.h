@@ -92,6 +92,16 @@ struct Raw8 {
             a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
         }
     }
+    // the same past the caches' usual keeping: read once, by one lane
+    __device__ __forceinline__ void load_stream(const void* p, int64_t i) {
+        if (F32) {
+            const u32x4* s = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
+            a = __builtin_nontemporal_load(s);
+            b = __builtin_nontemporal_load(s + 1);
+        } else {
+            a = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i));
+        }
+    }
     __device__ __forceinline__ void zero() { a = u32x4{0, 0, 0, 0}; b = u32x4{0, 0, 0, 0}; }
     __device__ __forceinline__ float at(int k) const {      // k a constant once unrolled
         if (F32) return __uint_as_float(k < 4 ? a[k & 3] : b[k & 3]);
