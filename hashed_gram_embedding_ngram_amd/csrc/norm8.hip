@@ -293,24 +293,39 @@ __global__ void __launch_bounds__(64 * kMaxWaves) add_norm_grad_kernel(const Nor
     }
 }
 
-// dgamma[col] = the sum of `rows` rows of partial sums: 64 columns per
-// workgroup, 16 wavefronts that take every 16th row, joined in LDS.
+// dgamma[col] = the sum of `rows` <= 512 rows of partial sums.  64 columns per
+// workgroup: thread t has columns 4 (t & 15) .. +3 of every 64th row, at most
+// eight loads that are all in flight at once, and LDS joins the 64 sums.
+constexpr int kPartialRows = 512;
+
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ partial, int rows, int d,
                                                           float* __restrict__ out) {
-    __shared__ float part[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int col = blockIdx.x * 64 + lane;
-    float t = 0.0f;
-    if (col < d) {
-#pragma unroll 8
-        for (int r = wave; r < rows; r += 16) t += partial[static_cast<int64_t>(r) * d + col];
+    __shared__ float part[64][64];
+    const int t = threadIdx.x, group = t >> 4, c4 = 4 * (t & 15);
+    const int col = blockIdx.x * 64 + c4;
+    f32x4 v[kPartialRows / 64];
+#pragma unroll
+    for (int i = 0; i < kPartialRows / 64; ++i) {
+        const int r = group + 64 * i;
+        v[i] = r < rows && col < d ? *reinterpret_cast<const f32x4*>(partial + static_cast<int64_t>(r) * d + col)
+                                   : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    part[wave][lane] = t;
+    f32x4 s = v[0];
+#pragma unroll
+    for (int i = 1; i < kPartialRows / 64; ++i) s += v[i];
+    *reinterpret_cast<f32x4*>(&part[group][c4]) = s;
     __syncthreads();
-    if (wave == 0 && col < d) {
-        t = 0.0f;
-        for (int w = 0; w < 16; ++w) t += part[w][lane];
-        out[col] = t;
+    // column t & 63: 16 threads add four sums each, then one adds the 16
+    const int c = t & 63, w = t >> 6;
+    const float q = (part[4 * w][c] + part[4 * w + 1][c]) + (part[4 * w + 2][c] + part[4 * w + 3][c]);
+    __syncthreads();
+    part[w][c] = q;
+    __syncthreads();
+    if (t < 64 && blockIdx.x * 64 + t < d) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum += part[i][t];
+        out[blockIdx.x * 64 + t] = sum;
     }
 }
 
@@ -498,7 +513,7 @@ RowShape grad_shape(int64_t n, int d) {
     s.waves = std::min(kMaxWaves, total);
     s.chunks = (total + s.waves - 1) / s.waves;
     s.waves = (total + s.chunks - 1) / s.chunks;
-    s.grid = std::max<int64_t>(1, std::min<int64_t>(n, 512));   // no rows: one workgroup writes a row of zeros
+    s.grid = std::max<int64_t>(1, std::min<int64_t>(n, kPartialRows));   // no rows: one workgroup writes a row of zeros
     return s;
 }
 
