@@ -416,6 +416,15 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
 // waits is G times shorter, and join their accumulators in LDS at the end.
 // Same LDS layout and fragments as above; a scale word is loaded with every
 // G steps.
+//
+// Bound by a round's chain of load, barrier, fragment reads and products, not
+// by a unit: 777 x 4104 over 1032 columns in fp32, 14.7 us (231 tiles, five
+// rounds of about 1.6 us, launch and first loads 5, stores 3.5); one group of
+// 8 or 4 wavefronts with four steps' loads ahead took 17 to 20, 64 x 64 tiles
+// 17.6.  128 x 128 tiles have 4 x 4 fragments a wavefront, not 4 x 2
+// (14.7 against 15.4 us): a widened fragment then serves four products, not
+// two, and widening is 16 vector instructions.  A bf16 result has nothing to
+// widen and takes the same time either way (1024 x 2560 x 2560: 16.5 us).
 template <int TM_, int TN_, int WM_, int WN_, int G_, bool F32_>
 struct SmallTile {
     static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, G = G_;
@@ -514,6 +523,7 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_small_kernel(const 
                 const Wide wa = widen(fa[s], sa[s]);
 #pragma unroll
                 for (int j = 0; j < TN; ++j) acc[s][j] = mfma_wide(wb[j], wa, acc[s][j]);
+                pin<TN>(acc[s]);
             }
         } else {
 #pragma unroll
@@ -744,7 +754,7 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
     } else if (p.kind == 1) {
         rc = f32 ? launch_small<SmallTile<2, 2, 2, 2, 4, true>>(a, stream) : launch_small<SmallTile<2, 2, 2, 2, 4, false>>(a, stream);
     } else if (p.kind == 2) {
-        rc = f32 ? launch_small<SmallTile<4, 2, 2, 4, 2, true>>(a, stream) : launch_small<SmallTile<4, 2, 2, 4, 2, false>>(a, stream);
+        rc = f32 ? launch_small<SmallTile<4, 4, 2, 2, 2, true>>(a, stream) : launch_small<SmallTile<4, 4, 2, 2, 2, false>>(a, stream);
     } else {
         rc = f32 ? launch_tile<Tile<4, 4, 4, 2, 3, true>>(a, stream) : launch_tile<Tile<8, 4, 2, 4, 2, false>>(a, stream);
     }
