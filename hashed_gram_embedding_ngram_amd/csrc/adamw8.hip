@@ -8,7 +8,7 @@
 // moves.  Everything is read and written once, so all of it goes past the
 // caches' usual keeping (260,000 rows of 2560: 1670-1700 us with plain
 // accesses, 1400-1450 so).  Measured: 200M bf16 parameters with 8-bit moments
-// 326 us, 6.1 TB/s; 60M of everything in fp32 322 us, 5.2 TB/s; those rows 5.5
+// 322 us, 6.2 TB/s; 60M of everything in fp32 322 us, 5.2 TB/s; those rows 5.5
 // TB/s.  A large copy reaches 5.5 TB/s.
 #include "common8.h"
 
@@ -202,8 +202,9 @@ struct TensorArg {
 // nothing is allocated or copied and the call can be captured in a graph.
 constexpr int kTensorsPerLaunch = 48;
 // Elements per workgroup: one round of 256 lanes x 8.  Measured on 200M bf16
-// parameters with 8-bit moments: 367 us against 387 with two rounds and 402
-// with four; on 300,000 fp32 elements 3.6 us against 4.2 and 6.1.
+// parameters with 8-bit moments, before the streaming accesses: 367 us against
+// 387 with two rounds and 402 with four; on 300,000 fp32 elements 3.6 us
+// against 4.2 and 6.1.
 constexpr int kChunk = 2048;
 
 struct AdamArgs {

@@ -52,9 +52,15 @@ namespace {
 // columns 512 c + 8 l .. +7 of its chunks, so every load and store of a
 // chunk is one 16-byte (bf16) or 8-byte (codes) access per lane over
 // consecutive addresses, and a scale block of 128 columns is one group of 16
-// lanes.  A wavefront keeps C chunks of gamma in registers and walks over
-// rows; with WIDE, the wavefronts of a workgroup share each row (wavefront w
-// has chunks w C .. w C + C - 1) and join the sums of squares in LDS.
+// lanes.  A wavefront takes one row of C chunks, every load of it issued
+// before the first is used; with WIDE, the wavefronts of a workgroup share a
+// row (wavefront w has chunks w C .. w C + C - 1) and join the sums of squares
+// in LDS.
+//
+// Bound by memory: 32768 x 2560 from bf16 (7 bytes an element with the 8-bit
+// output) 100 us, 5.9 TB/s, where a large copy reaches 5.5; 5003 x 1032 from
+// fp32 with everything kept 11.6 us, 4.9 TB/s; 4 x 2560 2.7 us, which is an
+// empty launch and one dependent load.
 struct NormArgs {
     const void* x;
     const uint16_t* residual;
@@ -74,16 +80,18 @@ struct NormArgs {
 
 constexpr int kMaxWaves = 16;
 
-// A store past the caches' usual keeping (STREAM: outputs of many rows, which
-// are gone from L2 before anyone reads them; 106 -> 101 us at 32768 x 2560), or
-// a plain one.
+// A store past the caches' usual keeping (large outputs, which are gone from
+// L2 before anyone reads them), or a plain one.  Streaming against plain, us:
+// 32768 x 2560 101 / 106, 2048 x 8192 20.9 / 25.2, 1024 x 2560 5.3 / 5.9,
+// 512 x 1032 3.5 / 3.2.  Rows shared by wavefronts take it from 2^20 elements
+// on, whole rows (2048 and more) always.
 template <bool STREAM, typename V, typename P>
 __device__ __forceinline__ void put(P* to, V v) {
     if (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<V*>(to));
     else *reinterpret_cast<V*>(to) = v;
 }
 
-template <int C, bool F32, bool WIDE>
+template <int C, bool F32, bool WIDE, bool STREAM>
 __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_kernel(const NormArgs a) {
     __shared__ float part[kMaxWaves];
     const int lane = threadIdx.x & 63;
@@ -130,7 +138,7 @@ __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_kernel(c
             s[c][2 * k] = bf16_lo(packed[k]);
             s[c][2 * k + 1] = bf16_hi(packed[k]);
         }
-        if (a.sum_out && col < a.d) put<!WIDE>(a.sum_out + at + col, packed);
+        if (a.sum_out && col < a.d) put<STREAM>(a.sum_out + at + col, packed);
         float t = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) t = fmaf(s[c][k], s[c][k], t);
@@ -157,7 +165,7 @@ __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_kernel(c
             u32x4 packed;
 #pragma unroll
             for (int k = 0; k < 4; ++k) packed[k] = bf16_pair(y[2 * k], y[2 * k + 1]);
-            put<!WIDE>(a.y_out + at + col, packed);
+            put<STREAM>(a.y_out + at + col, packed);
         }
         if (a.codes) {
             if (col >= a.d) {       // past the row: zero codes, also where r is not finite
@@ -170,7 +178,7 @@ __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_kernel(c
                 u32x2 q;
                 q[0] = codes4(y[0], y[1], y[2], y[3], inv);
                 q[1] = codes4(y[4], y[5], y[6], y[7], inv);
-                put<!WIDE>(a.codes + row * a.ld + col, q);
+                put<STREAM>(a.codes + row * a.ld + col, q);
             }
             const uint32_t b0 = __builtin_amdgcn_readlane(byte, 0), b1 = __builtin_amdgcn_readlane(byte, 16);
             const uint32_t b2 = __builtin_amdgcn_readlane(byte, 32), b3 = __builtin_amdgcn_readlane(byte, 48);
@@ -189,6 +197,10 @@ __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_kernel(c
 // A workgroup walks over rows, its wavefronts sharing each as in the wide
 // forward; a lane adds its columns' dgamma terms in registers, and one row of
 // partial sums per workgroup goes to the workspace for the kernel below.
+//
+// Bound by memory, 8 bytes an element: 32768 x 2560 in bf16 112 us, 6.0 TB/s
+// (5.8 with the column sums); 777 x 520 3.2 to 3.9 us, a launch and three
+// dependent loads.
 struct NormGradArgs {
     const void* dy;
     const uint16_t* sum;
@@ -295,7 +307,9 @@ __global__ void __launch_bounds__(64 * kMaxWaves) add_norm_grad_kernel(const Nor
 
 // dgamma[col] = the sum of `rows` <= 512 rows of partial sums.  64 columns per
 // workgroup: thread t has columns 4 (t & 15) .. +3 of every 64th row, at most
-// eight loads that are all in flight at once, and LDS joins the 64 sums.
+// eight loads that are all in flight at once, and LDS joins the 64 sums, each
+// in a fixed order.  3.1 to 3.7 us over 520 columns and 4.7 over 2560 (512
+// rows), of which a launch is 2.5; with four rows at a time it was 4.6 and 7.
 constexpr int kPartialRows = 512;
 
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ partial, int rows, int d,
@@ -339,6 +353,9 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
 // group of 16 lanes (row scales by lane moves), and the patch transposes in
 // registers.  Column maxima go through LDS; so do the transposed codes, which
 // then leave as whole 128-byte lines.
+//
+// Bound by memory, with the two barriers of a tile in the way: 8192 x 2560 in
+// bf16, both outputs, 19.1 us, 4.4 TB/s (a large copy 5.5).
 struct QuantArgs {
     const void* x;
     uint8_t *q, *qs, *qt, *qts;
@@ -473,10 +490,13 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(F32 ? 
 // ---------------------------------------------------------------------------
 // Launch shapes.
 
-// Forward.  Many rows: a wavefront takes a whole row of up to 5 chunks, wider
-// rows are shared by wavefronts of 4 chunks.  Few rows: one chunk per
-// wavefront, so that a row's loads are all in flight at once on as many
-// wavefronts as there are chunks.
+// Forward.  Many rows of up to 5 chunks: a wavefront takes a whole row and
+// needs no barrier (2560 columns, us, whole rows / shared rows: 4096 rows 13.9
+// / 16.7, 2048 rows 8.5 / 10.2, 1024 rows 6.7 / 5.9, 256 rows 5.1 / 3.2; 1032
+// columns: the same at 2048 rows, 12.2 / 13.9 at 8192).  Few rows and wide ones:
+// one chunk per wavefront up to 16, so that a row's loads are spread over as
+// many wavefronts as it has chunks (8192 x 8192: 84.1 against 86.4 with four,
+// before streaming stores).
 struct RowShape {
     int chunks;     // per wavefront
     int waves;      // per workgroup
@@ -493,8 +513,7 @@ RowShape row_shape(int64_t n, int d) {
         s.waves = 4;
         s.grid = (n + 3) / 4;
     } else {
-        const int want = n < 2048 ? 1 : 4;
-        s.waves = std::min(kMaxWaves, (total + want - 1) / want);
+        s.waves = std::min(kMaxWaves, total);
         s.chunks = (total + s.waves - 1) / s.waves;
         s.waves = (total + s.chunks - 1) / s.chunks;
         s.grid = n;
@@ -502,10 +521,11 @@ RowShape row_shape(int64_t n, int d) {
     return s;
 }
 
-// Gradient.  A row by a workgroup, one chunk per wavefront up to 16: at 32768
-// x 2560, 119 us against 128 with two chunks and 132 with a wavefront to a
-// row (fewer registers, more wavefronts).  512 workgroups walk over the rows (1024: 132
-// us: more partial sums; 256: slower in every shape).
+// Gradient.  A row by a workgroup, one chunk per wavefront up to 16: when the
+// shape was chosen, at 32768 x 2560 119 us with the column sums against 128
+// with two chunks and 132 with a wavefront to a row (fewer registers, more
+// wavefronts); 116 now.  512 workgroups walk over the rows (1024: 132 us then:
+// more partial sums; 256: slower in every shape).
 RowShape grad_shape(int64_t n, int d) {
     const int total = (d + kSlice - 1) / kSlice;
     RowShape s;
@@ -517,9 +537,9 @@ RowShape grad_shape(int64_t n, int d) {
     return s;
 }
 
-template <bool F32, bool WIDE>
+template <bool F32, bool WIDE, bool STREAM>
 void launch_norm(int chunks, dim3 grid, dim3 block, hipStream_t st, const NormArgs& a) {
-#define NG8_CASE(C) case C: hipLaunchKernelGGL((add_norm_kernel<C, F32, WIDE>), grid, block, 0, st, a); break
+#define NG8_CASE(C) case C: hipLaunchKernelGGL((add_norm_kernel<C, F32, WIDE, STREAM>), grid, block, 0, st, a); break
     switch (chunks) { NG8_CASE(1); NG8_CASE(2); NG8_CASE(3); NG8_CASE(4); NG8_CASE(5); default:
         if constexpr (WIDE) switch (chunks) { NG8_CASE(6); NG8_CASE(7); default: NG8_CASE(8); } }
 #undef NG8_CASE
@@ -595,12 +615,16 @@ int ngram_add_norm(const void* x, int32_t x_dtype, const uint16_t* residual, int
     a.inv_d = 1.0f / static_cast<float>(d);
     const RowShape s = row_shape(n, d);
     const dim3 grid(static_cast<unsigned>(s.grid)), block(64 * s.waves);
-    if (x_dtype == NGRAM_F32) {
-        if (s.wide) launch_norm<true, true>(s.chunks, grid, block, stream, a);
-        else launch_norm<true, false>(s.chunks, grid, block, stream, a);
+    const bool f32 = x_dtype == NGRAM_F32;
+    if (!s.wide) {
+        if (f32) launch_norm<true, false, true>(s.chunks, grid, block, stream, a);
+        else launch_norm<false, false, true>(s.chunks, grid, block, stream, a);
+    } else if (n * d >= 1 << 20) {      // see put()
+        if (f32) launch_norm<true, true, true>(s.chunks, grid, block, stream, a);
+        else launch_norm<false, true, true>(s.chunks, grid, block, stream, a);
     } else {
-        if (s.wide) launch_norm<false, true>(s.chunks, grid, block, stream, a);
-        else launch_norm<false, false>(s.chunks, grid, block, stream, a);
+        if (f32) launch_norm<true, true, false>(s.chunks, grid, block, stream, a);
+        else launch_norm<false, true, false>(s.chunks, grid, block, stream, a);
     }
     return hip_status("ngram_add_norm launch");
 }

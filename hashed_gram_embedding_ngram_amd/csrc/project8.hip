@@ -109,6 +109,17 @@ __device__ __forceinline__ void store4(void* c, int64_t at, f32x4 v) {
 //
 // Scales go through LDS as well: a row's word of four steps' bytes with the
 // first of the four, and a byte read for each fragment and step.
+//
+// Measured: bf16 results (256 x 256 tiles) 32768 x 2560 x 2560 197 to 201 us,
+// 2.1 to 2.2 PFLOP/s; 8192 x 8192 x 8192 449 us, 2.45 PFLOP/s.  The matrix
+// cores are busy half of the time at the 2.0 GHz that the card holds under
+// this load; products alone, on random codes, stop at 3.9 to 4.0 PFLOP/s.  A
+// step is bound by the way of its 64 KB from L2 through one barrier rather
+// than by its products (tiles of 256 x 160 and 256 x 192 have nearly the same
+// time a step), and a tile's 128 KB of stores, all at once, take another 15%.
+// fp32 results (256 x 128 tiles) 2560 x 2560 x 8192 97 to 105 us, 1.0 to 1.1
+// PFLOP/s of the 1.3 that a large bf16 product reaches: 200 tiles for 256
+// compute units.
 template <int TM_, int TN_, int WM_, int WN_, int NS_, bool F32_>
 struct Tile {
     static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, NS = NS_;
@@ -164,8 +175,8 @@ __device__ __forceinline__ void pin(f32x4* acc) {
 // B: four consecutive outputs, 16 bytes of fp32.  In bf16 that is 8, so two
 // neighbouring tiles' values are exchanged between lane groups 0 and 1, 2 and
 // 3: then a lane has eight consecutive outputs of one of the two, and a store
-// writes 64 consecutive bytes of 16 rows (32-byte pieces took 8% of the whole
-// product's time at 32768 x 2560 x 2560).
+// writes 64 consecutive bytes of 16 rows (32-byte pieces took 8% more time for
+// the whole product at 32768 x 2560 x 2560).
 template <int TM, int TN, bool F32>
 __device__ __forceinline__ void store_tile(const ProjArgs& a, const f32x4 (&acc)[TM][TN], int64_t m0, int64_t n0, int split, int lane) {
     const int lr = lane & 15, g = lane >> 4;
@@ -554,7 +565,8 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_small_kernel(const 
     store_tile<TM, TN, F32>(a, acc, m0 + wm, n0 + wn, it.split, lane);
 }
 
-// The sum of the splits' partial products, in their order.
+// The sum of the splits' partial products, in their order: bound by memory,
+// 4 (splits + 1) bytes an element for fp32.
 template <bool F32>
 __global__ void __launch_bounds__(256) split_sum_kernel(const float* __restrict__ partial, int splits, int64_t count, void* c) {
     const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
