@@ -58,8 +58,8 @@ namespace {
 // in LDS.
 //
 // Bound by memory: 32768 x 2560 from bf16 (7 bytes an element with the 8-bit
-// output) 100 us, 5.9 TB/s, where a large copy reaches 5.5; 5003 x 1032 from
-// fp32 with everything kept 11.6 us, 4.9 TB/s; 4 x 2560 2.7 us, which is an
+// output) 101 us, 5.8 TB/s, where a large copy reaches 5.5; 5003 x 1032 from
+// fp32 with everything kept 11.7 us, 4.8 TB/s; 4 x 2560 2.7 us, which is an
 // empty launch and one dependent load.
 struct NormArgs {
     const void* x;
@@ -80,11 +80,14 @@ struct NormArgs {
 
 constexpr int kMaxWaves = 16;
 
-// A store past the caches' usual keeping (large outputs, which are gone from
-// L2 before anyone reads them), or a plain one.  Streaming against plain, us:
-// 32768 x 2560 101 / 106, 2048 x 8192 20.9 / 25.2, 1024 x 2560 5.3 / 5.9,
-// 512 x 1032 3.5 / 3.2.  Rows shared by wavefronts take it from 2^20 elements
-// on, whole rows (2048 and more) always.
+// A store past the caches' usual keeping, or a plain one.  The sum and y are
+// next read much later, and stream: us with and without, 32768 x 2560 101 /
+// 106, 2048 x 8192 23.9 / 25.2, 1024 x 2560 5.4 / 5.9, 512 x 1032 3.5 / 3.2
+// (rows shared by wavefronts stream from 2^20 elements on, whole rows, 2048
+// and more, always).  The codes are read by the very next product and do not:
+// streaming them too saves this kernel 1% (2048 x 8192 13%) and costs that
+// product more (norm and product of 1024 x 2560 25.0 against 22.1 us, of 8192
+// x 2560 100.1 / 96.4, of 32768 x 2560 297 / 295).
 template <bool STREAM, typename V, typename P>
 __device__ __forceinline__ void put(P* to, V v) {
     if (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<V*>(to));
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_kernel(c
                 u32x2 q;
                 q[0] = codes4(y[0], y[1], y[2], y[3], inv);
                 q[1] = codes4(y[4], y[5], y[6], y[7], inv);
-                put<STREAM>(a.codes + row * a.ld + col, q);
+                put<false>(a.codes + row * a.ld + col, q);
             }
             const uint32_t b0 = __builtin_amdgcn_readlane(byte, 0), b1 = __builtin_amdgcn_readlane(byte, 16);
             const uint32_t b2 = __builtin_amdgcn_readlane(byte, 32), b3 = __builtin_amdgcn_readlane(byte, 48);
@@ -355,7 +358,10 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
 // then leave as whole 128-byte lines.
 //
 // Bound by memory, with the two barriers of a tile in the way: 8192 x 2560 in
-// bf16, both outputs, 19.1 us, 4.4 TB/s (a large copy 5.5).
+// bf16, both outputs, 19.8 us, 4.2 TB/s (a large copy 5.5), the transposed one
+// alone 14.4.  Streaming stores: 18.2 and 12.6 us, but the products that read
+// the codes next then take longer (a layer's two gradients 206 us against
+// 199), so the stores are plain.
 struct QuantArgs {
     const void* x;
     uint8_t *q, *qs, *qt, *qts;
