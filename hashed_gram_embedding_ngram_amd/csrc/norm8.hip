@@ -202,8 +202,7 @@ __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_kernel(c
 // partial sums per workgroup goes to the workspace for the kernel below.
 //
 // Bound by memory, 8 bytes an element: 32768 x 2560 in bf16 112 us, 6.0 TB/s
-// (5.8 with the column sums); 777 x 520 3.2 to 3.9 us, a launch and three
-// dependent loads.
+// (5.8 with the column sums).
 struct NormGradArgs {
     const void* dy;
     const uint16_t* sum;
@@ -311,8 +310,8 @@ __global__ void __launch_bounds__(64 * kMaxWaves) add_norm_grad_kernel(const Nor
 // dgamma[col] = the sum of `rows` <= 512 rows of partial sums.  64 columns per
 // workgroup: thread t has columns 4 (t & 15) .. +3 of every 64th row, at most
 // eight loads that are all in flight at once, and LDS joins the 64 sums, each
-// in a fixed order.  3.1 to 3.7 us over 520 columns and 4.7 over 2560 (512
-// rows), of which a launch is 2.5; with four rows at a time it was 4.6 and 7.
+// in a fixed order.  4.7 us over 2560 columns of 512 rows, of which a launch is
+// 2.5; with four rows at a time it was 7.
 constexpr int kPartialRows = 512;
 
 __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restrict__ partial, int rows, int d,
@@ -343,6 +342,114 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* __restric
 #pragma unroll
         for (int i = 0; i < 16; ++i) sum += part[i][t];
         out[blockIdx.x * 64 + t] = sum;
+    }
+}
+
+// Few rows, where launches are most of the time: dx and dgamma in one.  dgamma
+// needs no result of dx's (r is given), so the first workgroups take 32
+// columns each of all rows (thread t has columns 4 (t & 7) .. +3 of every
+// 128th row, four rows in flight, and LDS joins the 128 sums in a fixed
+// order), and the rest take rows once more, as many each as `waves` wavefronts
+// to a row leave room for.  Bound by the launch and its chain of loads.  The second reading must find dy as it was, so a call whose dx
+// replaces dy goes the other way.
+constexpr int kFewGroups = 8 * kMaxWaves;       // row groups of a column workgroup
+
+struct NormGradFewArgs {
+    NormGradArgs g;     // without partial sums
+    float* dgamma;
+    int32_t column_groups;  // workgroups that take columns
+    int32_t waves;          // of a row
+};
+
+template <bool F32>
+__global__ void __launch_bounds__(64 * kMaxWaves) add_norm_grad_few_kernel(const NormGradFewArgs f) {
+    __shared__ __attribute__((aligned(16))) float part[kFewGroups][32];
+    const NormGradArgs& a = f.g;
+    const int t = threadIdx.x, lane = t & 63;
+    if (static_cast<int>(blockIdx.x) >= f.column_groups) {
+        const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+        const int slots = kMaxWaves / f.waves, slot = wave / f.waves, col = (wave - slot * f.waves) * kSlice + lane * kVec;
+        const int64_t row = static_cast<int64_t>(blockIdx.x - f.column_groups) * slots + slot;
+        const bool live = slot < slots && row < a.n;
+        const int64_t at = row * a.d + col;
+        Raw8<F32> dy;
+        Raw8<true> gam;
+        Raw8<false> s, ds;
+        dy.zero(); gam.zero(); s.zero(); ds.zero();
+        const float r = live ? a.r[row] : 0.0f;
+        if (live && col < a.d) {
+            dy.load(a.dy, at);
+            gam.load(a.gamma, col);
+            s.load(a.sum, at);
+            if (a.dsum) ds.load(a.dsum, at);
+        }
+        float u[8], v[8], w[8], h[8];
+        dy.get(u);
+        s.get(v);
+        ds.get(w);
+        gam.get(h);
+        float dot = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) dot = fmaf(u[k] * h[k], v[k], dot);
+        dot = wave_sum(dot);
+        if (lane == 0) part[0][wave] = dot;
+        __syncthreads();
+        if (!live) return;
+        dot = 0.0f;
+        for (int i = 0; i < f.waves; ++i) dot += part[0][slot * f.waves + i];
+        const float scale = dot * r * r * r * a.inv_d;
+        u32x4 packed;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            packed[k] = bf16_pair((u[2 * k] * h[2 * k] * r - v[2 * k] * scale) + w[2 * k],
+                                  (u[2 * k + 1] * h[2 * k + 1] * r - v[2 * k + 1] * scale) + w[2 * k + 1]);
+        if (col < a.d) put<false>(a.dx + at, packed);
+        return;
+    }
+    const int first = blockIdx.x * 32, c4 = 4 * (t & 7), group = t >> 3, col = first + c4;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (col < a.d) {
+        for (int64_t base = group; base < a.n; base += 4 * kFewGroups) {
+            f32x4 u[4];
+            u32x2 p[4] = {}, v[4];
+            float r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t row = base + i * kFewGroups;
+                const int64_t at = row * a.d + col;
+                u[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                v[i] = u32x2{0, 0};
+                r[i] = 0.0f;
+                if (row < a.n) {
+                    r[i] = a.r[row];
+                    v[i] = *reinterpret_cast<const u32x2*>(a.sum + at);
+                    if (F32) u[i] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(a.dy) + at);
+                    else p[i] = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(a.dy) + at);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (!F32) u[i] = f32x4{bf16_lo(p[i][0]), bf16_hi(p[i][0]), bf16_lo(p[i][1]), bf16_hi(p[i][1])};
+                acc[0] = fmaf(u[i][0], bf16_lo(v[i][0]) * r[i], acc[0]);
+                acc[1] = fmaf(u[i][1], bf16_hi(v[i][0]) * r[i], acc[1]);
+                acc[2] = fmaf(u[i][2], bf16_lo(v[i][1]) * r[i], acc[2]);
+                acc[3] = fmaf(u[i][3], bf16_hi(v[i][1]) * r[i], acc[3]);
+            }
+        }
+    }
+    *reinterpret_cast<f32x4*>(&part[group][c4]) = acc;
+    __syncthreads();
+    // column t & 31: 32 threads add four sums each, then one adds the 32
+    const int c = t & 31, w = t >> 5;
+    const float q = (part[4 * w][c] + part[4 * w + 1][c]) + (part[4 * w + 2][c] + part[4 * w + 3][c]);
+    __syncthreads();
+    part[w][c] = q;
+    __syncthreads();
+    if (t < 32 && first + t < a.d) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum += part[i][t];
+        f.dgamma[first + t] = sum;
     }
 }
 
@@ -532,6 +639,13 @@ RowShape row_shape(int64_t n, int d) {
 // with two chunks and 132 with a wavefront to a row (fewer registers, more
 // wavefronts); 116 now.  512 workgroups walk over the rows (1024: 132 us then:
 // more partial sums; 256: slower in every shape).
+// One launch or two, us: 1 x 2560 2.5 / 4.4, 512 x 2560 5.9 / 10.0, 777 x 520
+// (fp32) 5.5 / 7.6, 1024 x 2560 10.4 / 11.5, 512 x 8192 (fp32) 14.1 / 16.6; but
+// 1024 x 8192 21.9 / 19.4, 1500 x 2560 13.7 / 12.7, 1500 x 520 8.7 / 9.0, 2048 x
+// 136 9.3 / 8.0.
+bool few_rows(int64_t n, int d) { return n <= 1024 && n * d <= 1 << 22; }
+
+
 RowShape grad_shape(int64_t n, int d) {
     const int total = (d + kSlice - 1) / kSlice;
     RowShape s;
@@ -661,6 +775,14 @@ int ngram_add_norm_grad(const void* dy, int32_t dy_dtype, const uint16_t* sum, c
     a.n = n; a.d = d;
     a.inv_d = 1.0f / static_cast<float>(d);
     const RowShape s = grad_shape(n, d);
+    if (few_rows(n, d) && s.chunks == 1 && dx_out != dy) {
+        const int slots = kMaxWaves / s.waves;
+        const NormGradFewArgs f{a, dgamma_out, (d + 31) / 32, s.waves};
+        const dim3 few(static_cast<unsigned>(f.column_groups + (n + slots - 1) / slots)), threads(64 * kMaxWaves);
+        if (dy_dtype == NGRAM_F32) hipLaunchKernelGGL((add_norm_grad_few_kernel<true>), few, threads, 0, stream, f);
+        else hipLaunchKernelGGL((add_norm_grad_few_kernel<false>), few, threads, 0, stream, f);
+        return hip_status("ngram_add_norm_grad launch");
+    }
     const dim3 grid(static_cast<unsigned>(s.grid)), block(64 * s.waves);
     if (dy_dtype == NGRAM_F32) launch_norm_grad<true>(s.chunks, grid, block, stream, a);
     else launch_norm_grad<false>(s.chunks, grid, block, stream, a);

@@ -466,7 +466,8 @@ int ngram_add_norm(const void* x, int32_t x_dtype, const uint16_t* residual, int
  *   dgamma[j] = sum over rows of dy[j] s[j] r
  * dx_out[n][d] bf16 is the gradient of both x and residual (and may equal
  * dsum, or a bf16 dy); dgamma_out[d] fp32 sums in a fixed order with no
- * atomics.  n = 0 gives dgamma 0.  workspace: device, 16-byte aligned,
+ * atomics (one order for n, d and whether dx takes dy's place).  n = 0 gives
+ * dgamma 0.  workspace: device, 16-byte aligned,
  * ngram_add_norm_grad_workspace_bytes(n, d) bytes. */
 int64_t ngram_add_norm_grad_workspace_bytes(int64_t n, int32_t d);
 int ngram_add_norm_grad(const void* dy, int32_t dy_dtype, const uint16_t* sum, const float* r, const float* gamma,

@@ -183,6 +183,28 @@ def test_add_norm_grad(n, d, dtype):
         assert torch.equal(again, dx)
 
 
+@pytest.mark.parametrize("n,d", [(5, 24), (127, 40), (513, 2560), (1024, 8), (1024, 4096), (1025, 40), (513, 8192), (900, 1032)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_add_norm_grad_at_the_edge_of_few_rows(n, d, dtype):
+    """Up to 1024 rows and 2^22 elements one launch computes both gradients, unless dx takes dy's place."""
+    say(f"add_norm_grad, few rows n={n} d={d} {dtype}")
+    rng = np.random.default_rng(3 * n + d)
+    s, dy = rounded(hidden(rng, n, d), BF), rounded(rng.normal(size=(n, d)) * 0.01, dtype)
+    gamma = (1 + 0.2 * rng.normal(size=d)).astype(np.float32)
+    r = (1 / np.sqrt((s.astype(np.float64) ** 2).mean(axis=1) + EPS)).astype(np.float32)
+    f = lambda a: a.astype(np.float64)  # noqa: E731
+    want, want_g, size, size_g = ref8.add_norm_grad(f(dy), f(s), f(r), f(gamma), np.zeros((n, d)))
+    dx, dg = ng.ngram_add_norm_grad(dev(dy, dtype), dev(s, BF), dev(r), dev(gamma))
+    assert np.all(np.abs(host(dx) - want) <= ref8.bf16_half_step(want) * (1 + 2.0 ** -7) + 50 * U * size)
+    # a column's sum: every 128th row by one thread, joins of 4 and 32, two roundings a term; with two launches up to 512 partial sums
+    assert np.all(np.abs(host(dg) - want_g) <= 560 * U * size_g)
+    if dtype == BF:
+        own = dev(dy, BF)
+        again, dg2 = ng.ngram_add_norm_grad(own, dev(s, BF), dev(r), dev(gamma), dx_out=own)
+        assert torch.equal(again, dx)
+        assert np.all(np.abs(host(dg2) - want_g) <= 560 * U * size_g)
+
+
 def test_no_rows():
     say("no rows")
     d = 264
