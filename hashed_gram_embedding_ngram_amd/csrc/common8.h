@@ -69,12 +69,13 @@ __device__ __forceinline__ float wave_sum(float x) {
     return (a + b) + (c + d);
 }
 
-// fp32 to bf16, nearest, ties to even; NaN to 0x7FC0.
-__device__ __forceinline__ uint32_t bf16_bits(float x) {
-    const uint32_t u = __float_as_uint(x);
-    return (u & 0x7FFFFFFFu) > kInfBits ? 0x7FC0u : (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+// Two fp32 values to bf16, nearest, ties to even, in one instruction (for all
+// 2^32 values the same bits as rounding by hand; a NaN stays a NaN).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) { return bf16_bits(lo) | bf16_bits(hi) << 16; }
 __device__ __forceinline__ float bf16_lo(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
 

@@ -127,13 +127,16 @@ struct Tile {
     static constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN, Waves = WM * WN, Threads = 64 * Waves;
     static constexpr int Rows = BM + BN;
     static constexpr int Stage = Rows * kStep;                  // bytes of one operand buffer
-    static constexpr int ScaleStage = Rows * 4;                 // bytes of one scale buffer: four steps
+    static constexpr int ScaleLoads = (Rows + Threads - 1) / Threads;       // instructions per wavefront and four steps
+    static constexpr int ScaleStage = (Rows + 63) / 64 * 256;         // bytes of one scale buffer: four steps
     static constexpr int ScaleBuffers = 4;      // the item's steps, NS ahead at most, touch no more groups of four
     static constexpr int Lds = NS * Stage + ScaleBuffers * ScaleStage;
-    static constexpr int LoadsA = BM / 8 / Waves, LoadsB = BN / 8 / Waves, Loads = LoadsA + LoadsB;     // instructions per wavefront and step
-    static_assert(BM % 64 == 0 && BN % 64 == 0 && LoadsA % 2 == 0 && LoadsB % 2 == 0 && Rows / 64 <= Waves, "tile shape");
-    static_assert(TM % 2 == 0 && TN % 2 == 0, "fragments are stored in pairs");
+    static constexpr int Tail = TN > 4 ? 1 : 2;                 // rows of fragments multiplied after a step's barrier
+    // load instructions per wavefront and step, 8 rows each; B's last may be some wavefronts' only
+    static constexpr int LoadsA = BM / 8 / Waves, LoadsB = (BN / 8 + Waves - 1) / Waves, Loads = LoadsA + LoadsB;
+    static_assert(BM % (8 * Waves) == 0 && Waves % 2 == 0, "tile shape");
     static_assert(NS >= 2 && NS <= 4 && Lds <= 160 * 1024, "buffers");
+    static_assert(NS == 2 || BN % (8 * Waves) == 0, "counted waits need every wavefront's loads alike");
 };
 
 // Work item w of the launch's order: workgroup b runs on XCD b mod 8 and takes
@@ -194,13 +197,17 @@ __device__ __forceinline__ void store_tile(const ProjArgs& a, const f32x4 (&acc)
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < TN; j += 2) {
+            for (int j = 0; j + 1 < TN; j += 2) {
                 const f32x4 x = acc[s][j], y = acc[s][j + 1];
                 const auto p = __builtin_amdgcn_permlane16_swap(bf16_pair(x[0], x[1]), bf16_pair(y[0], y[1]), false, false);
                 const auto q = __builtin_amdgcn_permlane16_swap(bf16_pair(x[2], x[3]), bf16_pair(y[2], y[3]), false, false);
                 const int64_t col = n0 + 16 * j + 16 * (g & 1) + 8 * (g >> 1);
                 if (row < a.m && col < a.n)
                     *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.c) + row * a.n + col) = u32x4{p[0], q[0], p[1], q[1]};
+            }
+            if (TN % 2 == 1) {
+                const int64_t col = n0 + 16 * (TN - 1) + 4 * g;
+                if (row < a.m && col < a.n) store4<false>(a.c, row * a.n + col, acc[s][TN - 1]);
             }
         }
     }
@@ -220,16 +227,17 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
 
     // Loads run ahead of the products, through the end of an item into the next.
     //
-    // Operands: wavefront v fills row groups v LoadsA .. of the A tile and v
-    // LoadsB .. of the B tile, 8 rows an instruction; every other group has
-    // the same swizzle.  Rows past M or N are clamped to the last row (their
+    // Operands: wavefront v fills row groups v, v + Waves, .. of the A tile
+    // and of the B tile, 8 rows an instruction; every other group has the
+    // same swizzle, so all of a wavefront's do.  Rows past M or N are clamped to the last row (their
     // results are never stored): the limit is that row's offset.  Scales:
     // thread t < Rows brings the word of row t of [A tile | B tile].
     const uint32_t ld = static_cast<uint32_t>(a.ld);
-    const uint32_t chunk0 = 16u * ((lane & 7) ^ (lane >> 4)), flip = (chunk0 ^ 64u) - chunk0;
-    const uint32_t off_a = (8 * wave * T::LoadsA + (lane >> 3)) * ld + chunk0, off_b = (8 * wave * T::LoadsB + (lane >> 3)) * ld + chunk0;
+    const uint32_t chunk = 16u * ((lane & 7) ^ (lane >> 4) ^ 4 * (wave & 1));
+    const uint32_t off = (8 * wave + (lane >> 3)) * ld + chunk;
     uint8_t* const sbuf = lds + NS * T::Stage;
-    const uint8_t *pa, *pb, *ps;        // the load step's first rows; the thread's scale byte of it
+    const uint8_t *pa, *pb, *ps[T::ScaleLoads];     // the load step's first rows, the first of its scale bytes
+    uint32_t soff[T::ScaleLoads];                   // from there to the thread's
     uint32_t last_a, last_b;            // offsets of the tiles' last rows
     int ahead, left;                    // the load step in its item, steps left with it
     int put_to = -1;                    // the scale buffer loaded last
@@ -241,9 +249,14 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
         last_b = (static_cast<uint32_t>(min(a.n - n0, static_cast<int64_t>(T::BN))) - 1) * ld;
         pa = a.a + m0 * a.ld + k0 * kStep;
         pb = a.b + n0 * a.ld + k0 * kStep;
-        const bool sa = t < T::BM;
-        const int64_t row = sa ? min(m0 + t, a.m - 1) : min(n0 + t - T::BM, a.n - 1);
-        ps = (sa ? a.as : a.bs) + (row >> (sa ? a.ash : a.bsh)) * a.sld + k0;
+#pragma unroll
+        for (int q = 0; q < T::ScaleLoads; ++q) {
+            const bool sa = (q * T::Waves + wave) * 64 < T::BM;
+            const int64_t first = sa ? m0 : n0, row = min(first + t + q * T::Threads - (sa ? 0 : T::BM), (sa ? a.m : a.n) - 1);
+            const int shift = sa ? a.ash : a.bsh;
+            ps[q] = (sa ? a.as : a.bs) + (first >> shift) * a.sld + k0;
+            soff[q] = static_cast<uint32_t>((row >> shift) - (first >> shift)) * static_cast<uint32_t>(a.sld);
+        }
         ahead = 0;
         left = steps_of(it);
     };
@@ -251,7 +264,8 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
         if (--left > 0) {
             pa += kStep;
             pb += kStep;
-            ps += 1;
+#pragma unroll
+            for (int q = 0; q < T::ScaleLoads; ++q) ps[q] += 1;
             ++ahead;
             return;
         }
@@ -264,21 +278,24 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
             left = 1;
         }
     };
-    const auto load = [&](const uint8_t* s, uint32_t off, uint32_t last, uint8_t* to, int q) {
-        const uint32_t at = min(off + 8 * q * ld, last + chunk0) + (q & 1 ? flip : 0u);     // modulo 2^32: flip may be -64
+    const auto load = [&](const uint8_t* s, uint32_t last, uint8_t* to, int q) {
+        const uint32_t at = min(off + 8 * T::Waves * q * ld, last + chunk);
         __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(s + at),
-                                         (__attribute__((address_space(3))) void*)(to + q * 1024), 16, 0, 0);
+                                         (__attribute__((address_space(3))) void*)(to + (q * T::Waves + wave) * 1024), 16, 0, 0);
     };
-    const auto load_a = [&](int buffer, int q) { load(pa, off_a, last_a, lds + buffer * T::Stage + wave * T::LoadsA * 1024, q); };
+    const auto load_a = [&](int buffer, int q) { load(pa, last_a, lds + buffer * T::Stage, q); };
     const auto load_b = [&](int buffer, int q) {
-        load(pb, off_b, last_b, lds + buffer * T::Stage + T::BM * kStep + wave * T::LoadsB * 1024, q);
+        if ((q + 1) * T::Waves <= T::BN / 8 || q * T::Waves + wave < T::BN / 8)
+            load(pb, last_b, lds + buffer * T::Stage + T::BM * kStep, q);
     };
     const auto load_scales = [&] {      // ahead of a step's other loads
         if ((ahead & 3) != 0) return;
         put_to = (put_to + 1) & (T::ScaleBuffers - 1);
-        if (wave < T::Rows / 64)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)ps,
-                                             (__attribute__((address_space(3))) void*)(sbuf + put_to * T::ScaleStage + wave * 256), 4, 0, 0);
+#pragma unroll
+        for (int q = 0; q < T::ScaleLoads; ++q)
+            if ((q * T::Waves + wave) * 64 < T::Rows)
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(ps[q] + soff[q]),
+                                                 (__attribute__((address_space(3))) void*)(sbuf + put_to * T::ScaleStage + (q * T::Waves + wave) * 256), 4, 0, 0);
     };
 
     // A lane reads chunks g and g + 4 (g = lane >> 4) of its fragment rows.
@@ -291,13 +308,10 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
     };
     const uint32_t a_row = wm * kStep, b_row = (T::BM + wn) * kStep;
     uint32_t sa[TM], sb[TN];
-    const auto scales = [&](int i, int buffer) {        // step i's bytes of this wavefront's rows
-        const uint8_t* const p = sbuf + buffer * T::ScaleStage + (i & 3) + lr * 4;
-#pragma unroll
-        for (int s = 0; s < TM; ++s) sa[s] = p[(wm + 16 * s) * 4];
-#pragma unroll
-        for (int s = 0; s < TN; ++s) sb[s] = p[(T::BM + wn + 16 * s) * 4];
-    };
+    const auto scales = [&](int i, int buffer) { return sbuf + buffer * T::ScaleStage + (i & 3) + lr * 4; };  // step i's
+    const uint8_t* sp = scales(0, 0);
+    const auto a_scale = [&](int s) -> uint32_t { return sp[(wm + 16 * s) * 4]; };
+    const auto b_scale = [&](int j) -> uint32_t { return sp[(T::BM + wn + 16 * j) * 4]; };
     f32x4 acc[TM][TN];
     const auto clear = [&] {
 #pragma unroll
@@ -335,9 +349,13 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
 #pragma unroll
         for (int q = 0; q < T::LoadsA; ++q) load_a(1, q);
     }
-    scales(0, 0);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) fb[j] = frag(lds + b_row, j);
+    for (int j = 0; j < TN; ++j) {
+        sb[j] = b_scale(j);
+        fb[j] = frag(lds + b_row, j);
+    }
+    sa[0] = a_scale(0);
+    sa[1] = a_scale(1);
     fa = frag(lds + a_row, 0);
     clear();
     int i = 0, steps = steps_of(now), read_from = 0;
@@ -353,9 +371,10 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
         // the step that frees the buffer, B's over the head of the next.
         i32x8 over;
 #pragma unroll
-        for (int s = 0; s < TM - 2; ++s) {
+        for (int s = 0; s < TM - T::Tail; ++s) {
             next = frag(at, s + 1);
-            if (s == TM - 3) over = frag(at, TM - 1);
+            if (T::Tail == 2 && s == TM - 3) over = frag(at, TM - 1);
+            if (s + 2 < TM) sa[s + 2] = a_scale(s + 2);
             const Wide xw = wide(fa, sa[s]);
 #pragma unroll
             for (int j = 0; j < TN; ++j) times(s, j, fa, xw, sa[s], sb[j]);
@@ -364,8 +383,8 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
             // group's are issued behind it
             if (!F32) {
                 __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                if (s == TM - 3) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-                else __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+                if (s == TM - 3) __builtin_amdgcn_sched_group_barrier(0x100, T::Tail == 2 ? 5 : 3, 0);
+                else __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
                 __builtin_amdgcn_sched_group_barrier(0x008, TN - 1, 0);
             }
             pin<TN>(acc[s]);
@@ -373,32 +392,33 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
 #pragma unroll
                 for (int q = s * T::LoadsB / 2; q < (s + 1) * T::LoadsB / 2; ++q) load_b(after, q);
         }
-        if (TM == 2) over = frag(at, 1);
         if (Two) step_on();
         // the next step's loads have landed: NS - 2 later steps' may be in flight
         __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((NS - 2) * T::Loads) : "memory");
         __builtin_amdgcn_s_barrier();
         __asm__ volatile("" ::: "memory");
-        const uint32_t tx = sa[TM - 2], ty = sa[TM - 1];
-        uint32_t tb[TN];
-#pragma unroll
-        for (int s = 0; s < TN; ++s) tb[s] = sb[s];
         const int to = ++i < steps ? i : 0;
         if ((to & 3) == 0) read_from = (read_from + 1) & (T::ScaleBuffers - 1);
-        scales(to, read_from);
+        sp = scales(to, read_from);
         // A step's last two row fragments (fa, over) are multiplied after
         // the barrier that ends its reads, while the next step's first
         // fragments are on their way.
         const uint8_t* const nt = lds + after * T::Stage;
         const i32x8 first = frag(nt + a_row, 0);
-        const Wide xw = wide(fa, tx), yw = wide(over, ty);
+        const Wide xw = wide(fa, sa[TM - T::Tail]), yw = wide(over, sa[TM - 1]);
+        uint32_t s0, s1;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            times(TM - 2, j, fa, xw, tx, tb[j]);
-            times(TM - 1, j, over, yw, ty, tb[j]);
+            times(TM - T::Tail, j, fa, xw, sa[TM - T::Tail], sb[j]);
+            if (T::Tail == 2) times(TM - 1, j, over, yw, sa[TM - 1], sb[j]);
+            pin<1>(&acc[TM - T::Tail][j]);
+            if (T::Tail == 2) pin<1>(&acc[TM - 1][j]);
             fb[j] = frag(nt + b_row, j);
-            pin<1>(&acc[TM - 2][j]);
-            pin<1>(&acc[TM - 1][j]);
+            sb[j] = b_scale(j);
+            if (j == 0) {
+                s0 = a_scale(0);
+                s1 = a_scale(1);
+            }
             if (j == 0) load_scales();
 #pragma unroll
             for (int q = j * T::LoadsA / TN; q < (j + 1) * T::LoadsA / TN; ++q) load_a(buffer, q);
@@ -408,6 +428,8 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
         }
         if (!Two) step_on();
         fa = first;
+        sa[0] = s0;
+        sa[1] = s1;
         buffer = after;
         if (i < steps) continue;
         store_tile<TM, TN, F32>(a, acc, static_cast<int64_t>(now.mt) * T::BM + wm, static_cast<int64_t>(now.nt) * T::BN + wn, now.split, lane);
@@ -632,7 +654,7 @@ __global__ void __launch_bounds__(64 * kRowWaves) project_fp8_rows_kernel(const 
 // ---------------------------------------------------------------------------
 // Which kernel, tile and split.
 struct Plan {
-    int kind;           // 0: few rows; 1: 64 x 64; 2: 128 x 128; 3: 256 x 256 (fp32: 256 x 128)
+    int kind;           // 0: few rows; 1: 64 x 64; 2: 128 x 128; 3: 256 x 256 (fp32: 256 x 128); 4: 256 x 320 (bf16 only)
     int splits;
     int split_steps;    // a multiple of 4
 };
@@ -644,18 +666,21 @@ constexpr int64_t kRows = 32;   // most rows of A for the few-rows kernel (64 ro
 // ceil(items / 256) rounds of one item's time, and an item's time is nearly a fixed
 // part plus a part per step.  Measured on MI355X at 16 to 32768 rows (us, bf16 /
 // fp32 result): 64 x 64: 3 + 0.23 / 0.32 a step; 128 x 128: 4 + 0.53 / 0.9;
-// the large tile 8 + 1.4 / 1.5.  At 2560 x 2560 the large tile wins from about 4000
-// rows (36 against 45 us), 128 x 128 from about 600 (1024 rows: 16 against 24).  Splitting K
-// pays where tiles are few and K is long; it costs a second launch and the
-// partial sums' way through memory.
+// the large tiles 8 + 1.5 (256 x 256), 13 + 1.75 (256 x 320), fp32 8 + 1.5.  At 2560 x
+// 2560 the large tiles win from about 4000 rows (36 against 45 us), 128 x 128
+// from about 600 (1024 rows: 16 against 24).  256 x 320 has the better rate where
+// it fills its rounds: 8192 x 2560 x 2560 is one round of 256 tiles, 52 us, or
+// 320 tiles of 256 x 256 in two rounds, 69; 8192 x 8192 x 8192 is 832 in four
+// rounds, 487 us, or 1024 in four, 450.  Splitting K pays where tiles are few
+// and K is long; it costs a second launch and the partial sums' way through memory.
 Plan plan_of(int64_t m, int64_t n, int64_t k, bool f32) {
     const int steps = static_cast<int>(blocks_of(k));
     Plan best{0, 1, (steps + 3) / 4 * 4};
     if (m <= kRows) return best;
-    const double fixed[3] = {3, 4, 8}, step16[3] = {0.23, 0.53, 1.4}, step32[3] = {0.32, 0.9, 1.5};
-    const int64_t rows[3] = {64, 128, 256}, cols[3] = {64, 128, f32 ? 128 : 256};
+    const double fixed[4] = {3, 4, 8, 13}, step16[4] = {0.23, 0.53, 1.5, 1.75}, step32[4] = {0.32, 0.9, 1.5, 0};
+    const int64_t rows[4] = {64, 128, 256, 256}, cols[4] = {64, 128, f32 ? 128 : 256, 320};
     double least = 0;
-    for (int kind = 1; kind <= 3; ++kind) {
+    for (int kind = 1; kind <= (f32 ? 3 : 4); ++kind) {
         const int64_t tiles = ((m + rows[kind - 1] - 1) / rows[kind - 1]) * ((n + cols[kind - 1] - 1) / cols[kind - 1]);
         int before = 0;
         for (int want = 1; want <= 32; ++want) {
@@ -767,8 +792,10 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
         rc = f32 ? launch_small<SmallTile<2, 2, 2, 2, 4, true>>(a, stream) : launch_small<SmallTile<2, 2, 2, 2, 4, false>>(a, stream);
     } else if (p.kind == 2) {
         rc = f32 ? launch_small<SmallTile<4, 4, 2, 2, 2, true>>(a, stream) : launch_small<SmallTile<4, 4, 2, 2, 2, false>>(a, stream);
-    } else {
+    } else if (p.kind == 3) {
         rc = f32 ? launch_tile<Tile<4, 4, 4, 2, 3, true>>(a, stream) : launch_tile<Tile<8, 4, 2, 4, 2, false>>(a, stream);
+    } else {
+        rc = launch_tile<Tile<8, 5, 2, 4, 2, false>>(a, stream);
     }
     if (rc) return rc;
     if (a.splits > 1) {
