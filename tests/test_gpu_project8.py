@@ -60,6 +60,14 @@ def test_product(m, n, k, dtype):
         check(m, n, k, a, b, tile, dtype)
 
 
+@pytest.mark.parametrize("m,n,k", [(7900, 2552, 136), (8192, 2560, 100), (4090, 5000, 1032), (16300, 2552, 640), (2500, 7672, 1544)])
+def test_many_rows_and_columns(m, n, k):
+    """Results that fill the card's rounds with the largest tiles, with ragged edges; one, few and many steps of K."""
+    say(f"large product {m} x {n} x {k}")
+    a, b = operands(np.random.default_rng(m + n + k), m, n, k, False)
+    check(m, n, k, a, b, False, BF)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("m,n,k", [(136, 264, 16392), (264, 520, 5000), (520, 264, 4097), (72, 8, 8200)])
 def test_long_k_is_split(m, n, k, dtype):
