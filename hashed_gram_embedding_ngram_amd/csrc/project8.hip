@@ -110,14 +110,17 @@ __device__ __forceinline__ void store4(void* c, int64_t at, f32x4 v) {
 // Scales go through LDS as well: a row's word of four steps' bytes with the
 // first of the four, and a byte read for each fragment and step.
 //
-// Measured: bf16 results (256 x 256 tiles) 32768 x 2560 x 2560 197 to 201 us,
-// 2.1 to 2.2 PFLOP/s; 8192 x 8192 x 8192 449 us, 2.45 PFLOP/s.  The matrix
-// cores are busy half of the time at the 2.0 GHz that the card holds under
-// this load; products alone, on random codes, stop at 3.9 to 4.0 PFLOP/s.  A
-// step is bound by the way of its 64 KB from L2 through one barrier rather
-// than by its products (tiles of 256 x 160 and 256 x 192 have nearly the same
-// time a step), and a tile's 128 KB of stores, all at once, take another 15%.
-// fp32 results (256 x 128 tiles) 2560 x 2560 x 8192 97 to 105 us, 1.0 to 1.1
+// Measured: bf16 results 32768 x 2560 x 2560 181 us, 2.4 PFLOP/s, and 8192 x
+// 2560 x 2560 49 to 53 us, 2.0 to 2.2 (256 x 320 tiles); 8192 x 8192 x 8192
+// 440 us, 2.5 PFLOP/s (256 x 256).  Products alone, on random codes, stop at 3.9
+// to 4.0 PFLOP/s: the card holds about 2.0 GHz under this load.  A step is bound
+// by LDS and the matrix cores together: 256 x 256 reads 192 KB of fragments
+// and has 64 KB brought in, 2000 cycles at 128 bytes a cycle, beside 2048 of
+// products, and takes about 3400 (without the products 2500).  Hence the
+// largest tile a wavefront can hold, 128 x 80: 13 fragments for 40 products,
+// where 128 x 64 has 12 for 32.  A round's stores, 128 or 160 KB a unit, all
+// at once, take 10 to 15%.
+// fp32 results (256 x 128 tiles) 2560 x 2560 x 8192 97 to 110 us, 1.0 to 1.1
 // PFLOP/s of the 1.3 that a large bf16 product reaches: 200 tiles for 256
 // compute units.
 template <int TM_, int TN_, int WM_, int WN_, int NS_, bool F32_>
@@ -129,9 +132,9 @@ struct Tile {
     static constexpr int Stage = Rows * kStep;                  // bytes of one operand buffer
     static constexpr int ScaleLoads = (Rows + Threads - 1) / Threads;       // instructions per wavefront and four steps
     static constexpr int ScaleStage = (Rows + 63) / 64 * 256;         // bytes of one scale buffer: four steps
-    static constexpr int ScaleBuffers = 4;      // the item's steps, NS ahead at most, touch no more groups of four
+    static constexpr int ScaleBuffers = 4;      // a step and the NS that are loaded ahead of it touch no more groups of four
     static constexpr int Lds = NS * Stage + ScaleBuffers * ScaleStage;
-    static constexpr int Tail = TN > 4 ? 1 : 2;                 // rows of fragments multiplied after a step's barrier
+    static constexpr int Tail = TN > 4 ? 1 : 2;     // rows of fragments multiplied after a step's barrier (no registers for two with TN = 5)
     // load instructions per wavefront and step, 8 rows each; B's last may be some wavefronts' only
     static constexpr int LoadsA = BM / 8 / Waves, LoadsB = (BN / 8 + Waves - 1) / Waves, Loads = LoadsA + LoadsB;
     static_assert(BM % (8 * Waves) == 0 && Waves % 2 == 0, "tile shape");
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
         if constexpr (F32)
 #pragma unroll
             for (int j = 0; j < TN; ++j) wb[j] = widen(fb[j], sb[j]);
-        // Rows 0 .. TM - 3.  A load instruction takes the wavefront's turn
+        // Rows 0 .. TM - Tail - 1.  A load instruction takes the wavefront's turn
         // for as long as the CU's one load path needs for it (16 cycles or
         // more), so the large tile's loads are spread: A's over the tail of
         // the step that frees the buffer, B's over the head of the next.
@@ -400,9 +403,10 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
         const int to = ++i < steps ? i : 0;
         if ((to & 3) == 0) read_from = (read_from + 1) & (T::ScaleBuffers - 1);
         sp = scales(to, read_from);
-        // A step's last two row fragments (fa, over) are multiplied after
-        // the barrier that ends its reads, while the next step's first
-        // fragments are on their way.
+        // A step's last row fragments (fa, over) are multiplied after the
+        // barrier that ends its reads, while the next step's first fragments
+        // are on their way.  A B fragment and its scale are read again only
+        // behind their last product: no registers for both.
         const uint8_t* const nt = lds + after * T::Stage;
         const i32x8 first = frag(nt + a_row, 0);
         const Wide xw = wide(fa, sa[TM - T::Tail]), yw = wide(over, sa[TM - 1]);
@@ -666,18 +670,19 @@ constexpr int64_t kRows = 32;   // most rows of A for the few-rows kernel (64 ro
 // ceil(items / 256) rounds of one item's time, and an item's time is nearly a fixed
 // part plus a part per step.  Measured on MI355X at 16 to 32768 rows (us, bf16 /
 // fp32 result): 64 x 64: 3 + 0.23 / 0.32 a step; 128 x 128: 4 + 0.53 / 0.9;
-// the large tiles 8 + 1.5 (256 x 256), 13 + 1.75 (256 x 320), fp32 8 + 1.5.  At 2560 x
+// the large tiles 8 + 1.5 (256 x 256), 12 + 1.75 (256 x 320), fp32 8 + 1.5.  At 2560 x
 // 2560 the large tiles win from about 4000 rows (36 against 45 us), 128 x 128
 // from about 600 (1024 rows: 16 against 24).  256 x 320 has the better rate where
 // it fills its rounds: 8192 x 2560 x 2560 is one round of 256 tiles, 52 us, or
-// 320 tiles of 256 x 256 in two rounds, 69; 8192 x 8192 x 8192 is 832 in four
-// rounds, 487 us, or 1024 in four, 450.  Splitting K pays where tiles are few
+// 320 tiles of 256 x 256 in two rounds, 69; 32768 rows are four rounds, 181 us,
+// or five, 190; but 8192 x 8192 x 8192 is 832 in four rounds, 472 us, or 1024
+// in four, 440.  Splitting K pays where tiles are few
 // and K is long; it costs a second launch and the partial sums' way through memory.
 Plan plan_of(int64_t m, int64_t n, int64_t k, bool f32) {
     const int steps = static_cast<int>(blocks_of(k));
     Plan best{0, 1, (steps + 3) / 4 * 4};
     if (m <= kRows) return best;
-    const double fixed[4] = {3, 4, 8, 13}, step16[4] = {0.23, 0.53, 1.5, 1.75}, step32[4] = {0.32, 0.9, 1.5, 0};
+    const double fixed[4] = {3, 4, 8, 12}, step16[4] = {0.23, 0.53, 1.5, 1.75}, step32[4] = {0.32, 0.9, 1.5, 0};
     const int64_t rows[4] = {64, 128, 256, 256}, cols[4] = {64, 128, f32 ? 128 : 256, 320};
     double least = 0;
     for (int kind = 1; kind <= (f32 ? 3 : 4); ++kind) {
