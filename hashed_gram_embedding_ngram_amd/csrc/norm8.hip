@@ -58,8 +58,8 @@ namespace {
 // in LDS.
 //
 // Bound by memory: 32768 x 2560 from bf16 (7 bytes an element with the 8-bit
-// output) 101 us, 5.8 TB/s, where a large copy reaches 5.5; 5003 x 1032 from
-// fp32 with everything kept 11.7 us, 4.8 TB/s; 4 x 2560 2.7 us, which is an
+// output) 102 us, 5.8 TB/s, where a large copy reaches 5.5; 5003 x 1032 from
+// fp32 with everything kept 10.9 us, 5.2 TB/s; 4 x 2560 2.7 us, which is an
 // empty launch and one dependent load.
 struct NormArgs {
     const void* x;
