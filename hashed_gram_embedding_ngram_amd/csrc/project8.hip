@@ -137,7 +137,7 @@ struct Tile {
     static constexpr int Tail = TN > 4 ? 1 : 2;     // rows of fragments multiplied after a step's barrier (no registers for two with TN = 5)
     // load instructions per wavefront and step, 8 rows each; B's last may be some wavefronts' only
     static constexpr int LoadsA = BM / 8 / Waves, LoadsB = (BN / 8 + Waves - 1) / Waves, Loads = LoadsA + LoadsB;
-    static_assert(BM % (8 * Waves) == 0 && Waves % 2 == 0, "tile shape");
+    static_assert(BM % (8 * Waves) == 0 && Waves % 2 == 0 && TM >= 4 && TM % 2 == 0, "tile shape");
     static_assert(NS >= 2 && NS <= 4 && Lds <= 160 * 1024, "buffers");
     static_assert(NS == 2 || BN % (8 * Waves) == 0, "counted waits need every wavefront's loads alike");
 };
@@ -182,20 +182,23 @@ __device__ __forceinline__ void pin(f32x4* acc) {
 // neighbouring tiles' values are exchanged between lane groups 0 and 1, 2 and
 // 3: then a lane has eight consecutive outputs of one of the two, and a store
 // writes 64 consecutive bytes of 16 rows (32-byte pieces took 8% more time for
-// the whole product at 32768 x 2560 x 2560).
+// the whole product at 32768 x 2560 x 2560).  An odd last tile is exchanged with
+// the one of the next 16 rows.
 template <int TM, int TN, bool F32>
-__device__ __forceinline__ void store_tile(const ProjArgs& a, const f32x4 (&acc)[TM][TN], int64_t m0, int64_t n0, int split, int lane) {
+__device__ __forceinline__ void store_tile(const ProjArgs& a, const f32x4 (&acc)[TM][TN], int m0, int n0, int split, int lane) {
+    const int m = static_cast<int>(a.m), n = static_cast<int>(a.n);     // at most 2^30
     const int lr = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int s = 0; s < TM; ++s) {
-        const int64_t row = m0 + 16 * s + lr;
+        const int row = m0 + 16 * s + lr;
+        const int64_t at = static_cast<int64_t>(row) * a.n;
         if (F32 || a.splits > 1) {
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                const int64_t col = n0 + 16 * j + 4 * g;
-                if (row < a.m && col < a.n) {
-                    if (a.splits > 1) store4<true>(a.partial, (split * a.m + row) * a.n + col, acc[s][j]);
-                    else store4<F32>(a.c, row * a.n + col, acc[s][j]);
+                const int col = n0 + 16 * j + 4 * g;
+                if (row < m && col < n) {
+                    if (a.splits > 1) store4<true>(a.partial, split * a.m * a.n + at + col, acc[s][j]);
+                    else store4<F32>(a.c, at + col, acc[s][j]);
                 }
             }
         } else {
@@ -204,13 +207,17 @@ __device__ __forceinline__ void store_tile(const ProjArgs& a, const f32x4 (&acc)
                 const f32x4 x = acc[s][j], y = acc[s][j + 1];
                 const auto p = __builtin_amdgcn_permlane16_swap(bf16_pair(x[0], x[1]), bf16_pair(y[0], y[1]), false, false);
                 const auto q = __builtin_amdgcn_permlane16_swap(bf16_pair(x[2], x[3]), bf16_pair(y[2], y[3]), false, false);
-                const int64_t col = n0 + 16 * j + 16 * (g & 1) + 8 * (g >> 1);
-                if (row < a.m && col < a.n)
-                    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.c) + row * a.n + col) = u32x4{p[0], q[0], p[1], q[1]};
+                const int col = n0 + 16 * j + 16 * (g & 1) + 8 * (g >> 1);
+                if (row < m && col < n)
+                    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.c) + at + col) = u32x4{p[0], q[0], p[1], q[1]};
             }
-            if (TN % 2 == 1) {
-                const int64_t col = n0 + 16 * (TN - 1) + 4 * g;
-                if (row < a.m && col < a.n) store4<false>(a.c, row * a.n + col, acc[s][TN - 1]);
+            if (TN % 2 == 1 && s % 2 == 1) {
+                const f32x4 x = acc[s - 1][TN - 1], y = acc[s][TN - 1];
+                const auto p = __builtin_amdgcn_permlane16_swap(bf16_pair(x[0], x[1]), bf16_pair(y[0], y[1]), false, false);
+                const auto q = __builtin_amdgcn_permlane16_swap(bf16_pair(x[2], x[3]), bf16_pair(y[2], y[3]), false, false);
+                const int r = row - 16 * (1 - (g & 1)), col = n0 + 16 * (TN - 1) + 8 * (g >> 1);
+                if (r < m && col < n)
+                    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.c) + static_cast<int64_t>(r) * a.n + col) = u32x4{p[0], q[0], p[1], q[1]};
             }
         }
     }
@@ -436,7 +443,7 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
         sa[1] = s1;
         buffer = after;
         if (i < steps) continue;
-        store_tile<TM, TN, F32>(a, acc, static_cast<int64_t>(now.mt) * T::BM + wm, static_cast<int64_t>(now.nt) * T::BN + wn, now.split, lane);
+        store_tile<TM, TN, F32>(a, acc, now.mt * T::BM + wm, now.nt * T::BN + wn, now.split, lane);
         w += a.stride;
         now = item_of(w, a);
         if (!now.valid) break;
@@ -588,7 +595,7 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_small_kernel(const 
 #pragma unroll
                 for (int j = 0; j < TN; ++j) acc[s][j] += part[(o * T::Waves + wave) * PerWave + (s * TN + j) * 64 + lane];
     }
-    store_tile<TM, TN, F32>(a, acc, m0 + wm, n0 + wn, it.split, lane);
+    store_tile<TM, TN, F32>(a, acc, it.mt * T::BM + wm, it.nt * T::BN + wn, it.split, lane);
 }
 
 // The sum of the splits' partial products, in their order: bound by memory,
