@@ -734,6 +734,13 @@ def _made(t, stream):
     return t
 
 
+def _new(rows, cols, dtype, device, stream):
+    """A contiguous [rows][cols] tensor for _made ([rows] where cols is
+    None); with its strides given, making it takes three quarters of the time."""
+    shape, strides = ((rows,), (1,)) if cols is None else ((rows, cols), (cols, 1))
+    return _made(torch.empty_strided(shape, strides, dtype=dtype, device=device), stream)
+
+
 def _value(t):
     """The ngram_value of a tensor that has been checked against _VALUES."""
     return F32 if t.dtype is torch.float32 else BF16
@@ -762,8 +769,8 @@ class Fp8:
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda:0", stream=None) -> "Fp8":
         ld, srows, sld = _fp8_shape(rows, cols, block_rows)
-        codes = _made(torch.empty((rows, ld), dtype=torch.float8_e4m3fn, device=device), stream)
-        scales = _made(torch.empty((srows, sld), dtype=torch.uint8, device=device), stream)
+        codes = _new(rows, ld, torch.float8_e4m3fn, device, stream)
+        scales = _new(srows, sld, torch.uint8, device, stream)
         self = cls.__new__(cls)
         self.rows, self.cols, self.block_rows, self.codes, self.scales = rows, cols, block_rows, codes, scales
         self.c = _Fp8(codes.data_ptr(), scales.data_ptr(), rows, cols, block_rows, 0)
@@ -820,9 +827,9 @@ def ngram_add_norm(x, gamma, eps, residual=None, sum_out=None, y_out=None, q_out
     if q_out is None and quantise:
         q_out = Fp8.empty(n, d, 1, x.device, stream)
     if y_out is None and keep_y:
-        y_out = _made(torch.empty((n, d), dtype=torch.bfloat16, device=x.device), stream)
+        y_out = _new(n, d, torch.bfloat16, x.device, stream)
     if r_out is None and keep_r:
-        r_out = _made(torch.empty(n, dtype=torch.float32, device=x.device), stream)
+        r_out = _new(n, None, torch.float32, x.device, stream)
     rc = lib().ngram_add_norm(px, _value(x), _opt(residual, _BF16, count, "residual"), n, d, pg, eps,
                               _opt(sum_out, _BF16, count, "sum_out"), _opt(y_out, _BF16, count, "y_out"), _fp8_c(q_out),
                               _opt(r_out, _F32, n, "r_out"), _raw_stream(stream))
@@ -835,7 +842,7 @@ def add_norm_grad_workspace(n: int, d: int, device="cuda:0"):
     nbytes = lib().ngram_add_norm_grad_workspace_bytes(n, d)
     if nbytes < 0:
         raise NgramError(f"no norm gradient has n={n}, d={d}")
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _new(nbytes, None, torch.uint8, device, None)
 
 
 def ngram_add_norm_grad(dy, sum, r, gamma, dsum=None, dx_out=None, dgamma_out=None, workspace=None, stream=None):
@@ -847,9 +854,9 @@ def ngram_add_norm_grad(dy, sum, r, gamma, dsum=None, dx_out=None, dgamma_out=No
     pdy = _arg(dy, _VALUES, count, "dy")
     ps, pr, pg = _arg(sum, _BF16, count, "sum"), _arg(r, _F32, n, "r"), _arg(gamma, _F32, d, "gamma")
     if dx_out is None:
-        dx_out = _made(torch.empty((n, d), dtype=torch.bfloat16, device=dy.device), stream)
+        dx_out = _new(n, d, torch.bfloat16, dy.device, stream)
     if dgamma_out is None:
-        dgamma_out = _made(torch.empty(d, dtype=torch.float32, device=dy.device), stream)
+        dgamma_out = _new(d, None, torch.float32, dy.device, stream)
     if workspace is None:
         workspace = _made(add_norm_grad_workspace(n, d, dy.device), stream)
     rc = lib().ngram_add_norm_grad(pdy, _value(dy), ps, pr, pg, _opt(dsum, _BF16, count, "dsum"), n, d,
@@ -874,7 +881,7 @@ def ngram_project_fp8(a: Fp8, b: Fp8, out=None, dtype=torch.bfloat16, workspace=
     (see ngram_project_fp8 in ngram.h)."""
     m, n = a.rows, b.rows
     if out is None:
-        out = _made(torch.empty((m, n), dtype=dtype, device=a.codes.device), stream)
+        out = _new(m, n, dtype, a.codes.device, stream)
     po = _arg(out, _VALUES, m * n, "out")
     if workspace is None:
         workspace = project_fp8_workspace(m, n, a.cols, out.dtype, out.device)
