@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) add_norm_kernel(c
 // Gradients of the norm: with h = gamma dy,
 //   dx = r h - s (r^3 / d) sum(h s) + dsum,   dgamma = sum over rows of dy s r.
 // A workgroup walks over rows, its wavefronts sharing each as in the wide
-// forward; a lane adds its columns' dgamma terms in registers, and one row of
+// forward (SLOTS: several narrow rows at once); a lane adds its columns' dgamma terms in registers, and one row of
 // partial sums per workgroup goes to the workspace for the kernel below.
 //
 // Bound by memory, 8 bytes an element: 32768 x 2560 in bf16 112 us, 6.0 TB/s
@@ -213,16 +213,21 @@ struct NormGradArgs {
     float* partial;     // [workgroups][d]
     int64_t n;
     int32_t d;
+    int32_t waves;      // of a row, where a workgroup takes several at once
     float inv_d;
 };
 
-template <int C, bool F32>
+template <int C, bool F32, bool SLOTS>
 __global__ void __launch_bounds__(64 * kMaxWaves) add_norm_grad_kernel(const NormGradArgs a) {
+    static_assert(C == 1 || !SLOTS, "narrow rows have one chunk a wavefront");
     __shared__ float part[2][kMaxWaves];
+    __shared__ __attribute__((aligned(16))) float joined[SLOTS ? kMaxWaves : 1][SLOTS ? kSlice : 4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int waves = blockDim.x >> 6;
-    const int c0 = wave * C;
+    const int waves = SLOTS ? a.waves : blockDim.x >> 6;
+    const int slots = SLOTS ? (blockDim.x >> 6) / waves : 1, slot = SLOTS ? wave / waves : 0;
+    const int first = slot * waves;     // the row's first wavefront
+    const int c0 = (wave - first) * C;
     float gam[C][8], acc[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -234,15 +239,17 @@ __global__ void __launch_bounds__(64 * kMaxWaves) add_norm_grad_kernel(const Nor
         for (int k = 0; k < 8; ++k) acc[c][k] = 0.0f;
     }
     int it = 0;
-    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x, ++it) {
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * slots; base < a.n; base += static_cast<int64_t>(gridDim.x) * slots, ++it) {
+        const int64_t row = base + slot;
+        const bool live = !SLOTS || row < a.n;
         Raw8<F32> dy[C];
         Raw8<false> s[C], ds[C];
         const int64_t at = row * a.d;
-        const float r = a.r[row];
+        const float r = live ? a.r[row] : 0.0f;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int col = (c0 + c) * kSlice + lane * kVec;
-            if (col < a.d) {
+            if (live && col < a.d) {
                 dy[c].load(a.dy, at + col);
                 s[c].load(a.sum, at + col);
                 if (a.dsum) ds[c].load(a.dsum, at + col); else ds[c].zero();
@@ -273,7 +280,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) add_norm_grad_kernel(const Nor
         if (lane == 0) p[wave] = dot;
         __syncthreads();
         dot = 0.0f;
-        for (int w = 0; w < waves; ++w) dot += p[w];
+        for (int w = 0; w < waves; ++w) dot += p[first + w];
         const float f = dot * r * r * r * a.inv_d;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -293,8 +300,18 @@ __global__ void __launch_bounds__(64 * kMaxWaves) add_norm_grad_kernel(const Nor
                 }
                 packed[k] = bf16_pair(o[0], o[1]);
             }
-            if (col < a.d) put<true>(a.dx + at + col, packed);
+            if (live && col < a.d) put<true>(a.dx + at + col, packed);
         }
+    }
+    if constexpr (SLOTS) {              // the rows' sums, in the order of the slots
+        float* const mine = joined[wave] + lane * kVec;
+        *reinterpret_cast<f32x4*>(mine) = f32x4{acc[0][0], acc[0][1], acc[0][2], acc[0][3]};
+        *reinterpret_cast<f32x4*>(mine + 4) = f32x4{acc[0][4], acc[0][5], acc[0][6], acc[0][7]};
+        __syncthreads();
+        if (slot > 0) return;
+        for (int s = 1; s < slots; ++s)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[0][k] += joined[s * waves + wave][lane * kVec + k];
     }
     float* const out = a.partial + static_cast<int64_t>(blockIdx.x) * a.d;
 #pragma unroll
@@ -657,6 +674,16 @@ RowShape grad_shape(int64_t n, int d) {
     return s;
 }
 
+// Rows that a workgroup of the gradient takes at once: narrow rows alone would
+// leave too few wavefronts to the chip.  One row / several, us: 200,000 x 136
+// 357 / 57, 32768 x 512 70 / 29, 32768 x 1024 81 / 51, 6024 x 120 14.9 / 7.9, 4000 x
+// 1032 (fp32) 16.1 / 13.8 (two rows; five 15.9), 32768 x 2048 101 / 98, 8192 x
+// 2048 (fp32) 34.0 / 35.1; at 2560 columns three rows take 128 us for one's 116.
+int grad_slots(int64_t n, const RowShape& s) {
+    const int most = s.waves <= 2 ? kMaxWaves / s.waves : s.waves <= 4 ? 2 : 1;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, (n + s.grid - 1) / s.grid)));
+}
+
 template <bool F32, bool WIDE, bool STREAM>
 void launch_norm(int chunks, dim3 grid, dim3 block, hipStream_t st, const NormArgs& a) {
 #define NG8_CASE(C) case C: hipLaunchKernelGGL((add_norm_kernel<C, F32, WIDE, STREAM>), grid, block, 0, st, a); break
@@ -667,8 +694,9 @@ void launch_norm(int chunks, dim3 grid, dim3 block, hipStream_t st, const NormAr
 
 template <bool F32>
 void launch_norm_grad(int chunks, dim3 grid, dim3 block, hipStream_t st, const NormGradArgs& a) {
-#define NG8_CASE(C) case C: hipLaunchKernelGGL((add_norm_grad_kernel<C, F32>), grid, block, 0, st, a); break
-    switch (chunks) { NG8_CASE(1); NG8_CASE(2); NG8_CASE(3); NG8_CASE(4); NG8_CASE(5); NG8_CASE(6); NG8_CASE(7); default: NG8_CASE(8); }
+#define NG8_CASE(C) case C: hipLaunchKernelGGL((add_norm_grad_kernel<C, F32, false>), grid, block, 0, st, a); break
+    if (static_cast<int>(block.x) > 64 * a.waves) hipLaunchKernelGGL((add_norm_grad_kernel<1, F32, true>), grid, block, 0, st, a);
+    else switch (chunks) { NG8_CASE(1); NG8_CASE(2); NG8_CASE(3); NG8_CASE(4); NG8_CASE(5); NG8_CASE(6); NG8_CASE(7); default: NG8_CASE(8); }
 #undef NG8_CASE
 }
 
@@ -770,6 +798,7 @@ int ngram_add_norm_grad(const void* dy, int32_t dy_dtype, const uint16_t* sum, c
     if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
         return fail(NGRAM_EINVAL, "workspace must hold %lld bytes, 16-byte aligned", (long long)need);
     NormGradArgs a;
+    a.waves = 0;
     a.dy = dy; a.sum = sum; a.r = r; a.gamma = gamma; a.dsum = dsum; a.dx = dx_out;
     a.partial = static_cast<float*>(workspace);
     a.n = n; a.d = d;
@@ -783,7 +812,8 @@ int ngram_add_norm_grad(const void* dy, int32_t dy_dtype, const uint16_t* sum, c
         else hipLaunchKernelGGL((add_norm_grad_few_kernel<false>), few, threads, 0, stream, f);
         return hip_status("ngram_add_norm_grad launch");
     }
-    const dim3 grid(static_cast<unsigned>(s.grid)), block(64 * s.waves);
+    const dim3 grid(static_cast<unsigned>(s.grid)), block(64 * s.waves * grad_slots(n, s));
+    a.waves = s.waves;
     if (dy_dtype == NGRAM_F32) launch_norm_grad<true>(s.chunks, grid, block, stream, a);
     else launch_norm_grad<false>(s.chunks, grid, block, stream, a);
     hipLaunchKernelGGL(column_sum_kernel, dim3((d + 63) / 64), dim3(1024), 0, stream, a.partial,

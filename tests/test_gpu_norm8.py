@@ -205,6 +205,24 @@ def test_add_norm_grad_at_the_edge_of_few_rows(n, d, dtype):
         assert np.all(np.abs(host(dg2) - want_g) <= 560 * U * size_g)
 
 
+@pytest.mark.parametrize("n,d", [(20001, 8), (9001, 136), (6024, 520), (5003, 1032), (2049, 1544), (1030, 2048), (1100, 1000)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_add_norm_grad_of_many_narrow_rows(n, d, dtype):
+    """A workgroup takes several narrow rows at once, the last of them past the end."""
+    say(f"add_norm_grad, narrow rows n={n} d={d} {dtype}")
+    rng = np.random.default_rng(5 * n + d)
+    s, dsum = rounded(hidden(rng, n, d), BF), rounded(rng.normal(size=(n, d)) * 0.01, BF)
+    dy = rounded(rng.normal(size=(n, d)) * 0.01, dtype)
+    gamma = (1 + 0.2 * rng.normal(size=d)).astype(np.float32)
+    r = (1 / np.sqrt((s.astype(np.float64) ** 2).mean(axis=1) + EPS)).astype(np.float32)
+    f = lambda a: a.astype(np.float64)  # noqa: E731
+    want, want_g, size, size_g = ref8.add_norm_grad(f(dy), f(s), f(r), f(gamma), f(dsum))
+    dx, dg = ng.ngram_add_norm_grad(dev(dy, dtype), dev(s, BF), dev(r), dev(gamma), dsum=dev(dsum, BF))
+    assert np.all(np.abs(host(dx) - want) <= ref8.bf16_half_step(want) * (1 + 2.0 ** -7) + 50 * U * size)
+    # a column's sum: the rows of one wavefront, up to 16 slots, then at most 512 partial sums
+    assert np.all(np.abs(host(dg) - want_g) <= (ref8.ceil_div(n, 512) + 556) * U * size_g)
+
+
 def test_no_rows():
     say("no rows")
     d = 264
