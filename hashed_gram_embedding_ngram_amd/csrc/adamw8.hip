@@ -290,9 +290,9 @@ __global__ void __launch_bounds__(256) adamw_kernel(const AdamArgs a) {
 }
 
 // The step on rows rows[0 .. *count) of a [R][d] table from their gradients
-// g[u][d].  A wavefront owns one 512-column chunk of one row; the launch
-// covers max_rows rows and the wavefronts past *count leave at once, so the
-// count stays on the device.
+// g[u][d].  16 lanes own a block of 128 columns of one row; the launch covers
+// max_rows rows and the lanes past *count leave at once, so the count stays on
+// the device.
 struct RowsArgs {
     void* p;
     void* m;
@@ -305,26 +305,24 @@ struct RowsArgs {
     int64_t max_rows;
     int64_t R;
     int32_t d;
-    int32_t chunks;
-    int32_t nb;
+    int32_t nb;         // blocks of 128 columns in a row
     StepConst c;
 };
 
 template <bool P32, bool G32, bool S8>
 __global__ void __launch_bounds__(256) adamw_rows_kernel(const RowsArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t u = unit / a.chunks;
+    const uint32_t unit = blockIdx.x * 16 + (threadIdx.x >> 4), nb = static_cast<uint32_t>(a.nb);
+    const uint32_t u = unit / nb;
     const int64_t count = a.count ? min(*a.count, a.max_rows) : a.max_rows;
     if (u >= count) return;
     const int64_t row = a.rows[u];
     if (row < 0 || row >= a.R) return;
-    const int col = static_cast<int>(unit - u * a.chunks) * kSlice + lane * kVec;
+    const int col = static_cast<int>(unit - u * nb) * kBlock + static_cast<int>(threadIdx.x & 15) * kVec;
     const bool live = col < a.d;
     const int64_t at = row * a.d + col;
     Eight<P32, G32, S8> e;
     if (live) {
-        e.g.load_stream(a.g, u * a.d + col);
+        e.g.load_stream(a.g, static_cast<int64_t>(u) * a.d + col);
         e.p.load_stream(a.p, at);
         if (S8) {
             e.mc = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.m) + at));
@@ -350,7 +348,7 @@ __global__ void __launch_bounds__(256) adamw_rows_kernel(const RowsArgs a) {
     if (S8) {
         __builtin_nontemporal_store(e.mc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.m) + at));
         __builtin_nontemporal_store(e.vc, reinterpret_cast<u32x2*>(static_cast<uint8_t*>(a.v) + at));
-        if ((lane & 15) == 0) {
+        if ((threadIdx.x & 15) == 0) {
             a.ms[row * a.nb + (col >> 7)] = static_cast<uint8_t>(e.ms);
             a.vs[row * a.nb + (col >> 7)] = static_cast<uint8_t>(e.vs);
         }
@@ -485,10 +483,9 @@ int ngram_adamw_rows(const ngram_adamw_tensor* table, int64_t R, int32_t d, cons
         return fail(NGRAM_EALIGN, "p, g and fp32 moments must be 16-byte aligned, 8-bit moments and n_rows 8-byte, rows 4-byte");
     a.p = table->p; a.m = table->m; a.v = table->v; a.ms = table->m_scale; a.vs = table->v_scale;
     a.rows = rows; a.g = table->g; a.count = n_rows; a.max_rows = max_rows; a.R = R; a.d = d;
-    a.chunks = (d + kSlice - 1) / kSlice;
     a.nb = static_cast<int32_t>(blocks_of(d));
-    if (max_rows > INT32_MAX / a.chunks) return fail(NGRAM_ERANGE, "max_rows=%lld too large for one launch", (long long)max_rows);
-    const dim3 grid(static_cast<unsigned>((max_rows * a.chunks + 3) / 4)), block(256);
+    if (max_rows > INT32_MAX / a.nb) return fail(NGRAM_ERANGE, "max_rows=%lld too large for one launch", (long long)max_rows);
+    const dim3 grid(static_cast<unsigned>((max_rows * a.nb + 15) / 16)), block(256);
 #define NG8_ROWS(P, G, S) hipLaunchKernelGGL((adamw_rows_kernel<P, G, S>), grid, block, 0, stream, a)
     NG8_BY_KIND(kind_of(table->p_dtype, table->g_dtype, table->state), NG8_ROWS)
 #undef NG8_ROWS
