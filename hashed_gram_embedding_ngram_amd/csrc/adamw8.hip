@@ -8,7 +8,7 @@
 // moves.  Everything is read and written once, so all of it goes past the
 // caches' usual keeping (260,000 rows of 2560: 1670-1700 us with plain
 // accesses, 1400-1450 so).  Measured: 200M bf16 parameters with 8-bit moments
-// 322 us, 6.2 TB/s; 60M of everything in fp32 322 us, 5.2 TB/s; those rows 5.5
+// 325 us, 6.2 TB/s; 60M of everything in fp32 322 us, 5.2 TB/s; those rows 5.5
 // TB/s.  A large copy reaches 5.5 TB/s.
 #include "common8.h"
 
@@ -156,25 +156,31 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const Raw8<F32>& x) {
     }
 }
 
-// The first `live` (< 8) of eight elements, one by one.
+// The first `live` (1 .. 7) of eight elements, zeros behind them: one load for
+// each element, the last one's again past it, so that all are in flight at once.
+template <typename V>
+__device__ __forceinline__ void load_each(uint32_t u[8], const void* p, int64_t i, int live) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) u[k] = static_cast<const V*>(p)[i + min(k, live - 1)];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) u[k] = k < live ? u[k] : 0u;
+}
 template <bool F32>
 __device__ __forceinline__ void load_some(Raw8<F32>& x, const void* p, int64_t i, int live) {
-    x.zero();
-    for (int k = 0; k < live; ++k) {
-        if (F32) {
-            const uint32_t u = static_cast<const uint32_t*>(p)[i + k];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (k == q) x.a[q] = u;
-                if (k == 4 + q) x.b[q] = u;
-            }
-        } else {
-            const uint32_t u = static_cast<const uint16_t*>(p)[i + k];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if ((k >> 1) == q) x.a[q] |= u << (16 * (k & 1));
-        }
+    uint32_t u[8];
+    if (F32) {
+        load_each<uint32_t>(u, p, i, live);
+        x.a = u32x4{u[0], u[1], u[2], u[3]};
+        x.b = u32x4{u[4], u[5], u[6], u[7]};
+    } else {
+        load_each<uint16_t>(u, p, i, live);
+        x.a = u32x4{u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16};
     }
+}
+__device__ __forceinline__ u32x2 codes_some(const void* p, int64_t i, int live) {
+    uint32_t u[8];
+    load_each<uint8_t>(u, p, i, live);
+    return u32x2{u[0] | u[1] << 8 | u[2] << 16 | u[3] << 24, u[4] | u[5] << 8 | u[6] << 16 | u[7] << 24};
 }
 template <bool F32>
 __device__ __forceinline__ void store_some(void* p, int64_t i, const Raw8<F32>& x, int live) {
@@ -204,7 +210,7 @@ constexpr int kTensorsPerLaunch = 48;
 // Elements per workgroup: one round of 256 lanes x 8.  Measured on 200M bf16
 // parameters with 8-bit moments, before the streaming accesses: 367 us against
 // 387 with two rounds and 402 with four; on 300,000 fp32 elements 3.6 us
-// against 4.2 and 6.1.
+// against 4.2 and 6.1 (3.3 now: a tensor's odd last elements are loaded at once).
 constexpr int kChunk = 2048;
 
 struct AdamArgs {
@@ -238,22 +244,23 @@ __global__ void __launch_bounds__(256) adamw_kernel(const AdamArgs a) {
             e.m.load_stream(t.m, i);
             e.v.load_stream(t.v, i);
         }
-    } else {
+    } else if (live > 0) {
         load_some(e.p, t.p, i, live);
         load_some(e.g, t.g, i, live);
         if (S8) {
-            e.mc = u32x2{0, 0};
-            e.vc = u32x2{0, 0};
-            for (int k = 0; k < live; ++k) {
-                const uint32_t cm = static_cast<const uint8_t*>(t.m)[i + k], cv = static_cast<const uint8_t*>(t.v)[i + k];
-                const int sh = 8 * (k & 3);
-                if (k < 4) { e.mc[0] |= cm << sh; e.vc[0] |= cv << sh; }
-                else { e.mc[1] |= cm << sh; e.vc[1] |= cv << sh; }
-            }
+            e.mc = codes_some(t.m, i, live);
+            e.vc = codes_some(t.v, i, live);
         } else {
             load_some(e.m, t.m, i, live);
             load_some(e.v, t.v, i, live);
         }
+    } else {
+        e.p.zero();
+        e.g.zero();
+        e.m.zero();
+        e.v.zero();
+        e.mc = u32x2{0, 0};
+        e.vc = u32x2{0, 0};
     }
     if (S8) {
         e.ms = t.ms[i >> 7];
