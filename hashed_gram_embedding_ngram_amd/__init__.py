@@ -877,8 +877,10 @@ def project_fp8_workspace(m: int, n: int, k: int, dtype=torch.float32, device="c
 
 
 def ngram_project_fp8(a: Fp8, b: Fp8, out=None, dtype=torch.bfloat16, workspace=None, stream=None):
-    """out [a.rows][b.rows] (fp32 or bf16) = a b^T over their common columns
-    (see ngram_project_fp8 in ngram.h)."""
+    """out [a.rows][b.rows] (fp32 or bf16) = a b^T over their common columns.
+    A bf16 result of more than 32 rows keeps 13 bits below the largest product
+    of each eight columns, an fp32 result everything (see ngram_project_fp8 in
+    ngram.h)."""
     m, n = a.rows, b.rows
     if out is None:
         out = _new(m, n, dtype, a.codes.device, stream)
