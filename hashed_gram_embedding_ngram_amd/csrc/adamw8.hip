@@ -73,12 +73,19 @@ struct Eight {
     uint32_t ms, vs;        // and scale bytes
 };
 
+// The hardware's root of a v below 2^-126 is zero.  Beside an eps of 2^24 times
+// the largest root that this drops (2^-63 c.root) the quotient stays what it
+// is; with a smaller eps the step would become m / eps, and SMALL kernels take
+// the root of 2^64 v there.  (A test of the values in every call, or of a flag,
+// took 1.2 to 1.7% of the time with 8-bit moments.)
+inline bool needs_small(const StepConst& c) { return c.eps < 0x1p-39f * c.root; }
+
 // One step on eight elements; `index` is the first one's place in the random
 // sequence.  All 16 lanes of a block of 128 take part (those past the end with
 // zeros).  In 8 bits v holds the square root of the second moment, which
 // needs half the exponent range, and keeps it above zero where it was above
 // zero: a zero would make the next step divide by eps alone.
-template <bool P32, bool G32, bool S8>
+template <bool SMALL, bool P32, bool G32, bool S8>
 __device__ __forceinline__ void step8(Eight<P32, G32, S8>& e, const StepConst& c, uint64_t index) {
     float p[8], g[8], m[8], v[8];
     e.p.get(p);
@@ -115,8 +122,9 @@ __device__ __forceinline__ void step8(Eight<P32, G32, S8>& e, const StepConst& c
         // hardware root and reciprocal: one unit in the last place each
         // (correctly rounded ones are 18 instructions more, and 8-bit moments
         // leave about 65 an element before arithmetic and not memory sets
-        // the time); a v below 2^-126 gives a root of zero
+        // the time)
         root[k] = __builtin_amdgcn_sqrtf(v[k]);
+        if (SMALL) root[k] = v[k] < 0x1p-126f ? __builtin_amdgcn_sqrtf(v[k] * 0x1p64f) * 0x1p-32f : root[k];
         p[k] = p[k] * c.decay - c.rate * (m[k] * __builtin_amdgcn_rcpf(root[k] * c.root + c.eps));
     }
     if (P32) {
@@ -220,7 +228,7 @@ struct AdamArgs {
     int32_t count;
 };
 
-template <bool P32, bool G32, bool S8>
+template <bool SMALL, bool P32, bool G32, bool S8>
 __global__ void __launch_bounds__(256) adamw_kernel(const AdamArgs a) {
     const int lane = threadIdx.x & 63;
     // the tensor of this workgroup: the number of tensors that end at or
@@ -266,7 +274,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(const AdamArgs a) {
         e.ms = t.ms[i >> 7];
         e.vs = t.vs[i >> 7];
     }
-    step8(e, a.c, t.offset + static_cast<uint64_t>(i));
+    step8<SMALL>(e, a.c, t.offset + static_cast<uint64_t>(i));
     if (live == 8) {
         store8(t.p, i, e.p);
         if (S8) {
@@ -316,7 +324,7 @@ struct RowsArgs {
     StepConst c;
 };
 
-template <bool P32, bool G32, bool S8>
+template <bool SMALL, bool P32, bool G32, bool S8>
 __global__ void __launch_bounds__(256) adamw_rows_kernel(const RowsArgs a) {
     const uint32_t unit = blockIdx.x * 16 + (threadIdx.x >> 4), nb = static_cast<uint32_t>(a.nb);
     const uint32_t u = unit / nb;
@@ -349,7 +357,7 @@ __global__ void __launch_bounds__(256) adamw_rows_kernel(const RowsArgs a) {
         e.vc = u32x2{0, 0};
         e.ms = e.vs = kUnitScale;
     }
-    step8(e, a.c, static_cast<uint64_t>(at));
+    step8<SMALL>(e, a.c, static_cast<uint64_t>(at));
     if (!live) return;
     store8(a.p, at, e.p);
     if (S8) {
@@ -440,6 +448,7 @@ int ngram_adamw(const ngram_adamw_tensor* tensors, int32_t count, const ngram_ad
         if (!aligned(t.p, 16) || !aligned(t.g, 16) || !aligned(t.m, s8 ? 8 : 16) || !aligned(t.v, s8 ? 8 : 16))
             return fail(NGRAM_EALIGN, "tensor %d: p, g and fp32 moments must be 16-byte aligned, 8-bit moments 8-byte", i);
     }
+    const bool small = needs_small(a.c);
     // one launch for each kind that occurs and each 48 tensors of it
     for (int kind = 0; kind < 8; ++kind) {
         int32_t i = 0;
@@ -458,7 +467,9 @@ int ngram_adamw(const ngram_adamw_tensor* tensors, int32_t count, const ngram_ad
             }
             if (a.count == 0) break;
             const dim3 grid(static_cast<unsigned>(groups)), block(256);
-#define NG8_ADAM(P, G, S) hipLaunchKernelGGL((adamw_kernel<P, G, S>), grid, block, 0, stream, a)
+#define NG8_ADAM(P, G, S)                                                                           \
+    if (small) hipLaunchKernelGGL((adamw_kernel<true, P, G, S>), grid, block, 0, stream, a);        \
+    else hipLaunchKernelGGL((adamw_kernel<false, P, G, S>), grid, block, 0, stream, a)
             NG8_BY_KIND(kind, NG8_ADAM)
 #undef NG8_ADAM
             if ((rc = hip_status("ngram_adamw launch"))) return rc;
@@ -493,7 +504,9 @@ int ngram_adamw_rows(const ngram_adamw_tensor* table, int64_t R, int32_t d, cons
     a.nb = static_cast<int32_t>(blocks_of(d));
     if (max_rows > INT32_MAX / a.nb) return fail(NGRAM_ERANGE, "max_rows=%lld too large for one launch", (long long)max_rows);
     const dim3 grid(static_cast<unsigned>((max_rows * a.nb + 15) / 16)), block(256);
-#define NG8_ROWS(P, G, S) hipLaunchKernelGGL((adamw_rows_kernel<P, G, S>), grid, block, 0, stream, a)
+#define NG8_ROWS(P, G, S)                                                                           \
+    if (needs_small(a.c)) hipLaunchKernelGGL((adamw_rows_kernel<true, P, G, S>), grid, block, 0, stream, a);    \
+    else hipLaunchKernelGGL((adamw_rows_kernel<false, P, G, S>), grid, block, 0, stream, a)
     NG8_BY_KIND(kind_of(table->p_dtype, table->g_dtype, table->state), NG8_ROWS)
 #undef NG8_ROWS
     return hip_status("ngram_adamw_rows launch");

@@ -505,6 +505,9 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
  * g (times grad_scale):
  *   m' = beta1 m + (1 - beta1) g,    v' = beta2 v + (1 - beta2) g^2
  *   p' = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m' / (sqrt(v') / sqrt(1 - beta2^step) + eps)
+ * v' is an fp32 number down to 2^-149, with moments in 8 bits too, but below
+ * 2^-126 it counts as zero under an eps >= 2^-39 / sqrt(1 - beta2^step), which
+ * its root does not change.
  * p fp32 or bf16, g fp32 or bf16, moments in fp32 (NGRAM_STATE_F32) or in 8
  * bits (NGRAM_STATE_FP8): m and sqrt(v) as E4M3 codes with an E8M0 scale per
  * 128 consecutive elements of the tensor (of the row, in a table).
@@ -512,8 +515,7 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
  * sqrt(v) by 0.05% where E4M3's neighbours lie 6 to 12% apart, and an
  * update of a bf16 parameter is often below half its last place.  So 8-bit moments and bf16
  * parameters round up or down at random, with the probabilities that make the
- * expected value exact, and a positive sqrt(v) never becomes zero (a v' below
- * 2^-126 counts as zero).  The
+ * expected value exact, and a positive sqrt(v) never becomes zero.  The
  * random bits of element i are half (even i: low) of
  * splitmix64(key + (rng_offset + i) / 2), key = splitmix64(splitmix64(seed) +
  * step): m takes bits 0..19, sqrt(v) bits 12..31, p bits 8..23.  Equal inputs
