@@ -12,6 +12,7 @@
 // TB/s.  A large copy reaches 5.5 TB/s.
 #include "common8.h"
 
+#include <algorithm>
 #include <cmath>
 
 namespace ng8 {
@@ -408,6 +409,15 @@ int kind_of(int p_dtype, int g_dtype, int state) {
     return (p_dtype == NGRAM_F32 ? 4 : 0) | (g_dtype == NGRAM_F32 ? 2 : 0) | (state == NGRAM_STATE_FP8 ? 1 : 0);
 }
 
+// Elements from .. from + take - 1 of a tensor; `from` is a multiple of kChunk.
+TensorArg part_of(const ngram_adamw_tensor& t, int64_t from, int64_t take) {
+    const size_t pb = value_bytes(t.p_dtype), gb = value_bytes(t.g_dtype), sb = t.state == NGRAM_STATE_FP8 ? 1 : 4;
+    return TensorArg{static_cast<uint8_t*>(t.p) + from * pb, static_cast<const uint8_t*>(t.g) + from * gb,
+                     static_cast<uint8_t*>(t.m) + from * sb, static_cast<uint8_t*>(t.v) + from * sb,
+                     t.m_scale ? t.m_scale + from / kBlock : nullptr, t.v_scale ? t.v_scale + from / kBlock : nullptr,
+                     take, static_cast<uint64_t>(t.rng_offset + from)};
+}
+
 #define NG8_BY_KIND(kind, CALL)                      \
     switch (kind) {                                  \
         case 0: CALL(false, false, false); break;    \
@@ -449,21 +459,30 @@ int ngram_adamw(const ngram_adamw_tensor* tensors, int32_t count, const ngram_ad
             return fail(NGRAM_EALIGN, "tensor %d: p, g and fp32 moments must be 16-byte aligned, 8-bit moments 8-byte", i);
     }
     const bool small = needs_small(a.c);
-    // one launch for each kind that occurs and each 48 tensors of it
+    // one launch for each kind that occurs and each 48 tensors of it, or each
+    // 2^35 elements: a tensor is cut there, and goes on in the next launch
     for (int kind = 0; kind < 8; ++kind) {
         int32_t i = 0;
+        int64_t from = 0;       // tensor i's elements that earlier launches have
         while (i < count) {
             a.count = 0;
-            uint64_t groups = 0;
-            for (; i < count && a.count < kTensorsPerLaunch; ++i) {
+            int64_t groups = 0;
+            const int64_t most = most_groups(256);
+            while (i < count && a.count < kTensorsPerLaunch && groups < most) {
                 const ngram_adamw_tensor& t = tensors[i];
-                if (t.numel == 0 || kind_of(t.p_dtype, t.g_dtype, t.state) != kind) continue;
-                const uint64_t more = static_cast<uint64_t>((t.numel + kChunk - 1) / kChunk);
-                if (a.count > 0 && groups + more > INT32_MAX) break;
-                a.t[a.count] = TensorArg{t.p, t.g, t.m, t.v, t.m_scale, t.v_scale, t.numel,
-                                         static_cast<uint64_t>(t.rng_offset)};
-                groups += more;
+                if (t.numel == 0 || kind_of(t.p_dtype, t.g_dtype, t.state) != kind) {
+                    ++i;
+                    continue;
+                }
+                const int64_t take = std::min(t.numel - from, (most - groups) * kChunk);
+                a.t[a.count] = part_of(t, from, take);
+                groups += (take + kChunk - 1) / kChunk;
                 a.end[a.count++] = static_cast<uint32_t>(groups);
+                from += take;
+                if (from == t.numel) {
+                    ++i;
+                    from = 0;
+                }
             }
             if (a.count == 0) break;
             const dim3 grid(static_cast<unsigned>(groups)), block(256);

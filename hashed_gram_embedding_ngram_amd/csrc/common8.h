@@ -35,6 +35,9 @@ inline int64_t blocks_of(int64_t cols) { return (cols + kBlock - 1) / kBlock; }
 inline int64_t code_ld(int64_t cols) { return blocks_of(cols) * kBlock; }
 inline int64_t scale_ld(int64_t cols) { return (blocks_of(cols) + 3) / 4 * 4; }
 inline size_t value_bytes(int dtype) { return dtype == NGRAM_F32 ? 4 : 2; }
+// The most workgroups of a launch: 2^32 and more work items in a dimension are
+// not run in full, and no error tells.  Larger work goes in several launches.
+inline int64_t most_groups(int threads) { return INT64_C(0xFFFFFFFF) / threads; }
 // Checks a caller's 8-bit matrix; `what` names it in the message.
 int check_fp8(const ngram_fp8* q, const char* what);
 

@@ -554,7 +554,7 @@ typedef struct {
 
 /* The step on tensors[0 .. count) (a HOST array, read before the call
  * returns), in place; tensors must not overlap.  One launch for up to 48
- * tensors of one combination of types.  Errors: EINVAL, EALIGN, ERANGE. */
+ * tensors and 2^35 elements of one combination of types.  Errors: EINVAL, EALIGN, ERANGE. */
 int ngram_adamw(const ngram_adamw_tensor* tensors, int32_t count, const ngram_adamw_step* step, ngram_stream_t stream);
 
 /* The step on the touched rows of a table, from a sparse gradient as

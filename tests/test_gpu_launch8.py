@@ -1,0 +1,50 @@
+"""The 8-bit layer's calls on sizes that one launch cannot cover (HIP takes
+fewer than 2^32 work items in a dimension): they are done in parts.  Narrow
+rows, so that the memory fits; values are checked in the first rows, around the
+parts' borders and in the last."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import hashed_gram_embedding_ngram_amd as ng  # noqa: E402
+from tests.test_gpu_parity import say  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF = torch.bfloat16
+
+
+def room(gib):
+    """Skips where the card has less memory than the test takes."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < gib * 2 ** 30:
+        pytest.skip(f"needs {gib} GiB of device memory")
+
+
+def test_adamw_of_many_elements():
+    """33 tensors of 2^30 and more elements in one call, reading one gradient; borders of launches lie inside tensors."""
+    sizes = [(1 << 30) + 24 * i + (i % 8) for i in range(33)]
+    say(f"adamw on {sum(sizes)} elements")
+    room(160)
+    assert sum(sizes) > 1 << 35
+    g = torch.ones(max(sizes), dtype=BF, device=DEV)
+    g[1::2] = -1.0
+    u8 = lambda n, v: torch.full((n,), v, dtype=torch.uint8, device=DEV)  # noqa: E731
+    p = [torch.zeros(n, dtype=BF, device=DEV) for n in sizes]
+    m, v = [u8(n, 0) for n in sizes], [u8(n, 0) for n in sizes]
+    ms, vs = ([u8(-(-n // 128), 127) for n in sizes] for _ in range(2))
+    t = ng.AdamWTensors(p, [g[:n] for n in sizes], m, v, ms, vs)
+    ng.ngram_adamw(t, lr=1e-2, step=1)
+    for i in range(33):
+        # every element moved by lr against its gradient's sign, once, to within a bf16 step
+        lo, hi = (p[i][0::2].min(), p[i][0::2].max()), (p[i][1::2].min(), p[i][1::2].max())
+        assert all(abs(float(a) + 1e-2) <= 1e-4 for a in lo) and all(abs(float(a) - 1e-2) <= 1e-4 for a in hi), i
+        assert int(v[i].min()) > 0 and int(vs[i].max()) < 127 and int(ms[i].max()) < 127, i
+    # the random words go on where a tensor is cut: equal to the step on the tail alone with its place in the sequence
+    i, cut = 31, 1 << 29
+    assert sum(sizes[:i]) + cut < (1 << 35) - 2048 < sum(sizes[:i + 1])
+    q, qm, qv = torch.zeros(sizes[i] - cut, dtype=BF, device=DEV), u8(sizes[i] - cut, 0), u8(sizes[i] - cut, 0)
+    qs = [u8(-(-(sizes[i] - cut) // 128), 127) for _ in range(2)]
+    place = sum(-(-n // 128) * 128 for n in sizes[:i]) + cut
+    ng.ngram_adamw(ng.AdamWTensors([q], [g[cut:sizes[i]]], [qm], [qv], [qs[0]], [qs[1]], rng_offsets=[place]), lr=1e-2, step=1)
+    assert torch.equal(q, p[i][cut:]) and torch.equal(qm, m[i][cut:]) and torch.equal(qv, v[i][cut:])
