@@ -318,7 +318,8 @@ struct RowsArgs {
     const int32_t* rows;
     const void* g;
     const int64_t* count;
-    int64_t max_rows;
+    int64_t first;      // rows and gradient rows of earlier launches, which `rows` and `g` are already past
+    int64_t max_rows;   // of this launch
     int64_t R;
     int32_t d;
     int32_t nb;         // blocks of 128 columns in a row
@@ -329,7 +330,7 @@ template <bool SMALL, bool P32, bool G32, bool S8>
 __global__ void __launch_bounds__(256) adamw_rows_kernel(const RowsArgs a) {
     const uint32_t unit = blockIdx.x * 16 + (threadIdx.x >> 4), nb = static_cast<uint32_t>(a.nb);
     const uint32_t u = unit / nb;
-    const int64_t count = a.count ? min(*a.count, a.max_rows) : a.max_rows;
+    const int64_t count = a.count ? min(*a.count - a.first, a.max_rows) : a.max_rows;
     if (u >= count) return;
     const int64_t row = a.rows[u];
     if (row < 0 || row >= a.R) return;
@@ -511,6 +512,7 @@ int ngram_adamw_rows(const ngram_adamw_tensor* table, int64_t R, int32_t d, cons
     if (table->numel != R * d) return fail(NGRAM_EINVAL, "table: numel=%lld is not R * d", (long long)table->numel);
     if (table->rng_offset != 0) return fail(NGRAM_EINVAL, "table: rng_offset must be 0");
     if (max_rows < 0) return fail(NGRAM_EINVAL, "max_rows=%lld is negative", (long long)max_rows);
+    if (max_rows > NGRAM_MAX_ROWS) return fail(NGRAM_ERANGE, "max_rows=%lld above 2^31 - 1", (long long)max_rows);
     if (max_rows == 0) return NGRAM_OK;
     const bool s8 = table->state == NGRAM_STATE_FP8;
     if (!rows || !table->p || !table->g || !table->m || !table->v || (s8 && (!table->m_scale || !table->v_scale)))
@@ -519,16 +521,23 @@ int ngram_adamw_rows(const ngram_adamw_tensor* table, int64_t R, int32_t d, cons
         !aligned(table->v, s8 ? 8 : 16) || !aligned(rows, 4) || !aligned(n_rows, 8))
         return fail(NGRAM_EALIGN, "p, g and fp32 moments must be 16-byte aligned, 8-bit moments and n_rows 8-byte, rows 4-byte");
     a.p = table->p; a.m = table->m; a.v = table->v; a.ms = table->m_scale; a.vs = table->v_scale;
-    a.rows = rows; a.g = table->g; a.count = n_rows; a.max_rows = max_rows; a.R = R; a.d = d;
+    a.count = n_rows; a.R = R; a.d = d;
     a.nb = static_cast<int32_t>(blocks_of(d));
-    if (max_rows > INT32_MAX / a.nb) return fail(NGRAM_ERANGE, "max_rows=%lld too large for one launch", (long long)max_rows);
-    const dim3 grid(static_cast<unsigned>((max_rows * a.nb + 15) / 16)), block(256);
+    const int64_t most = most_groups(256) * 16 / a.nb;      // rows of a launch: 16 blocks a workgroup
+    const bool small = needs_small(a.c);
+    for (a.first = 0; a.first < max_rows; a.first += most) {
+        a.rows = rows + a.first;
+        a.g = static_cast<const uint8_t*>(table->g) + a.first * d * value_bytes(table->g_dtype);
+        a.max_rows = std::min(most, max_rows - a.first);
+        const dim3 grid(static_cast<unsigned>((a.max_rows * a.nb + 15) / 16)), block(256);
 #define NG8_ROWS(P, G, S)                                                                           \
-    if (needs_small(a.c)) hipLaunchKernelGGL((adamw_rows_kernel<true, P, G, S>), grid, block, 0, stream, a);    \
-    else hipLaunchKernelGGL((adamw_rows_kernel<false, P, G, S>), grid, block, 0, stream, a)
-    NG8_BY_KIND(kind_of(table->p_dtype, table->g_dtype, table->state), NG8_ROWS)
+        if (small) hipLaunchKernelGGL((adamw_rows_kernel<true, P, G, S>), grid, block, 0, stream, a);   \
+        else hipLaunchKernelGGL((adamw_rows_kernel<false, P, G, S>), grid, block, 0, stream, a)
+        NG8_BY_KIND(kind_of(table->p_dtype, table->g_dtype, table->state), NG8_ROWS)
 #undef NG8_ROWS
-    return hip_status("ngram_adamw_rows launch");
+        if ((rc = hip_status("ngram_adamw_rows launch"))) return rc;
+    }
+    return NGRAM_OK;
 }
 
 }  // extern "C"

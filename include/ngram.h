@@ -560,7 +560,8 @@ int ngram_adamw(const ngram_adamw_tensor* tensors, int32_t count, const ngram_ad
 /* The step on the touched rows of a table, from a sparse gradient as
  * ngram_grad_table and ngram_grad_e1 write it: table->p, m, v [R][d]
  * (numel = R d, rng_offset 0), scales [R][ceil(d / 128)]; row rows[u] takes
- * the gradient row table->g [max_rows][d], u < min(*n_rows, max_rows).  n_rows
+ * the gradient row table->g [max_rows][d], u < min(*n_rows, max_rows),
+ * max_rows <= NGRAM_MAX_ROWS.  n_rows
  * (device int64; NULL: max_rows) is read on the device, so the number of rows
  * need not come back to the host.  Rows must be distinct; ids outside [0, R)
  * are skipped.  Rows not listed keep their parameters and moments (their

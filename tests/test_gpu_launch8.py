@@ -48,3 +48,28 @@ def test_adamw_of_many_elements():
     place = sum(-(-n // 128) * 128 for n in sizes[:i]) + cut
     ng.ngram_adamw(ng.AdamWTensors([q], [g[cut:sizes[i]]], [qm], [qv], [qs[0]], [qs[1]], rng_offsets=[place]), lr=1e-2, step=1)
     assert torch.equal(q, p[i][cut:]) and torch.equal(qm, m[i][cut:]) and torch.equal(qv, v[i][cut:])
+
+
+@pytest.mark.parametrize("listed", [True, False])
+def test_adamw_rows_of_many_narrow_rows(listed):
+    room_for, R, d = (1 << 28) + 333, (1 << 28) + 500, 8     # a group of 16 lanes a row
+    say(f"adamw_rows, {room_for} rows of {d}")
+    room(20)
+    p = torch.zeros((R, d), dtype=BF, device=DEV)
+    m, v = (torch.zeros((R, d), dtype=torch.uint8, device=DEV) for _ in range(2))
+    ms, vs = (torch.full((R, 1), 127, dtype=torch.uint8, device=DEV) for _ in range(2))
+    rows = torch.arange(100, room_for + 100, dtype=torch.int32, device=DEV)
+    g = torch.ones((room_for, d), dtype=BF, device=DEV)
+    g[1::2] = -1.0
+    count = room_for - 50 if listed else room_for
+    n_rows = torch.tensor([count], device=DEV) if listed else None
+    ng.ngram_adamw_rows(p, m, v, rows, g, n_rows, m_scale=ms, v_scale=vs, lr=1e-2, step=1)
+    assert not bool(p[:100].any()) and not bool(p[100 + count:].any()) and not bool(v[100 + count:].any())
+    hit = p[100:100 + count]
+    assert float((hit[0::2].float() + 1e-2).abs().max()) <= 1e-4 and float((hit[1::2].float() - 1e-2).abs().max()) <= 1e-4
+    # the random words go by the row: the same as the step on the last rows alone
+    q, qm, qv = torch.zeros_like(p[:R]), torch.zeros_like(m), torch.zeros_like(v)
+    qs = [torch.full((R, 1), 127, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    a, b = count - 1001, count
+    ng.ngram_adamw_rows(q, qm, qv, rows[a:b], g[a:b], m_scale=qs[0], v_scale=qs[1], lr=1e-2, step=1)
+    assert torch.equal(q[100 + a:100 + b], p[100 + a:100 + b]) and torch.equal(qv[100 + a:100 + b], v[100 + a:100 + b])
