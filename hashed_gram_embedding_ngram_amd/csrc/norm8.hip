@@ -631,7 +631,7 @@ struct RowShape {
     int chunks;     // per wavefront
     int waves;      // per workgroup
     bool wide;
-    int64_t grid;
+    int64_t grid;   // of the gradient, whose workgroups walk over the rows
 };
 
 RowShape row_shape(int64_t n, int d) {
@@ -641,12 +641,10 @@ RowShape row_shape(int64_t n, int d) {
     if (!s.wide) {
         s.chunks = total;
         s.waves = 4;
-        s.grid = (n + 3) / 4;
     } else {
         s.waves = std::min(kMaxWaves, total);
         s.chunks = (total + s.waves - 1) / s.waves;
         s.waves = (total + s.chunks - 1) / s.chunks;
-        s.grid = n;
     }
     return s;
 }
@@ -753,28 +751,39 @@ int ngram_add_norm(const void* x, int32_t x_dtype, const uint16_t* residual, int
         return fail(NGRAM_EALIGN, "x, residual, gamma, sum_out and y_out must be 16-byte aligned");
     if (!aligned(r_out, 4)) return fail(NGRAM_EALIGN, "r_out must be 4-byte aligned");
     NormArgs a;
-    a.x = x; a.residual = residual; a.gamma = gamma; a.sum_out = sum_out; a.y_out = y_out;
-    a.codes = q_out ? q_out->codes : nullptr;
-    a.scales = q_out ? q_out->scales : nullptr;
-    a.r_out = r_out; a.n = n; a.d = d;
+    a.gamma = gamma; a.d = d;
     a.ld = static_cast<int32_t>(code_ld(d));
     a.sld = static_cast<int32_t>(scale_ld(d));
     a.eps = eps;
     a.inv_d = 1.0f / static_cast<float>(d);
     const RowShape s = row_shape(n, d);
-    const dim3 grid(static_cast<unsigned>(s.grid)), block(64 * s.waves);
+    const dim3 block(64 * s.waves);
+    const int per = s.wide ? 1 : s.waves;                       // rows of a workgroup
+    const int64_t most = most_groups(64 * s.waves) * per;       // and of a launch
     const bool f32 = x_dtype == NGRAM_F32;
-    if (!s.wide) {
-        if (f32) launch_norm<true, false, true>(s.chunks, grid, block, stream, a);
-        else launch_norm<false, false, true>(s.chunks, grid, block, stream, a);
-    } else if (n * d >= 1 << 20) {      // see put()
-        if (f32) launch_norm<true, true, true>(s.chunks, grid, block, stream, a);
-        else launch_norm<false, true, true>(s.chunks, grid, block, stream, a);
-    } else {
-        if (f32) launch_norm<true, true, false>(s.chunks, grid, block, stream, a);
-        else launch_norm<false, true, false>(s.chunks, grid, block, stream, a);
+    for (int64_t row = 0; row < n; row += most) {
+        a.n = std::min(most, n - row);
+        a.x = static_cast<const uint8_t*>(x) + row * d * value_bytes(x_dtype);
+        a.residual = residual ? residual + row * d : nullptr;
+        a.sum_out = sum_out ? sum_out + row * d : nullptr;
+        a.y_out = y_out ? y_out + row * d : nullptr;
+        a.codes = q_out ? q_out->codes + row * a.ld : nullptr;
+        a.scales = q_out ? q_out->scales + row * a.sld : nullptr;
+        a.r_out = r_out ? r_out + row : nullptr;
+        const dim3 grid(static_cast<unsigned>((a.n + per - 1) / per));
+        if (!s.wide) {
+            if (f32) launch_norm<true, false, true>(s.chunks, grid, block, stream, a);
+            else launch_norm<false, false, true>(s.chunks, grid, block, stream, a);
+        } else if (n * d >= 1 << 20) {      // see put()
+            if (f32) launch_norm<true, true, true>(s.chunks, grid, block, stream, a);
+            else launch_norm<false, true, true>(s.chunks, grid, block, stream, a);
+        } else {
+            if (f32) launch_norm<true, true, false>(s.chunks, grid, block, stream, a);
+            else launch_norm<false, true, false>(s.chunks, grid, block, stream, a);
+        }
+        if ((rc = hip_status("ngram_add_norm launch"))) return rc;
     }
-    return hip_status("ngram_add_norm launch");
+    return NGRAM_OK;
 }
 
 int64_t ngram_add_norm_grad_workspace_bytes(int64_t n, int32_t d) {

@@ -73,3 +73,37 @@ def test_adamw_rows_of_many_narrow_rows(listed):
     a, b = count - 1001, count
     ng.ngram_adamw_rows(q, qm, qv, rows[a:b], g[a:b], m_scale=qs[0], v_scale=qs[1], lr=1e-2, step=1)
     assert torch.equal(q[100 + a:100 + b], p[100 + a:100 + b]) and torch.equal(qv[100 + a:100 + b], v[100 + a:100 + b])
+
+
+def test_norm_of_many_narrow_rows():
+    n, d = (1 << 26) + 77, 8                            # 64 threads a row
+    say(f"norm {n} x {d}")
+    room(24)
+    x = torch.randn((n, d), device=DEV).to(BF)
+    gamma = torch.rand(d, device=DEV)
+    s, y = torch.empty_like(x), torch.empty_like(x)
+    res = torch.zeros_like(x)
+    res[-1000:] = 1.0
+    out = ng.ngram_add_norm(x, gamma, 1e-6, residual=res, sum_out=s, y_out=y, keep_r=True)
+    assert torch.equal(s[:-1000], x[:-1000]) and torch.equal(s[-1000:], x[-1000:] + res[-1000:])
+    for a, b in ((0, 5000), ((1 << 26) - 3000, n), ((1 << 25) - 3000, (1 << 25) + 3000)):
+        few = ng.ngram_add_norm(s[a:b].contiguous(), gamma, 1e-6, keep_y=True, keep_r=True)
+        assert torch.equal(out.r[a:b], few.r) and torch.equal(y[a:b], few.y)
+        assert torch.equal(out.q.codes[a:b].view(torch.uint8), few.q.codes.view(torch.uint8))
+        assert torch.equal(out.q.scales[a:b], few.q.scales)
+    want = torch.rsqrt((s.float() ** 2).mean(dim=1) + 1e-6)
+    assert torch.all((out.r - want).abs() <= 1e-5 * want)
+
+
+def test_norm_of_many_wide_rows():
+    n, d = (1 << 22) + 9, 8192                          # 16 wavefronts a row
+    say(f"norm {n} x {d}")
+    room(80)
+    x = torch.zeros((n, d), dtype=BF, device=DEV)
+    x.view(-1)[::4096] = 1.0
+    r = torch.zeros(n, device=DEV)
+    ng.ngram_add_norm(x, torch.ones(d, device=DEV), 1.0, quantise=False, r_out=r)
+    at = torch.arange(n, device=DEV) * d
+    ones = (at + d + 4095) // 4096 - (at + 4095) // 4096
+    want = torch.rsqrt(ones / d + 1.0)
+    assert torch.all((r - want).abs() <= 1e-6)
