@@ -55,6 +55,7 @@ struct ProjArgs {
     int32_t ntiles;
     int32_t band;           // tile rows walked together
     int32_t stride;         // items from one of a workgroup to its next
+    int32_t first;          // the launch's first item, a multiple of 8 (few rows: 16 rows of B)
 };
 
 // acc + x y, each scaled by the lowest byte of its word.
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = (wave / T::WN) * 16 * TM, wn = (wave % T::WN) * 16 * TN;
-    int w = blockIdx.x, lw = w;
+    int w = a.first + static_cast<int>(blockIdx.x), lw = w;
     Item now = item_of(w, a);
     if (!now.valid) return;
 
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_small_kernel(const 
     const int t = threadIdx.x, lane = t & 63;
     const int all = __builtin_amdgcn_readfirstlane(t >> 6), group = all / T::Waves, wave = all % T::Waves;
     const int wm = (wave / T::WN) * 16 * TM, wn = (wave % T::WN) * 16 * TN;
-    const Item it = item_of(blockIdx.x, a);
+    const Item it = item_of(a.first + static_cast<int>(blockIdx.x), a);
     if (!it.valid) return;
     const int64_t m0 = static_cast<int64_t>(it.mt) * T::BM, n0 = static_cast<int64_t>(it.nt) * T::BN;
     const int k0 = it.split * a.split_steps, k1 = min(k0 + a.split_steps, a.steps);
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(64 * kRowWaves) project_fp8_rows_kernel(const 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+    const int64_t n0 = (a.first + static_cast<int64_t>(blockIdx.x)) * 16;
     const int64_t br = min(n0 + lr, a.n - 1);
     const uint8_t* const bp = a.b + br * a.ld + 32 * (lane >> 4);
     const uint8_t* const bsp = a.bs + (br >> a.bsh) * a.sld;
@@ -717,6 +718,17 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool f32) {
     return best;
 }
 
+// Launches `groups` workgroups, `step` of them a unit, as many at once as a
+// launch takes; a.first tells each launch where it begins.
+template <class F>
+void in_parts(ProjArgs& a, int64_t groups, int threads, int64_t step, F launch) {
+    const int64_t most = most_groups(threads) / step * step;
+    for (int64_t at = 0; at < groups; at += most) {
+        a.first = static_cast<int32_t>(at);
+        launch(dim3(static_cast<unsigned>(std::min(most, groups - at))));
+    }
+}
+
 template <class T>
 int launch_tile(ProjArgs& a, hipStream_t st) {
     const int64_t mt = (a.m + T::BM - 1) / T::BM, nt = (a.n + T::BN - 1) / T::BN, items = mt * nt * a.splits;
@@ -728,9 +740,11 @@ int launch_tile(ProjArgs& a, hipStream_t st) {
     // item; where an item has fewer steps than there are buffers, an item each
     const int64_t room = kUnits * std::max(1, 160 * 1024 / T::Lds);
     const int64_t least = std::min<int64_t>(a.split_steps, a.steps - (a.splits - 1) * a.split_steps);     // the last split's steps
-    const dim3 grid(static_cast<unsigned>(least < 4 ? (items + 7) / 8 * 8 : std::min((items + 7) / 8 * 8, room))), block(T::Threads);
-    a.stride = static_cast<int32_t>(grid.x);
-    hipLaunchKernelGGL((project_fp8_kernel<T>), grid, block, T::Lds, st, a);
+    const int64_t all = (items + 7) / 8 * 8, groups = least < 4 ? all : std::min(all, room);
+    a.stride = static_cast<int32_t>(groups);
+    in_parts(a, groups, T::Threads, 8, [&](dim3 grid) {
+        hipLaunchKernelGGL((project_fp8_kernel<T>), grid, dim3(T::Threads), T::Lds, st, a);
+    });
     return NGRAM_OK;
 }
 
@@ -741,15 +755,19 @@ int launch_small(ProjArgs& a, hipStream_t st) {
     a.ntiles_n = static_cast<int32_t>(nt);
     a.ntiles = static_cast<int32_t>(mt * nt);
     a.band = 8;
-    hipLaunchKernelGGL((project_fp8_small_kernel<T>), dim3(static_cast<unsigned>((items + 7) / 8 * 8)), dim3(T::Threads), T::Lds, st, a);
+    in_parts(a, (items + 7) / 8 * 8, T::Threads, 8, [&](dim3 grid) {
+        hipLaunchKernelGGL((project_fp8_small_kernel<T>), grid, dim3(T::Threads), T::Lds, st, a);
+    });
     return NGRAM_OK;
 }
 
 template <int MT>
-void launch_rows(const ProjArgs& a, bool f32, hipStream_t st) {
-    const dim3 grid(static_cast<unsigned>((a.n + 15) / 16)), block(64 * kRowWaves);
-    if (f32) hipLaunchKernelGGL((project_fp8_rows_kernel<MT, true>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((project_fp8_rows_kernel<MT, false>), grid, block, 0, st, a);
+void launch_rows(ProjArgs& a, bool f32, hipStream_t st) {
+    const dim3 block(64 * kRowWaves);
+    in_parts(a, (a.n + 15) / 16, 64 * kRowWaves, 1, [&](dim3 grid) {
+        if (f32) hipLaunchKernelGGL((project_fp8_rows_kernel<MT, true>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((project_fp8_rows_kernel<MT, false>), grid, block, 0, st, a);
+    });
 }
 
 // m rows by n columns over k columns of K; the tile kernels address a tile's
@@ -793,6 +811,8 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
     const int64_t need = p.splits > 1 ? 4 * p.splits * A->rows * B->rows : 0;
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
         return fail(NGRAM_EINVAL, "workspace must hold %lld bytes, 16-byte aligned", (long long)need);
+    const int64_t count = A->rows * B->rows, groups = (count / 4 + 255) / 256;      // of the splits' sum
+    if (p.splits > 1 && groups > most_groups(256)) return fail(NGRAM_ERANGE, "C too large for a split of K");
     ProjArgs a;
     a.a = A->codes; a.as = A->scales; a.b = B->codes; a.bs = B->scales; a.c = C;
     a.partial = static_cast<float*>(workspace);
@@ -801,7 +821,7 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
     a.bsh = B->block_rows == kBlock ? 7 : 0;
     a.steps = static_cast<int32_t>(blocks_of(A->cols));
     a.split_steps = p.split_steps; a.splits = p.splits;
-    a.ntiles_n = a.ntiles = a.band = a.stride = 0;
+    a.ntiles_n = a.ntiles = a.band = a.stride = a.first = 0;
     rc = NGRAM_OK;
     if (p.kind == 0) {
         if (a.m <= 16) launch_rows<1>(a, f32, stream);
@@ -817,8 +837,6 @@ int ngram_project_fp8(const ngram_fp8* A, const ngram_fp8* B, void* C, int32_t c
     }
     if (rc) return rc;
     if (a.splits > 1) {
-        const int64_t count = a.m * a.n, groups = (count / 4 + 255) / 256;
-        if (groups > INT32_MAX) return fail(NGRAM_ERANGE, "C too large for one launch");
         if (f32) hipLaunchKernelGGL((split_sum_kernel<true>), dim3(static_cast<unsigned>(groups)), dim3(256), 0, stream, a.partial, a.splits, count, C);
         else hipLaunchKernelGGL((split_sum_kernel<false>), dim3(static_cast<unsigned>(groups)), dim3(256), 0, stream, a.partial, a.splits, count, C);
     }

@@ -107,3 +107,36 @@ def test_norm_of_many_wide_rows():
     ones = (at + d + 4095) // 4096 - (at + 4095) // 4096
     want = torch.rsqrt(ones / d + 1.0)
     assert torch.all((r - want).abs() <= 1e-6)
+
+
+def test_product_of_few_rows_with_many():
+    n, k = (1 << 26) + 136, 128                         # 64 threads an output column
+    say(f"product 2 x {n} x {k}")
+    room(16)
+    codes = torch.full((n, k), 0x38, dtype=torch.uint8, device=DEV)          # 1
+    codes[::3] = 0x40                                                        # 2
+    for block_rows in (1, 128):
+        rows = n if block_rows == 1 else -(-n // 128)
+        scales = (127 + torch.arange(rows, device=DEV) % 3).to(torch.uint8)[:, None].repeat(1, 4)
+        b = ng.Fp8(codes, scales, n, k, block_rows=block_rows)
+        a = ng.Fp8(torch.full((2, k), 0x38, dtype=torch.uint8, device=DEV), torch.tensor([[127] * 4, [128] * 4], dtype=torch.uint8, device=DEV), 2, k)
+        got = ng.ngram_project_fp8(a, b)
+        i = torch.arange(n, device=DEV)
+        want = 128.0 * torch.where(i % 3 == 0, 2.0, 1.0) * 2.0 ** ((i if block_rows == 1 else i // 128) % 3)
+        assert torch.equal(got[0].float(), want) and torch.equal(got[1].float(), 2 * want)
+
+
+def test_product_of_very_many_rows():
+    m, n, k = 1 << 30, 8, 128                           # 2^23 tiles of 512 threads
+    say(f"product {m} x {n} x {k}")
+    room(170)
+    a_codes = torch.full((m, k), 0x38, dtype=torch.uint8, device=DEV)
+    b_codes = torch.full((n, k), 0x38, dtype=torch.uint8, device=DEV)
+    one = lambda r: torch.full((-(-r // 128), 4), 127, dtype=torch.uint8, device=DEV)  # noqa: E731
+    a_s, b_s = one(m), one(n)
+    a_s[::2] = 128
+    got = ng.ngram_project_fp8(ng.Fp8(a_codes, a_s, m, k, block_rows=128), ng.Fp8(b_codes, b_s, n, k, block_rows=128))
+    got = got.view(-1, 2, 128, n)
+    for part, want in ((got[:, 0], 256.0), (got[:, 1], 128.0)):
+        lo, hi = torch.aminmax(part)
+        assert float(lo) == want and float(hi) == want
