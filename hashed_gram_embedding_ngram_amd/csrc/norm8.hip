@@ -862,7 +862,7 @@ int ngram_quant_fp8(const void* x, int32_t x_dtype, int64_t n, int32_t d, const 
     a.tiles_d = static_cast<int32_t>(blocks_of(d));
     a.tile_scale = (q ? q : qt)->block_rows == kBlock;
     const int64_t tiles = blocks_of(n) * a.tiles_d;
-    if (tiles > INT32_MAX) return fail(NGRAM_ERANGE, "n=%lld too large for one launch", (long long)n);
+    if (tiles > most_groups(256)) return fail(NGRAM_ERANGE, "n=%lld too large for one launch", (long long)n);
     if (x_dtype == NGRAM_F32)
         hipLaunchKernelGGL((quant_kernel<true>), dim3(static_cast<unsigned>(tiles)), dim3(256), 0, stream, a);
     else
