@@ -55,7 +55,7 @@ struct ProjArgs {
     int32_t ntiles;
     int32_t band;           // tile rows walked together
     int32_t stride;         // items from one of a workgroup to its next
-    int32_t first;          // the launch's first item, a multiple of 8 (few rows: 16 rows of B)
+    int32_t first;          // the launch's first item, a multiple of 8 (few rows: 16 rows of B; not of the large tiles)
 };
 
 // acc + x y, each scaled by the lowest byte of its word.
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int wm = (wave / T::WN) * 16 * TM, wn = (wave % T::WN) * 16 * TN;
-    int w = a.first + static_cast<int>(blockIdx.x), lw = w;
+    int w = blockIdx.x, lw = w;
     Item now = item_of(w, a);
     if (!now.valid) return;
 
@@ -740,11 +740,10 @@ int launch_tile(ProjArgs& a, hipStream_t st) {
     // item; where an item has fewer steps than there are buffers, an item each
     const int64_t room = kUnits * std::max(1, 160 * 1024 / T::Lds);
     const int64_t least = std::min<int64_t>(a.split_steps, a.steps - (a.splits - 1) * a.split_steps);     // the last split's steps
-    const int64_t all = (items + 7) / 8 * 8, groups = least < 4 ? all : std::min(all, room);
-    a.stride = static_cast<int32_t>(groups);
-    in_parts(a, groups, T::Threads, 8, [&](dim3 grid) {
-        hipLaunchKernelGGL((project_fp8_kernel<T>), grid, dim3(T::Threads), T::Lds, st, a);
-    });
+    const dim3 grid(static_cast<unsigned>(least < 4 ? (items + 7) / 8 * 8 : std::min((items + 7) / 8 * 8, room))), block(T::Threads);
+    if (grid.x > most_groups(T::Threads)) return fail(NGRAM_ERANGE, "%lld x %lld too large for one launch", (long long)a.m, (long long)a.n);
+    a.stride = static_cast<int32_t>(grid.x);
+    hipLaunchKernelGGL((project_fp8_kernel<T>), grid, block, T::Lds, st, a);
     return NGRAM_OK;
 }
 

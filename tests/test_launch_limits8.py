@@ -6,7 +6,7 @@ import pytest
 
 import hashed_gram_embedding_ngram_amd as ng
 
-EINVAL, ERANGE = -1, -3
+ERANGE = -3
 A = 0x10000             # a fake, aligned device address (never dereferenced)
 
 
@@ -18,4 +18,12 @@ def fp8(rows, cols, block_rows=1):
 def test_quantiser_of_too_many_tiles(n, d):
     """A workgroup of 256 threads for a tile of 128 x 128: 2^24 - 1 tiles at most."""
     assert ng.lib().ngram_quant_fp8(A, 1, n, d, fp8(n, d), None, None) == ERANGE, ng.lib().ngram_last_error()
+    assert b"too large" in ng.lib().ngram_last_error()
+
+
+@pytest.mark.parametrize("m,n,dtype", [(1 << 30, 8192, 1), (1 << 30, 1 << 20, 0), (1 << 26, 1 << 26, 1)])
+def test_product_of_too_many_tiles(m, n, dtype):
+    """Over one step of K a workgroup has one of the large tiles; their number is a launch's limit."""
+    assert ng.lib().ngram_project_fp8_workspace_bytes(m, n, 128, dtype) == 0
+    assert ng.lib().ngram_project_fp8(fp8(m, 128), fp8(n, 128), A, dtype, None, 0, None) == ERANGE, ng.lib().ngram_last_error()
     assert b"too large" in ng.lib().ngram_last_error()
