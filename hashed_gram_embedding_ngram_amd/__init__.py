@@ -704,6 +704,10 @@ _VALUES = (torch.float32,) + _BF16
 # The calls below are short on the GPU at decode sizes (a few microseconds), so
 # their marshalling is kept short too: tensors go through one check each, and
 # raw pointers, as ints, straight to ctypes.
+#
+# ``stream``: where the call's kernels run, by default the current stream.  Its
+# arguments have to be ready there, and the caller lets the current stream wait
+# for it before reading the results there.
 
 
 def _arg(t, dtypes, count, name):
@@ -726,19 +730,20 @@ def _raw_stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()) if stream is None else stream.cuda_stream
 
 
-def _made(t, stream):
-    """A tensor that a call makes for itself or for its caller: the allocator
-    is told of a stream other than the current one that it is used on."""
-    if stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 def _new(rows, cols, dtype, device, stream):
-    """A contiguous [rows][cols] tensor for _made ([rows] where cols is
-    None); with its strides given, making it takes three quarters of the time."""
+    """A contiguous [rows][cols] tensor ([rows] where cols is None) that a
+    call makes for itself or for its caller; with its strides given, making it
+    takes three quarters of the time.  For a given ``stream`` it is memory of
+    that stream: a block of the current one's may still be in use by what is
+    queued there, which the given stream does not wait for.  The allocator is
+    told of the current stream, on which the caller reads it."""
     shape, strides = ((rows,), (1,)) if cols is None else ((rows, cols), (cols, 1))
-    return _made(torch.empty_strided(shape, strides, dtype=dtype, device=device), stream)
+    if stream is None:
+        return torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty_strided(shape, strides, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
 
 
 def _value(t):
@@ -838,11 +843,12 @@ def ngram_add_norm(x, gamma, eps, residual=None, sum_out=None, y_out=None, q_out
     return NormOut(sum_out, y_out, q_out, r_out)
 
 
-def add_norm_grad_workspace(n: int, d: int, device="cuda:0"):
+def add_norm_grad_workspace(n: int, d: int, device="cuda:0", stream=None):
+    """Workspace of ngram_add_norm_grad, on ``stream`` (by default the current one)."""
     nbytes = lib().ngram_add_norm_grad_workspace_bytes(n, d)
     if nbytes < 0:
         raise NgramError(f"no norm gradient has n={n}, d={d}")
-    return _new(nbytes, None, torch.uint8, device, None)
+    return _new(nbytes, None, torch.uint8, device, stream)
 
 
 def ngram_add_norm_grad(dy, sum, r, gamma, dsum=None, dx_out=None, dgamma_out=None, workspace=None, stream=None):
@@ -858,7 +864,7 @@ def ngram_add_norm_grad(dy, sum, r, gamma, dsum=None, dx_out=None, dgamma_out=No
     if dgamma_out is None:
         dgamma_out = _new(d, None, torch.float32, dy.device, stream)
     if workspace is None:
-        workspace = _made(add_norm_grad_workspace(n, d, dy.device), stream)
+        workspace = add_norm_grad_workspace(n, d, dy.device, stream)
     rc = lib().ngram_add_norm_grad(pdy, _value(dy), ps, pr, pg, _opt(dsum, _BF16, count, "dsum"), n, d,
                                    _arg(dx_out, _BF16, count, "dx_out"), _arg(dgamma_out, _F32, d, "dgamma_out"),
                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream))
@@ -867,13 +873,14 @@ def ngram_add_norm_grad(dy, sum, r, gamma, dsum=None, dx_out=None, dgamma_out=No
     return dx_out, dgamma_out
 
 
-def project_fp8_workspace(m: int, n: int, k: int, dtype=torch.float32, device="cuda:0"):
+def project_fp8_workspace(m: int, n: int, k: int, dtype=torch.float32, device="cuda:0", stream=None):
     """Workspace of ngram_project_fp8 for C [m][n] of ``dtype`` over k
-    columns, or None where the call needs none."""
+    columns, on ``stream`` (by default the current one), or None where the
+    call needs none."""
     nbytes = lib().ngram_project_fp8_workspace_bytes(m, n, k, F32 if dtype is torch.float32 else BF16)
     if nbytes < 0:
         raise NgramError(f"no 8-bit product has m={m}, n={n}, k={k}")
-    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    return _new(nbytes, None, torch.uint8, device, stream) if nbytes else None
 
 
 def ngram_project_fp8(a: Fp8, b: Fp8, out=None, dtype=torch.bfloat16, workspace=None, stream=None):
@@ -886,9 +893,7 @@ def ngram_project_fp8(a: Fp8, b: Fp8, out=None, dtype=torch.bfloat16, workspace=
         out = _new(m, n, dtype, a.codes.device, stream)
     po = _arg(out, _VALUES, m * n, "out")
     if workspace is None:
-        workspace = project_fp8_workspace(m, n, a.cols, out.dtype, out.device)
-        if workspace is not None:
-            _made(workspace, stream)
+        workspace = project_fp8_workspace(m, n, a.cols, out.dtype, out.device, stream)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     rc = lib().ngram_project_fp8(a.c, b.c, po, _value(out), ws, ws_bytes, _raw_stream(stream))
     if rc:
