@@ -746,6 +746,13 @@ def _new(rows, cols, dtype, device, stream):
     return t
 
 
+def _scratch(t):
+    """(pointer, bytes) of a workspace: any contiguous device tensor."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise NgramError("workspace must be a contiguous device tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _value(t):
     """The ngram_value of a tensor that has been checked against _VALUES."""
     return F32 if t.dtype is torch.float32 else BF16
@@ -865,9 +872,10 @@ def ngram_add_norm_grad(dy, sum, r, gamma, dsum=None, dx_out=None, dgamma_out=No
         dgamma_out = _new(d, None, torch.float32, dy.device, stream)
     if workspace is None:
         workspace = add_norm_grad_workspace(n, d, dy.device, stream)
+    ws, ws_bytes = _scratch(workspace)
     rc = lib().ngram_add_norm_grad(pdy, _value(dy), ps, pr, pg, _opt(dsum, _BF16, count, "dsum"), n, d,
                                    _arg(dx_out, _BF16, count, "dx_out"), _arg(dgamma_out, _F32, d, "dgamma_out"),
-                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(stream))
+                                   ws, ws_bytes, _raw_stream(stream))
     if rc:
         _check(rc, "ngram_add_norm_grad")
     return dx_out, dgamma_out
@@ -894,7 +902,7 @@ def ngram_project_fp8(a: Fp8, b: Fp8, out=None, dtype=torch.bfloat16, workspace=
     po = _arg(out, _VALUES, m * n, "out")
     if workspace is None:
         workspace = project_fp8_workspace(m, n, a.cols, out.dtype, out.device, stream)
-    ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws, ws_bytes = (None, 0) if workspace is None else _scratch(workspace)
     rc = lib().ngram_project_fp8(a.c, b.c, po, _value(out), ws, ws_bytes, _raw_stream(stream))
     if rc:
         _check(rc, "ngram_project_fp8")
