@@ -780,6 +780,12 @@ class Fp8:
 
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device="cuda:0", stream=None) -> "Fp8":
+        if torch.device(device).type != "cuda":
+            raise NgramError(f"an 8-bit matrix lies on a GPU, not on device {device}")
+        return cls._empty(rows, cols, block_rows, device, stream)
+
+    @classmethod
+    def _empty(cls, rows, cols, block_rows, device, stream):
         ld, srows, sld = _fp8_shape(rows, cols, block_rows)
         codes = _new(rows, ld, torch.float8_e4m3fn, device, stream)
         scales = _new(srows, sld, torch.uint8, device, stream)
@@ -809,9 +815,9 @@ def ngram_quant_fp8(x, rows=True, transposed=False, block_rows: int = 1, q=None,
     n, d = _matrix(x, "x")
     px = _arg(x, _VALUES, n * d, "x")
     if q is None and rows:
-        q = Fp8.empty(n, d, block_rows, x.device, stream)
+        q = Fp8._empty(n, d, block_rows, x.device, stream)
     if qt is None and transposed:
-        qt = Fp8.empty(d, n, block_rows, x.device, stream)
+        qt = Fp8._empty(d, n, block_rows, x.device, stream)
     rc = lib().ngram_quant_fp8(px, _value(x), n, d, _fp8_c(q), _fp8_c(qt), _raw_stream(stream))
     if rc:
         _check(rc, "ngram_quant_fp8")
@@ -837,7 +843,7 @@ def ngram_add_norm(x, gamma, eps, residual=None, sum_out=None, y_out=None, q_out
     px = _arg(x, _VALUES, count, "x")
     pg = _arg(gamma, _F32, d, "gamma")
     if q_out is None and quantise:
-        q_out = Fp8.empty(n, d, 1, x.device, stream)
+        q_out = Fp8._empty(n, d, 1, x.device, stream)
     if y_out is None and keep_y:
         y_out = _new(n, d, torch.bfloat16, x.device, stream)
     if r_out is None and keep_r:

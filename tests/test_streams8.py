@@ -64,7 +64,7 @@ CALLS = {
     "norm": (lambda s: ng.ngram_add_norm(X, G, 1e-6, keep_y=True, keep_r=True, stream=s), 4),
     "norm_grad": (lambda s: ng.ngram_add_norm_grad(X, X, R, G, stream=s), 3),
     "project": (lambda s: ng.ngram_project_fp8(Q, Q, stream=s), 2),
-    "fp8": (lambda s: ng.Fp8.empty(5, 16, device="cpu", stream=s), 2),
+    "fp8": (lambda s: ng.Fp8.empty(5, 16, stream=s), 2),
 }
 
 

@@ -64,3 +64,10 @@ def test_taken(monkeypatch):
     monkeypatch.setattr(ng, "_check", lambda rc, what: 1 / 0)
     x, r, g = torch.zeros((4, 64)), torch.zeros(4), torch.zeros(64)
     ng.ngram_add_norm_grad(x, x, r, g, dx_out=x, dgamma_out=g, workspace=OnDevice(True))
+
+
+def test_no_8_bit_matrix_in_host_memory(monkeypatch):
+    """Fp8.empty of a device that kernels cannot write."""
+    for device in ("cpu", torch.device("cpu"), "meta"):
+        with pytest.raises(ng.NgramError, match="device"):
+            ng.Fp8.empty(4, 64, device=device)
