@@ -938,10 +938,16 @@ def _adamw_tensor(p, g, m, v, m_scale, v_scale, rng_offset, name, g_numel=None, 
 class AdamWTensors:
     """The tensors of ngram_adamw: equal-length lists of parameters (fp32 or
     bf16), gradients (fp32 or bf16) and moments, fp32 or 8-bit codes with
-    ``m_scales`` and ``v_scales`` (uint8, one byte per 128 elements).  Keeps
-    the tensors alive; build it again when one of them is another tensor.
-    ``rng_offsets``: each tensor's place in the random sequence (by default
-    one after the other, each at a multiple of 128)."""
+    ``m_scales`` and ``v_scales`` (uint8, one byte per 128 elements).
+
+    The list names memory, and keeps that memory: a step reads the gradients
+    and updates the parameters that were given here, whatever their names stand
+    for by then.  Build it again when a gradient or another of them is a new
+    tensor or has new memory (``p.data = ...``).  A program that lets its
+    gradients go builds it each step; one that keeps and refills them (as it
+    has to for a captured graph) does so once.  ``rng_offsets``: each tensor's
+    place in the random sequence (by default one after the other, each at a
+    multiple of 128)."""
 
     def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, rng_offsets=None):
         count = len(params)
@@ -958,6 +964,8 @@ class AdamWTensors:
         self.tensors = [tuple(x) for x in zip(*lists[:6])]
         self.count = count
         self.c = (_AdamWTensor * max(count, 1))(*[_adamw_tensor(*x, name=f"tensor {i}") for i, x in enumerate(zip(*lists))])
+        # a tensor may be given other memory (p.data = ...) while this list lives
+        self.storages = [t.untyped_storage() for x in self.tensors for t in x if t is not None]
 
 
 def ngram_adamw(tensors: AdamWTensors, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, grad_scale=1.0,
