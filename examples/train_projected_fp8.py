@@ -101,10 +101,11 @@ class Layer:
         return dh
 
     def update(self, step, lr=3e-3, seed=0):
-        h = {"lr": lr, "step": step, "seed": seed, "eps": 1e-10}
-        ng.ngram_adamw(self.dense, **h)
-        for rows, grad in zip((self.table, self.e1), self.sparse):
-            rows.update(*grad, **h)
+        h = {"lr": lr, "step": step, "eps": 1e-10}
+        # equal places of two tables round alike under one seed
+        ng.ngram_adamw(self.dense, seed=3 * seed, **h)
+        for i, (rows, grad) in enumerate(zip((self.table, self.e1), self.sparse), start=1):
+            rows.update(*grad, seed=3 * seed + i, **h)
         self.lay_out()
 
 

@@ -983,7 +983,8 @@ def ngram_adamw_rows(p, m, v, rows, g, n_rows=None, m_scale=None, v_scale=None, 
     """One AdamW step on rows ``rows`` of the table p [R][d] from the sparse
     gradient (rows, g [max_rows][d], n_rows [1] int64 on the device) that
     ngram_grad_table and ngram_grad_e1 return (see ngram_adamw_rows in
-    ngram.h)."""
+    ngram.h).  Two tables, or a table and the tensors of ngram_adamw, round
+    alike at equal places under one ``seed``: give each its own."""
     R, d = _matrix(p, "p")
     max_rows = 0 if rows is None else rows.numel()
     pr, pn = _arg(rows, _I32T, 0, "rows"), _opt(n_rows, (torch.int64,), 1, "n_rows")

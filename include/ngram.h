@@ -559,7 +559,9 @@ int ngram_adamw(const ngram_adamw_tensor* tensors, int32_t count, const ngram_ad
 
 /* The step on the touched rows of a table, from a sparse gradient as
  * ngram_grad_table and ngram_grad_e1 write it: table->p, m, v [R][d]
- * (numel = R d, rng_offset 0), scales [R][ceil(d / 128)]; row rows[u] takes
+ * (numel = R d, rng_offset 0: the random words go by seed, step and place in
+ * the table alone, so each table, and the tensors of ngram_adamw, take a seed
+ * of their own), scales [R][ceil(d / 128)]; row rows[u] takes
  * the gradient row table->g [max_rows][d], u < min(*n_rows, max_rows),
  * max_rows <= NGRAM_MAX_ROWS.  n_rows
  * (device int64; NULL: max_rows) is read on the device, so the number of rows
