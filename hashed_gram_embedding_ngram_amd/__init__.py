@@ -9,6 +9,7 @@ There is no fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import NamedTuple, Optional
@@ -891,14 +892,15 @@ def project_fp8_workspace(m: int, n: int, k: int, dtype=torch.float32, device="c
     """Workspace of ngram_project_fp8 for C [m][n] of ``dtype`` over k
     columns, on ``stream`` (by default the current one), or None where the
     call needs none."""
-    nbytes = lib().ngram_project_fp8_workspace_bytes(m, n, k, F32 if dtype is torch.float32 else BF16)
+    nbytes = lib().ngram_project_fp8_workspace_bytes(m, n, max(k, 1), F32 if dtype is torch.float32 else BF16)
     if nbytes < 0:
         raise NgramError(f"no 8-bit product has m={m}, n={n}, k={k}")
     return _new(nbytes, None, torch.uint8, device, stream) if nbytes else None
 
 
 def ngram_project_fp8(a: Fp8, b: Fp8, out=None, dtype=torch.bfloat16, workspace=None, stream=None):
-    """out [a.rows][b.rows] (fp32 or bf16) = a b^T over their common columns.
+    """out [a.rows][b.rows] (fp32 or bf16) = a b^T over their common columns
+    (of none, as in the weight gradient of an empty batch: zeros).
     A bf16 result of more than 32 rows keeps 13 bits below the largest product
     of each eight columns, an fp32 result everything (see ngram_project_fp8 in
     ngram.h)."""
@@ -906,6 +908,10 @@ def ngram_project_fp8(a: Fp8, b: Fp8, out=None, dtype=torch.bfloat16, workspace=
     if out is None:
         out = _new(m, n, dtype, a.codes.device, stream)
     po = _arg(out, _VALUES, m * n, "out")
+    if a.cols == 0 and b.cols == 0 and n > 0 and n % 8 == 0:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            out.view(-1)[:m * n].zero_()
+        return out
     if workspace is None:
         workspace = project_fp8_workspace(m, n, a.cols, out.dtype, out.device, stream)
     ws, ws_bytes = (None, 0) if workspace is None else _scratch(workspace)

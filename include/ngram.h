@@ -493,7 +493,8 @@ int ngram_add_norm_grad(const void* dy, int32_t dy_dtype, const uint16_t* sum, c
  * Either operand may have block_rows 1 or 128.  The layer y = P x is A = x, B = P (n x k = d_out x d_in); its
  * gradients are dx: A = dy, B = P transposed (ngram_quant_fp8's qt, its tile
  * scales the same), and dP: A = dy transposed, B = x transposed, both with
- * their blocks along the tokens.  k <= 2^23.  A NaN code gives NaN in its row or column
+ * their blocks along the tokens.  1 <= k <= 2^23 (a sum over no columns is
+ * EINVAL: C is to be cleared instead, as the Python binding does).  A NaN code gives NaN in its row or column
  * of C.  workspace: device, 16-byte aligned,
  * ngram_project_fp8_workspace_bytes(m, n, k, c_dtype) bytes (0 for many
  * sizes: then it may be NULL).  Errors: EINVAL, EALIGN, ERANGE; m = 0 launches nothing. */
