@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(T::Threads, 1) project_fp8_kernel(const ProjAr
         // for as long as the CU's one load path needs for it (16 cycles or
         // more), so the large tile's loads are spread: A's over the tail of
         // the step that frees the buffer, B's over the head of the next.
-        i32x8 over;
+        i32x8 over = {};        // the last row's, where two are multiplied after the barrier
 #pragma unroll
         for (int s = 0; s < TM - T::Tail; ++s) {
             next = frag(at, s + 1);
@@ -647,7 +647,6 @@ __global__ void __launch_bounds__(64 * kRowWaves) project_fp8_rows_kernel(const 
     f32x4 acc[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
     for (int kb = wave; kb < a.steps; kb += kRowWaves) {
         const u32x4* const p = reinterpret_cast<const u32x4*>(bp + static_cast<int64_t>(kb) * kStep);
         const Wide fb = widen(join(p[0], p[1]), bsp[kb]);
