@@ -482,10 +482,13 @@ __global__ void __launch_bounds__(64 * kMaxWaves) add_norm_grad_few_kernel(const
 // then leave as whole 128-byte lines.
 //
 // Bound by memory, with the two barriers of a tile in the way: 8192 x 2560 in
-// bf16, both outputs, 19.8 us, 4.2 TB/s (a large copy 5.5), the transposed one
-// alone 14.4.  Streaming stores: 18.2 and 12.6 us, but the products that read
-// the codes next then take longer (a layer's two gradients 206 us against
-// 199), so the stores are plain.
+// bf16, both outputs, 20.2 us, 4.2 TB/s (a large copy 5.5), the transposed one
+// alone 14.4, the rows alone 12.3; among a layer's products 22 and 16.  128 x
+// 128 tiles, both outputs: 2560 x 2560 in fp32 10.8 us, 3.6 TB/s (400 tiles for
+// 256 compute units), 8192 x 8192 in bf16 55 us, 4.9 TB/s.  Streaming stores took
+// 18.2 and 12.6 us where plain ones took 19.8 and 14.4, but the products that
+// read the codes next took longer (a layer's two gradients 206 us against 199
+// with the products of that time), so the stores are plain.
 struct QuantArgs {
     const void* x;
     uint8_t *q, *qs, *qt, *qts;
