@@ -416,7 +416,7 @@ TensorArg part_of(const ngram_adamw_tensor& t, int64_t from, int64_t take) {
     return TensorArg{static_cast<uint8_t*>(t.p) + from * pb, static_cast<const uint8_t*>(t.g) + from * gb,
                      static_cast<uint8_t*>(t.m) + from * sb, static_cast<uint8_t*>(t.v) + from * sb,
                      t.m_scale ? t.m_scale + from / kBlock : nullptr, t.v_scale ? t.v_scale + from / kBlock : nullptr,
-                     take, static_cast<uint64_t>(t.rng_offset + from)};
+                     take, static_cast<uint64_t>(t.rng_offset) + static_cast<uint64_t>(from)};
 }
 
 #define NG8_BY_KIND(kind, CALL)                      \
