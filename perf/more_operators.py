@@ -242,7 +242,7 @@ def _plain_distill(s):
     t = torch.where(on, s["teacher"].float() / T, torch.full_like(s["teacher"], NEG, dtype=torch.float32))
     any_on = on.any(dim=1, keepdim=True)
     log_q = z.gather(1, ids) - lse
-    stats = torch.stack((lse[:, 0], torch.zeros_like(lse[:, 0])), dim=1)
+    stats = torch.stack((s["logits"].float().amax(dim=1), e.sum(dim=1).log(), torch.zeros_like(lse[:, 0])), dim=1)
     if s["tail"]:
         log_p = t - s["teacher_lse"][:, None]
     else:
@@ -259,7 +259,7 @@ def _plain_distill(s):
         off[row[on], ids[on]] = False
         mass = torch.where(off, e, torch.zeros_like(e)).sum(dim=1)
         log_rest = (m[:, 0] + mass.log()) - lse[:, 0]
-        stats[:, 1] = log_rest
+        stats[:, 2] = log_rest
         loss = loss + torch.where(rest > 0, rest * (rest.log() - log_rest), torch.zeros_like(rest))
         factor = torch.where(rest > 0, 1.0 - (rest.log() - log_rest).exp(), torch.ones_like(rest))
         g = torch.where(off, q * factor[:, None], q)
@@ -500,7 +500,7 @@ def _x_beam_reorder(s, case):
 def _x_distill(s, case):
     T, V, n = s["T"], s["V"], s["n"]
     loss = torch.empty(n, dtype=torch.float64, device=DEV)
-    stats = torch.zeros((n, 2), dtype=torch.float64, device=DEV)
+    stats = torch.zeros((n, 3), dtype=torch.float64, device=DEV)
     grad = torch.empty((n, V), dtype=torch.float64, device=DEV)
     for at in range(0, n, 256):
         cut = slice(at, min(at + 256, n))
@@ -527,11 +527,12 @@ def _x_distill(s, case):
             row_loss = row_loss + torch.xlogy(rest, rest) - torch.where(rest > 0, rest * log_rest, torch.zeros_like(rest))
             ratio = torch.where(rest > 0, rest / torch.exp(log_rest), torch.zeros_like(rest))
             g = torch.where(listed_, g, g * (1 - ratio[:, None]))
-            stats[cut, 1] = log_rest
+            stats[cut, 2] = log_rest
         w = s["weight"][cut].double()[:, None]
         grad[cut] = (g - P) * w * (s["scale"] * T)
         loss[cut] = row_loss * T * T
-        stats[cut, 0] = torch.logsumexp(s["logits"][cut].double() / T, dim=1)
+        stats[cut, 0] = s["logits"][cut].double().max(dim=1).values
+        stats[cut, 1] = torch.logsumexp((s["logits"][cut].double() - stats[cut, :1]) / T, dim=1)
     return {"loss": loss, "dlogits": grad} | ({} if s["fused"] else {"stats": stats})
 
 
