@@ -65,6 +65,21 @@ class _AdamWStep(ctypes.Structure):
                 ("step", ctypes.c_int64), ("seed", ctypes.c_uint64)]
 
 
+class _Int4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("group", ctypes.c_int32), ("scale_dtype", ctypes.c_int32)]
+
+
+class _BeamState(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_bytes", ctypes.c_int64), ("stride", ctypes.c_int64)]
+
+
+class _DistillArgs(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("teacher", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("teacher_lse", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("V", ctypes.c_int64), ("ld", ctypes.c_int64), ("k", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("teacher_dtype", ctypes.c_int32), ("temperature", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -121,6 +136,17 @@ _SIGNATURES = {
     "ngram_adamw": (ctypes.c_int, [ctypes.POINTER(_AdamWTensor), _I32, ctypes.POINTER(_AdamWStep), _P]),
     "ngram_adamw_rows": (ctypes.c_int, [ctypes.POINTER(_AdamWTensor), _I64, _I32, _P, _I64, _P,
                                         ctypes.POINTER(_AdamWStep), _P]),
+    "ngram_int4_code_bytes": (ctypes.c_int64, [_I64, _I64]),
+    "ngram_int4_scales": (ctypes.c_int64, [_I64, _I64, _I32]),
+    "ngram_quant_int4": (ctypes.c_int, [_P, _I32, _I64, _I32, ctypes.POINTER(_Int4), _P]),
+    "ngram_dequant_int4": (ctypes.c_int, [ctypes.POINTER(_Int4), _P, _I32, _P]),
+    "ngram_project_int4": (ctypes.c_int, [_P, _I32, _I64, ctypes.POINTER(_Int4), _P, _I32, _P]),
+    "ngram_beam_step_workspace_bytes": (ctypes.c_int64, [_I64, _I32, _I64, _I32]),
+    "ngram_beam_step": (ctypes.c_int, [_P, _I32, _I64, _I32, _I64, _I64, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _I64, _P]),
+    "ngram_beam_reorder": (ctypes.c_int, [ctypes.POINTER(_BeamState), _I32, _P, _I64, _I32, _P]),
+    "ngram_distill_workspace_bytes": (ctypes.c_int64, [_I64, _I64, _I32]),
+    "ngram_distill": (ctypes.c_int, [ctypes.POINTER(_DistillArgs), _P, _P, _P, ctypes.c_float, _P, _I64, _P, _I64, _P]),
+    "ngram_distill_grad": (ctypes.c_int, [ctypes.POINTER(_DistillArgs), _P, _P, ctypes.c_float, _P, _I64, _P]),
 }
 
 _lib = None
@@ -999,3 +1025,270 @@ def ngram_adamw_rows(p, m, v, rows, g, n_rows=None, m_scale=None, v_scale=None, 
                                 _raw_stream(stream))
     if rc:
         _check(rc, "ngram_adamw_rows")
+
+
+INT4_GROUPS = (32, 64, 128)
+INT4_MAX_ROWS = 1 << 24
+INT4_MAX_COLS = 1 << 20
+MAX_BEAMS = 32
+DISTILL_MAX_K = 1024
+
+_MARKS = (torch.bool, torch.uint8)
+
+
+def _here(stream, *tensors):
+    """Refuse tensors of another device than the current one, on whose queue the call goes."""
+    d = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != d:
+            raise NgramError(f"a tensor of {t.device} in a call on cuda:{d}: make its device the current one")
+    if stream is not None and stream.device_index != d:
+        raise NgramError(f"a stream of cuda:{stream.device_index} in a call on cuda:{d}")
+
+
+def _rows_arg(t, dtypes, name):
+    """(pointer, rows, columns, distance of rows in elements) of a device matrix whose rows are contiguous."""
+    n, v = _matrix(t, name)
+    if t.dtype not in dtypes or not t.is_cuda:
+        _dev(t, dtypes, name)
+    sn, sv = t.stride()
+    if sv != 1 and v > 1:
+        raise NgramError(f"the rows of {name} must be contiguous")
+    if sn < v:
+        if n > 1:
+            raise NgramError(f"the rows of {name} overlap")
+        sn = v
+    return t.data_ptr(), n, v, sn
+
+
+class Int4:
+    """A matrix in 4 bits: ``codes`` [rows][16 ceil(cols / 32)] bytes, ``scales`` (fp32 or bf16) and optionally ``zeros``
+    (bytes) [rows][4 ceil(ceil(cols / group) / 4)]; see "4-bit matrices" in ngram.h.  It keeps its tensors."""
+
+    __slots__ = ("codes", "scales", "zeros", "rows", "cols", "group", "c")
+
+    def __init__(self, codes, scales, rows: int, cols: int, group: int = 128, zeros=None):
+        ld, sld = _int4_shape(rows, cols, group)
+        self.rows, self.cols, self.group = rows, cols, group
+        self.codes, self.scales, self.zeros = codes, scales, zeros
+        self.c = _Int4(_arg(codes, (torch.uint8,), rows * ld, "codes"), _arg(scales, _VALUES, rows * sld, "scales"),
+                       _opt(zeros, (torch.uint8,), rows * sld, "zeros"), rows, cols, group, _value(scales))
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, group: int = 128, zeros: bool = True, scale_dtype=torch.bfloat16, device="cuda:0",
+              stream=None) -> "Int4":
+        if torch.device(device).type != "cuda":
+            raise NgramError(f"a 4-bit matrix lies on a GPU, not on device {device}")
+        ld, sld = _int4_shape(rows, cols, group)
+        return cls(_new(rows, ld, torch.uint8, device, stream), _new(rows, sld, scale_dtype, device, stream), rows, cols, group,
+                   _new(rows, sld, torch.uint8, device, stream) if zeros else None)
+
+
+def _int4_shape(rows, cols, group):
+    """(code bytes a row, scales a row), as ngram_int4_code_bytes and ngram_int4_scales count them."""
+    if not (0 <= rows <= INT4_MAX_ROWS and 0 <= cols <= INT4_MAX_COLS) or cols % 8 or group not in INT4_GROUPS:
+        raise NgramError(f"no 4-bit matrix has rows={rows}, cols={cols}, group={group}")
+    return (cols + 31) // 32 * 16, ((cols + group - 1) // group + 3) // 4 * 4
+
+
+def ngram_quant_int4(x, group: int = 128, zeros: bool = True, scale_dtype=torch.bfloat16, out: Optional[Int4] = None, stream=None) -> Int4:
+    """x [n][d] (fp32 or bf16) in 4 bits (see ngram_quant_int4 in ngram.h); ``out``: the Int4 to fill, whose group, zeros
+    and scales' type then count."""
+    n, d = _matrix(x, "x")
+    px = _arg(x, _VALUES, n * d, "x")
+    _here(stream, x)
+    if out is None:
+        out = Int4.empty(n, d, group, zeros, scale_dtype, x.device, stream)
+    _here(stream, out.codes, out.scales, out.zeros)
+    rc = lib().ngram_quant_int4(px, _value(x), n, d, out.c, _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_quant_int4")
+    return out
+
+
+def ngram_dequant_int4(q: Int4, out=None, dtype=torch.float32, stream=None):
+    """The values of q, [q.rows][q.cols] fp32 or bf16 (see ngram_dequant_int4 in ngram.h)."""
+    _here(stream, q.codes, q.scales, q.zeros, out)
+    if out is None:
+        out = _new(q.rows, q.cols, dtype, q.codes.device, stream)
+    rc = lib().ngram_dequant_int4(q.c, _arg(out, _VALUES, q.rows * q.cols, "out"), _value(out), _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_dequant_int4")
+    return out
+
+
+def ngram_project_int4(x, w: Int4, out=None, dtype=torch.bfloat16, stream=None):
+    """out [n][w.rows] (fp32 or bf16) = x w^T for x [n][w.cols] (fp32 or bf16; see ngram_project_int4 in ngram.h)."""
+    n, k = _matrix(x, "x")
+    if k != w.cols:
+        raise NgramError(f"x has {k} columns and w {w.cols}")
+    px = _arg(x, _VALUES, n * k, "x")
+    _here(stream, x, w.codes, out)
+    if out is None:
+        out = _new(n, w.rows, dtype, x.device, stream)
+    rc = lib().ngram_project_int4(px, _value(x), n, w.c, _arg(out, _VALUES, n * w.rows, "out"), _value(out), _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_project_int4")
+    return out
+
+
+class BeamOut(NamedTuple):
+    """ngram_beam_step's outputs, one entry (history: two) for each row; None for those not asked for."""
+    scores: torch.Tensor
+    tokens: Optional[torch.Tensor]
+    parents: torch.Tensor
+    history: Optional[torch.Tensor]
+    finished: Optional[torch.Tensor]
+
+
+def beam_step_workspace(batch: int, beams: int, V: int, dtype=torch.float32, device="cuda:0", stream=None):
+    """Workspace of ngram_beam_step, on ``stream`` (by default the current one)."""
+    nbytes = lib().ngram_beam_step_workspace_bytes(batch, beams, V, F32 if dtype is torch.float32 else BF16)
+    if nbytes < 0:
+        raise NgramError(f"no beam step has batch={batch}, beams={beams}, V={V}")
+    return _new(nbytes, None, torch.uint8, device, stream)
+
+
+def ngram_beam_step(logits, scores, beams: int, tokens=None, history=None, finished=None, end_token: int = -1,
+                    out: Optional[BeamOut] = None, workspace=None, stream=None) -> BeamOut:
+    """The next beams of every sequence from logits [batch * beams][V] (fp32 or bf16; rows at any distance) and the beams'
+    scores (see ngram_beam_step in ngram.h).  ``tokens``, the tokens fed at this step, and ``history`` [rows][2], what
+    ngram_forward took with them, give the next history; ``finished`` (bool or uint8) marks beams that have ended.
+    ``out``: where to write, whose tensors may be the inputs of the same names; a None there is not written."""
+    pl, rows, V, ld = _rows_arg(logits, _VALUES, "logits")
+    if beams < 1 or rows % beams:
+        raise NgramError(f"{rows} rows of logits are no whole sequences of {beams} beams")
+    batch = rows // beams
+    _here(stream, logits, scores, tokens, history, finished, workspace)
+    if out is None:
+        dev = logits.device
+        out = BeamOut(_new(rows, None, torch.float32, dev, stream), _new(rows, None, torch.int32, dev, stream),
+                      _new(rows, None, torch.int32, dev, stream), None if history is None else _new(rows, 2, torch.int32, dev, stream),
+                      _new(rows, None, torch.bool, dev, stream) if end_token >= 0 else None)
+    else:
+        _here(stream, *out)
+    if workspace is None:
+        workspace = beam_step_workspace(batch, beams, V, logits.dtype, logits.device, stream)
+    ws, ws_bytes = _scratch(workspace)
+    rc = lib().ngram_beam_step(pl, _value(logits), batch, beams, V, ld, _arg(scores, _F32, rows, "scores"),
+                               _opt(tokens, _I32T, rows, "tokens"), _opt(history, _I32T, 2 * rows, "history"),
+                               _opt(finished, _MARKS, rows, "finished"), end_token, _arg(out.scores, _F32, rows, "out.scores"),
+                               _opt(out.tokens, _I32T, rows, "out.tokens"), _arg(out.parents, _I32T, rows, "out.parents"),
+                               _opt(out.history, _I32T, 2 * rows, "out.history"), _opt(out.finished, _MARKS, rows, "out.finished"),
+                               ws, ws_bytes, _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_beam_step")
+    return out
+
+
+class BeamStates:
+    """The tensors that ngram_beam_reorder moves: each has the rows of all beams as its first dimension (at any distance),
+    and contiguous rows.  The list names memory, and keeps that memory."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        rows = {t.shape[0] for t in self.tensors if t.dim() > 0}
+        if any(t.dim() == 0 for t in self.tensors) or len(rows) > 1:
+            raise NgramError("every state must have the same rows as its first dimension")
+        self.rows = rows.pop() if rows else 0
+        c = []
+        for i, t in enumerate(self.tensors):
+            if not t.is_cuda:
+                raise NgramError(f"state {i} must be a device tensor")
+            if self.rows > 0 and not t[0].is_contiguous():
+                raise NgramError(f"state {i}: its rows must be contiguous")
+            size = t.element_size()
+            row = t.numel() // max(self.rows, 1) * size
+            stride = t.stride(0) * size if self.rows > 1 else row
+            if stride < row:
+                raise NgramError(f"state {i}: its rows overlap")
+            c.append(_BeamState(t.data_ptr(), row, stride))
+        self.count = len(c)
+        self.c = (_BeamState * max(self.count, 1))(*c)
+        self.storages = [t.untyped_storage() for t in self.tensors]
+
+
+def ngram_beam_reorder(states: BeamStates, parents, beams: int, stream=None):
+    """Every state's row of a beam takes the row of the beam's parent, in place (see ngram_beam_reorder in ngram.h);
+    ``parents`` as ngram_beam_step returns them."""
+    rows = parents.numel()
+    if beams < 1 or rows % beams or (states.count and rows != states.rows):
+        raise NgramError(f"{rows} parents for {states.rows} rows of {beams} beams a sequence")
+    _here(stream, parents, *states.tensors[:1])
+    rc = lib().ngram_beam_reorder(states.c, states.count, _arg(parents, _I32T, rows, "parents"), rows // beams, beams, _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_beam_reorder")
+
+
+class DistillOut(NamedTuple):
+    """ngram_distill's outputs; None for those not asked for."""
+    loss: Optional[torch.Tensor]
+    stats: Optional[torch.Tensor]
+    dlogits: Optional[torch.Tensor]
+
+
+def distill_workspace(n: int, V: int, dtype=torch.float32, device="cuda:0", stream=None):
+    """Workspace of ngram_distill, on ``stream`` (by default the current one)."""
+    nbytes = lib().ngram_distill_workspace_bytes(n, V, F32 if dtype is torch.float32 else BF16)
+    if nbytes < 0:
+        raise NgramError(f"no distillation has n={n}, V={V}")
+    return _new(nbytes, None, torch.uint8, device, stream)
+
+
+def _distill_args(logits, teacher, ids, temperature, teacher_lse):
+    pz, n, V, ld = _rows_arg(logits, _VALUES, "logits")
+    rows, k = _matrix(teacher, "teacher")
+    if rows != n or ids is None or ids.shape != teacher.shape:
+        raise NgramError("teacher and ids must have a row for each row of logits, and equal shapes")
+    return _DistillArgs(pz, _arg(teacher, _VALUES, n * k, "teacher"), _arg(ids, _I32T, n * k, "ids"), _opt(teacher_lse, _F32, n, "teacher_lse"),
+                        n, V, ld, k, _value(logits), _value(teacher), temperature)
+
+
+def _dlogits(logits, n, V, dlogits_out, stream):
+    """(tensor, pointer, distance of rows) of the gradient's buffer."""
+    if dlogits_out is None:
+        dlogits_out = _new(n, V, logits.dtype, logits.device, stream)
+        return dlogits_out, dlogits_out.data_ptr(), V
+    p, rows, cols, ld = _rows_arg(dlogits_out, (logits.dtype,), "dlogits_out")
+    if rows != n or cols != V:
+        raise NgramError(f"dlogits_out is {rows} x {cols}, logits {n} x {V}")
+    return dlogits_out, p, ld
+
+
+def ngram_distill(logits, teacher, ids, temperature: float = 1.0, teacher_lse=None, grad: bool = False, weight=None, scale: float = 1.0,
+                  keep_stats: bool = False, loss_out=None, stats_out=None, dlogits_out=None, workspace=None, stream=None) -> DistillOut:
+    """Loss [n] fp32 of the student's logits [n][V] against the teacher's top logits ``teacher`` [n][k] at tokens ``ids``
+    [n][k] (see ngram_distill in ngram.h), and with ``grad`` or ``dlogits_out`` (which may be ``logits``) the gradient of the
+    sum of weight * scale * loss in the same call.  ``keep_stats``: what ngram_distill_grad reads."""
+    a = _distill_args(logits, teacher, ids, temperature, teacher_lse)
+    n, V, dev = a.n, a.V, logits.device
+    _here(stream, logits, teacher, ids, teacher_lse, weight, loss_out, stats_out, dlogits_out, workspace)
+    if loss_out is None:
+        loss_out = _new(n, None, torch.float32, dev, stream)
+    if stats_out is None and keep_stats:
+        stats_out = _new(n, 3, torch.float32, dev, stream)
+    pd, dld = None, V
+    if grad or dlogits_out is not None:
+        dlogits_out, pd, dld = _dlogits(logits, n, V, dlogits_out, stream)
+    if workspace is None:
+        workspace = distill_workspace(n, V, logits.dtype, dev, stream)
+    ws, ws_bytes = _scratch(workspace)
+    rc = lib().ngram_distill(a, _arg(loss_out, _F32, n, "loss_out"), _opt(stats_out, _F32, 3 * n, "stats_out"),
+                             _opt(weight, _F32, n, "weight"), scale, pd, dld, ws, ws_bytes, _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_distill")
+    return DistillOut(loss_out, stats_out, dlogits_out)
+
+
+def ngram_distill_grad(logits, teacher, ids, stats, temperature: float = 1.0, teacher_lse=None, weight=None, scale: float = 1.0,
+                       dlogits_out=None, stream=None):
+    """The gradient [n][V] of the sum of weight * scale * loss, from the forward's ``stats`` (see ngram_distill in ngram.h);
+    ``dlogits_out`` may be ``logits``."""
+    a = _distill_args(logits, teacher, ids, temperature, teacher_lse)
+    _here(stream, logits, teacher, ids, stats, teacher_lse, weight, dlogits_out)
+    dlogits_out, pd, dld = _dlogits(logits, a.n, a.V, dlogits_out, stream)
+    rc = lib().ngram_distill_grad(a, _arg(stats, _F32, 3 * a.n, "stats"), _opt(weight, _F32, a.n, "weight"), scale, pd, dld,
+                                  _raw_stream(stream))
+    if rc:
+        _check(rc, "ngram_distill_grad")
+    return dlogits_out

@@ -12,7 +12,8 @@ import tempfile
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc", "ngram.hip")
-SOURCES = [SRC] + [os.path.join(HERE, "csrc", f) for f in ("norm8.hip", "project8.hip", "adamw8.hip")]
+SOURCES = [SRC] + [os.path.join(HERE, "csrc", f) for f in ("norm8.hip", "project8.hip", "adamw8.hip", "int4.hip", "beam8.hip",
+                                                               "distill8.hip")]
 LIB = os.path.join(HERE, "libngram.so")
 ARCH = os.environ.get("NGRAM_OFFLOAD_ARCH", "gfx950")
 

@@ -1,0 +1,435 @@
+// Beam search for MI355X (gfx950): ngram_beam_step, ngram_beam_reorder.  The
+// formulas are in include/ngram.h.
+#include "rows8.h"
+
+#include <algorithm>
+
+namespace ng8 {
+namespace {
+
+// A logit and its token in one number that orders candidates of a beam: a
+// larger logit first, then a lower token.  0 is no candidate.
+__device__ __forceinline__ uint64_t key_of(float x, int token) {
+    uint32_t u = __float_as_uint(x + 0.0f);                         // -0 becomes 0
+    u = u & 0x80000000u ? ~u : u | 0x80000000u;
+    return static_cast<uint64_t>(u) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(token));
+}
+__device__ __forceinline__ float key_logit(uint64_t k) {
+    const uint32_t u = static_cast<uint32_t>(k >> 32);
+    return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+__device__ __forceinline__ int key_token(uint64_t k) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k)); }
+
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp64(uint64_t x) {
+    return static_cast<uint64_t>(dpp<CTRL>(static_cast<uint32_t>(x >> 32))) << 32 | dpp<CTRL>(static_cast<uint32_t>(x));
+}
+__device__ __forceinline__ uint64_t lane64(uint64_t x, int lane) {
+    return static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x >> 32), lane))) << 32 |
+           static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(x)), lane));
+}
+__device__ __forceinline__ uint64_t wave_max64(uint64_t x) {
+    x = max(x, dpp64<0xB1>(x));
+    x = max(x, dpp64<0x4E>(x));
+    x = max(x, dpp64<0x141>(x));
+    x = max(x, dpp64<0x140>(x));
+    return max(max(lane64(x, 0), lane64(x, 16)), max(lane64(x, 32), lane64(x, 48)));
+}
+
+struct StepArgs {
+    const void* logits;
+    const float* scores;
+    const int32_t* tokens;
+    const int32_t* history;
+    const uint8_t* finished;
+    float* scores_out;
+    int32_t* tokens_out;
+    int32_t* parents_out;
+    int32_t* history_out;
+    uint8_t* finished_out;
+    uint64_t* keys;         // [rows][lists][beams], each list falling, 0 past its end
+    Soft* soft;             // [rows][lists]
+    int64_t ld;
+    int64_t first;          // the launch's first row (scan) or sequence (join)
+    int32_t v, beams, end;
+    int32_t chunks;         // workgroups a row
+    int32_t lists;          // wavefronts a row: 4 chunks
+};
+
+__device__ __forceinline__ bool alive(const StepArgs& a, int64_t row) { return a.scores[row] > kNegInf; }
+
+constexpr int kScanWaves = 4;
+constexpr int kRoom = 640;          // keys of a wavefront's buffer: below 128 kept plus 512 of one vector
+
+// The `keep` largest keys of buf[0 .. count) to buf[0 .. keep), falling; 0 past
+// the last.  Each lane watches the places lane, lane + 64, ...
+__device__ __forceinline__ void compress(uint64_t* buf, int count, int keep, int lane) {
+    uint64_t best = 0;
+    for (int i = lane; i < count; i += 64) best = max(best, buf[i]);
+    uint64_t out = 0;
+    for (int r = 0; r < keep; ++r) {
+        const uint64_t top = wave_max64(best);
+        if (lane == r) out = top;
+        if (top == 0) break;
+        if (best == top) {
+            best = 0;
+            for (int i = lane; i < count; i += 64) {
+                const uint64_t k = buf[i];
+                if (k < top) best = max(best, k);
+            }
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (lane < keep) buf[lane] = out;
+    __builtin_amdgcn_wave_barrier();
+}
+
+// One pass over the logits: a wavefront takes a run of a row's vectors, keeps
+// the running maximum and sum of the softmax in each lane, and the `beams`
+// largest logits in a buffer in LDS: an element above the threshold (the
+// smallest kept so far) is appended, and the buffer is cut to the largest when
+// it fills, which raises the threshold.  A wavefront walks upwards, so an
+// element equal to the threshold has a higher token than those kept.
+template <bool F32>
+__global__ void __launch_bounds__(64 * kScanWaves) beam_scan_kernel(const StepArgs a) {
+    constexpr int E = Row<F32>::E;
+    constexpr float c = 1.44269504088896340736f;
+    __shared__ uint64_t room[kScanWaves][kRoom];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t row = a.first + blockIdx.x / a.chunks;
+    const int list = static_cast<int>(blockIdx.x % a.chunks) * kScanWaves + wave;
+    if (!alive(a, row) || (a.finished && a.finished[row])) return;
+    uint64_t* const buf = room[wave];
+    const Row<F32> r(a.logits, row * a.ld, a.v);
+    const int vectors = r.vectors();
+    const int groups = (vectors + 63) / 64, per = (groups + a.lists - 1) / a.lists;
+    const int from = list * per * 64, to = min(vectors, from + per * 64);
+    Soft soft{kLowest, 0.0f};
+    float thr = kNegInf;
+    int count = 0;
+    for (int i0 = from; i0 < to; i0 += 64) {
+        const int i = i0 + lane;
+        u32x4 raw;
+        float x[E];
+        float top = kNegInf;
+        if (i < to) {
+            raw = r.load(i);
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                x[k] = Row<F32>::at(raw, k);
+                top = fmaxf(top, x[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < E; ++k) x[k] = kNegInf;
+        }
+        const float m = fmaxf(soft.m, top);
+        soft.s *= exp2_fast((soft.m - m) * c);
+        soft.m = m;
+#pragma unroll
+        for (int k = 0; k < E; ++k) soft.s += exp2_fast((x[k] - m) * c);
+        if (__ballot(top > thr) == 0) continue;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const uint64_t hit = __ballot(x[k] > thr);
+            if (x[k] > thr) {
+                const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(hit >> 32),
+                                                             __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(hit), 0));
+                buf[count + before] = key_of(x[k], i * E + k);
+            }
+            count += __popcll(hit);
+        }
+        if (count >= 64) {
+            __builtin_amdgcn_wave_barrier();
+            compress(buf, count, a.beams, lane);
+            count = min(count, a.beams);
+            if (count == a.beams) thr = key_logit(buf[count - 1]);
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+    compress(buf, count, a.beams, lane);
+    const int64_t at = row * a.lists + list;
+    if (lane < a.beams) a.keys[at * a.beams + lane] = buf[lane];
+    soft = soft_wave(soft, c);
+    if (lane == 0) a.soft[at] = soft;
+}
+
+// A sequence's lists joined: a wavefront a beam merges its sorted lists (a
+// lane holds the head of one), then one wavefront merges the beams, each lane
+// holding the head of one beam's list.
+constexpr int kJoinWaves = 8;
+
+__global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(const StepArgs a) {
+    __shared__ uint64_t best[NGRAM_MAX_BEAMS][NGRAM_MAX_BEAMS];
+    // a candidate's score is score + ((logit - max) - log sum exp(logits - max)), in an order that keeps
+    // the differences of huge logits
+    __shared__ double score_of[NGRAM_MAX_BEAMS], log_sum[NGRAM_MAX_BEAMS], max_of[NGRAM_MAX_BEAMS];
+    __shared__ int done[NGRAM_MAX_BEAMS];
+    __shared__ int last[NGRAM_MAX_BEAMS][2];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t row0 = (a.first + blockIdx.x) * a.beams;
+    for (int b = wave; b < a.beams; b += kJoinWaves) {
+        const int64_t row = row0 + b;
+        const double score = a.scores[row];
+        const bool fin = a.finished && a.finished[row];
+        double log_s = 0, m = 0;
+        uint64_t out = 0;
+        if (!alive(a, row)) {
+            ;                                               // no candidate
+        } else if (fin) {
+            if (lane == 0) out = key_of(0.0f, a.end);       // its score and no more
+        } else {
+            // lists of this row: at most 64
+            Soft s{kLowest, 0.0f};
+            uint64_t head = 0;
+            int taken = 0;
+            const uint64_t* mine = a.keys + (row * a.lists + lane) * a.beams;
+            if (lane < a.lists) {
+                s = a.soft[row * a.lists + lane];
+                head = mine[0];
+            }
+            s = soft_wave(s, 1.44269504088896340736f);
+            m = s.m;
+            log_s = log(static_cast<double>(s.s));
+            if (!(log_s == log_s)) head = 0;                // a NaN or +inf in the row
+            for (int r = 0; r < a.beams; ++r) {
+                const uint64_t top = wave_max64(head);
+                if (top == 0) break;
+                if (lane == r) out = top;
+                if (head == top) head = ++taken < a.beams ? mine[taken] : 0;
+            }
+        }
+        if (lane < a.beams) best[b][lane] = out;
+        if (lane == 0) {
+            score_of[b] = score;
+            log_sum[b] = log_s;
+            max_of[b] = m;
+            done[b] = fin;
+            if (a.history) {
+                last[b][0] = a.history[2 * row + 1];
+                last[b][1] = a.tokens[row];
+            }
+        }
+    }
+    __syncthreads();
+    if (wave != 0) return;
+    int taken = 0;
+    double mine = 0;
+    uint64_t head = lane < a.beams ? best[lane][0] : 0;
+    const auto value = [&](uint64_t k) { return score_of[lane] + ((key_logit(k) - max_of[lane]) - log_sum[lane]); };
+    if (head) mine = value(head);
+    for (int r = 0; r < a.beams; ++r) {
+        // the largest score, ties to the lowest beam
+        double top = head ? mine : -__builtin_inf();
+        int who = head && mine > -__builtin_inf() ? lane : 64;
+#pragma unroll
+        for (int step = 1; step < 64; step *= 2) {
+            const double other = __shfl_xor(top, step);
+            const int ow = __shfl_xor(who, step);
+            if (other > top || (other == top && ow < who)) {
+                top = other;
+                who = ow;
+            }
+        }
+        const int64_t to = row0 + r;
+        if (who == 64) {
+            if (lane == 0) {
+                a.scores_out[to] = kNegInf;
+                if (a.tokens_out) a.tokens_out[to] = -1;
+                a.parents_out[to] = -1;
+                if (a.finished_out) a.finished_out[to] = 0;
+                if (a.history_out) {
+                    a.history_out[2 * to] = -1;
+                    a.history_out[2 * to + 1] = -1;
+                }
+            }
+            continue;
+        }
+        if (lane == who) {
+            const int token = key_token(head);
+            a.scores_out[to] = static_cast<float>(mine);
+            if (a.tokens_out) a.tokens_out[to] = token;
+            a.parents_out[to] = lane;
+            if (a.finished_out) a.finished_out[to] = done[lane] || token == a.end;
+            if (a.history_out) {
+                a.history_out[2 * to] = last[lane][0];
+                a.history_out[2 * to + 1] = last[lane][1];
+            }
+            head = ++taken < a.beams ? best[lane][taken] : 0;
+            if (head) mine = value(head);
+        }
+    }
+}
+
+// Workgroups a row: enough rows fill the card with one each; few rows are cut,
+// to 16 parts at most (64 lists, one a lane of the join) of 4096 elements and more.
+int chunks_of(int64_t rows, int64_t v) {
+    const int64_t want = (1024 + rows - 1) / std::max<int64_t>(rows, 1);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, 16, (v + 4095) / 4096})));
+}
+
+bool step_sizes_ok(int64_t batch, int32_t beams, int64_t v, int32_t dtype) {
+    return batch >= 0 && batch <= NGRAM_FP8_MAX && beams >= 1 && beams <= NGRAM_MAX_BEAMS && v >= 1 && v < NGRAM_PAD_ID &&
+           (dtype == NGRAM_F32 || dtype == NGRAM_BF16);
+}
+int64_t step_bytes(int64_t rows, int lists, int beams) { return rows * lists * (8 * static_cast<int64_t>(beams) + sizeof(Soft)); }
+
+// ---------------------------------------------------------------------------
+// Reordering.  A thread owns one column of 16, 4 or 1 bytes of a sequence's
+// rows: it reads what every row that changes takes, then writes those
+// rows, so nothing is read after it was overwritten and rows that stay move
+// no bytes.
+constexpr int kStates = 64;
+
+struct ReorderArgs {
+    const int32_t* parents;
+    int32_t beams;
+    int32_t count;
+    int64_t first;                      // the launch's first workgroup
+    int64_t start[kStates + 1];         // the first workgroup of each state
+    ngram_beam_state state[kStates];
+};
+
+template <int B, typename T>
+__device__ __forceinline__ void reorder_columns(const ReorderArgs& a, char* base, int64_t stride, int64_t columns, int64_t col, const int* parent) {
+    if (col >= columns) return;
+    char* const p = base + col * static_cast<int64_t>(sizeof(T));
+    T v[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+        if (parent[b] >= 0) v[b] = *reinterpret_cast<const T*>(p + parent[b] * stride);
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+        if (parent[b] >= 0) *reinterpret_cast<T*>(p + b * stride) = v[b];
+}
+
+inline __host__ __device__ int unit_of(const ngram_beam_state& s) {
+    const uint64_t u = reinterpret_cast<uint64_t>(s.data) | static_cast<uint64_t>(s.row_bytes) | static_cast<uint64_t>(s.stride);
+    return u % 16 == 0 ? 16 : u % 4 == 0 ? 4 : 1;
+}
+
+template <int B>
+__global__ void __launch_bounds__(256) beam_reorder_kernel(const ReorderArgs a) {
+    const int64_t wg = a.first + blockIdx.x;
+    int s = 0;
+    while (s + 1 < a.count && wg >= a.start[s + 1]) ++s;
+    const ngram_beam_state st = a.state[s];
+    const int unit = unit_of(st);
+    const int64_t columns = st.row_bytes / unit, blocks = (columns + 255) / 256;
+    const int64_t at = wg - a.start[s], seq = at / blocks, col = at % blocks * 256 + threadIdx.x;
+    // the parent of each row that changes, or -1
+    int parent[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        parent[b] = -1;
+        if (b < a.beams) {
+            const int p = a.parents[seq * a.beams + b];
+            if (p >= 0 && p < a.beams && p != b) parent[b] = p;
+        }
+    }
+    char* const base = static_cast<char*>(st.data) + seq * a.beams * st.stride;
+    if (unit == 16) reorder_columns<B, u32x4>(a, base, st.stride, columns, col, parent);
+    else if (unit == 4) reorder_columns<B, uint32_t>(a, base, st.stride, columns, col, parent);
+    else reorder_columns<B, uint8_t>(a, base, st.stride, columns, col, parent);
+}
+
+}  // namespace
+}  // namespace ng8
+
+using namespace ng8;
+
+extern "C" {
+
+int64_t ngram_beam_step_workspace_bytes(int64_t batch, int32_t beams, int64_t V, int32_t dtype) {
+    if (!step_sizes_ok(batch, beams, V, dtype)) return -1;
+    return step_bytes(batch * beams, kScanWaves * chunks_of(batch * beams, V), beams);
+}
+
+int ngram_beam_step(const void* logits, int32_t dtype, int64_t batch, int32_t beams, int64_t V, int64_t ld,
+                    const float* scores, const int32_t* tokens, const int32_t* history, const uint8_t* finished,
+                    int32_t end_token, float* scores_out, int32_t* tokens_out, int32_t* parents_out,
+                    int32_t* history_out, uint8_t* finished_out, void* workspace, int64_t workspace_bytes,
+                    ngram_stream_t stream) {
+    fail(NGRAM_OK, "%s", "");
+    if (batch < 0) return fail(NGRAM_EINVAL, "batch=%lld is negative", (long long)batch);
+    if (dtype != NGRAM_F32 && dtype != NGRAM_BF16) return fail(NGRAM_EINVAL, "dtype=%d is not an ngram_value", dtype);
+    if (!step_sizes_ok(batch, beams, V, dtype))
+        return fail(NGRAM_ERANGE, "batch=%lld, beams=%d (1 to %d) or V=%lld (1 to %d) out of range", (long long)batch, beams, NGRAM_MAX_BEAMS,
+                    (long long)V, NGRAM_PAD_ID - 1);
+    if (ld < V) return fail(NGRAM_EINVAL, "ld=%lld is below V=%lld", (long long)ld, (long long)V);
+    if (end_token < -1 || end_token >= V) return fail(NGRAM_EINVAL, "end_token=%d is neither -1 nor a token", end_token);
+    if (finished && end_token < 0) return fail(NGRAM_EINVAL, "finished beams need an end_token");
+    if ((history != nullptr) != (history_out != nullptr) || (history && !tokens))
+        return fail(NGRAM_EINVAL, "history, tokens and history_out go together");
+    if (batch == 0) return NGRAM_OK;
+    if (!logits || !scores || !scores_out || !parents_out) return fail(NGRAM_EINVAL, "logits, scores, scores_out or parents_out is NULL");
+    if (!aligned(logits, dtype == NGRAM_F32 ? 4 : 2) || !aligned(scores, 4) || !aligned(tokens, 4) || !aligned(history, 4) ||
+        !aligned(scores_out, 4) || !aligned(tokens_out, 4) || !aligned(parents_out, 4) || !aligned(history_out, 4))
+        return fail(NGRAM_EALIGN, "an argument is not aligned to its elements");
+    StepArgs a = {};
+    const int64_t rows = batch * beams;
+    a.logits = logits; a.scores = scores; a.tokens = tokens; a.history = history; a.finished = finished;
+    a.scores_out = scores_out; a.tokens_out = tokens_out; a.parents_out = parents_out; a.history_out = history_out; a.finished_out = finished_out;
+    a.ld = ld; a.v = static_cast<int32_t>(V); a.beams = beams; a.end = end_token;
+    a.chunks = chunks_of(rows, V); a.lists = kScanWaves * a.chunks;
+    const int64_t need = step_bytes(rows, a.lists, beams);
+    if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
+        return fail(NGRAM_EINVAL, "workspace must hold %lld bytes, 16-byte aligned", (long long)need);
+    a.keys = static_cast<uint64_t*>(workspace);
+    a.soft = reinterpret_cast<Soft*>(a.keys + rows * a.lists * beams);
+    const int64_t most = most_groups(64 * kScanWaves) / a.chunks;
+    for (a.first = 0; a.first < rows; a.first += most) {
+        const dim3 grid(static_cast<uint32_t>(std::min(most, rows - a.first) * a.chunks));
+        if (dtype == NGRAM_F32) hipLaunchKernelGGL(beam_scan_kernel<true>, grid, dim3(64 * kScanWaves), 0, stream, a);
+        else hipLaunchKernelGGL(beam_scan_kernel<false>, grid, dim3(64 * kScanWaves), 0, stream, a);
+    }
+    for (a.first = 0; a.first < batch; a.first += most_groups(64 * kJoinWaves))
+        hipLaunchKernelGGL(beam_join_kernel, dim3(static_cast<uint32_t>(std::min(most_groups(64 * kJoinWaves), batch - a.first))),
+                           dim3(64 * kJoinWaves), 0, stream, a);
+    return hip_status("ngram_beam_step");
+}
+
+int ngram_beam_reorder(const ngram_beam_state* states, int32_t count, const int32_t* parents, int64_t batch, int32_t beams,
+                       ngram_stream_t stream) {
+    fail(NGRAM_OK, "%s", "");
+    if (count < 0 || batch < 0) return fail(NGRAM_EINVAL, "count=%d or batch=%lld is negative", count, (long long)batch);
+    if (beams < 1 || beams > NGRAM_MAX_BEAMS || batch > NGRAM_FP8_MAX)
+        return fail(NGRAM_ERANGE, "beams=%d (1 to %d) or batch=%lld out of range", beams, NGRAM_MAX_BEAMS, (long long)batch);
+    if (count > 0 && !states) return fail(NGRAM_EINVAL, "states is NULL");
+    for (int i = 0; i < count; ++i) {
+        const ngram_beam_state& s = states[i];
+        if (s.row_bytes < 0 || s.stride < s.row_bytes)
+            return fail(NGRAM_EINVAL, "state %d: row_bytes=%lld must not be negative nor above stride=%lld", i, (long long)s.row_bytes, (long long)s.stride);
+        if (s.row_bytes > (INT64_C(1) << 40)) return fail(NGRAM_ERANGE, "state %d: row_bytes=%lld above 2^40", i, (long long)s.row_bytes);
+        if (s.row_bytes > 0 && batch > 0 && !s.data) return fail(NGRAM_EINVAL, "state %d: data is NULL", i);
+    }
+    if (batch == 0 || count == 0) return NGRAM_OK;
+    if (!parents) return fail(NGRAM_EINVAL, "parents is NULL");
+    if (!aligned(parents, 4)) return fail(NGRAM_EALIGN, "parents must be 4-byte aligned");
+    for (int at = 0; at < count; at += kStates) {
+        ReorderArgs a = {};
+        a.parents = parents;
+        a.beams = beams;
+        int64_t total = 0;
+        for (int i = at; i < std::min(count, at + kStates); ++i) {
+            if (states[i].row_bytes == 0) continue;
+            const int64_t blocks = (states[i].row_bytes / unit_of(states[i]) + 255) / 256;
+            a.start[a.count] = total;
+            a.state[a.count++] = states[i];
+            total += batch * blocks;
+        }
+        a.start[a.count] = total;
+        for (a.first = 0; a.first < total; a.first += most_groups(256)) {
+            const dim3 grid(static_cast<uint32_t>(std::min(most_groups(256), total - a.first))), block(256);
+            if (beams <= 4) hipLaunchKernelGGL(beam_reorder_kernel<4>, grid, block, 0, stream, a);
+            else if (beams <= 8) hipLaunchKernelGGL(beam_reorder_kernel<8>, grid, block, 0, stream, a);
+            else if (beams <= 16) hipLaunchKernelGGL(beam_reorder_kernel<16>, grid, block, 0, stream, a);
+            else hipLaunchKernelGGL(beam_reorder_kernel<32>, grid, block, 0, stream, a);
+        }
+    }
+    return hip_status("ngram_beam_reorder");
+}
+
+}  // extern "C"

@@ -572,6 +572,166 @@ int ngram_adamw(const ngram_adamw_tensor* tensors, int32_t count, const ngram_ad
 int ngram_adamw_rows(const ngram_adamw_tensor* table, int64_t R, int32_t d, const int32_t* rows, int64_t max_rows,
                      const int64_t* n_rows, const ngram_adamw_step* step, ngram_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The vocabulary's side of a model: the product with its weights in 4 bits,
+ * the choice of the next tokens, and the loss of a student against a teacher.
+ * The pages name none of these; the formulas are fixed here.  With
+ * ngram_forward they close a decoding loop (tokens and history in, logits, the
+ * next tokens and history out) and a training step.
+ *
+ * 4-bit matrices.  w[o][j] = scale[o][j / group] * (q[o][j] - zero[o][j / group]),
+ * q and zero whole numbers from 0 to 15 (zero 8 where `zeros` is NULL), group
+ * 32, 64 or 128 columns.
+ *   codes  [rows][16 ceil(cols / 32)] bytes, column 2m in the low nibble of
+ *     byte m (as in an MXFP4 table), 16-byte aligned;
+ *   scales [rows][4 ceil(groups / 4)] fp32 or bf16 (ngram_value), 16-byte
+ *     aligned, groups = ceil(cols / group);
+ *   zeros  the same shape in bytes, 4-byte aligned, or NULL.
+ * What lies past cols and past groups does not count.  cols a multiple of 8.
+ * ngram_int4_code_bytes and ngram_int4_scales give the sizes (bytes, and
+ * elements of scales and of zeros; -1 for sizes out of range). */
+#define NGRAM_INT4_MAX_ROWS 16777216    /* 2^24 */
+#define NGRAM_INT4_MAX_COLS 1048576     /* 2^20 */
+
+typedef struct {
+    uint8_t* codes;
+    void* scales;
+    uint8_t* zeros;
+    int64_t rows;
+    int64_t cols;
+    int32_t group;
+    int32_t scale_dtype;   /* ngram_value */
+} ngram_int4;
+
+int64_t ngram_int4_code_bytes(int64_t rows, int64_t cols);
+int64_t ngram_int4_scales(int64_t rows, int64_t cols, int32_t group);
+
+/* Round x[n][d] (fp32 or bf16, 16-byte aligned) to the format, group by group,
+ * in fp32 with correctly rounded divisions:
+ *   with zeros: lo = min(0, x), hi = max(0, x), scale = (hi - lo) / 15,
+ *     zero = rint(-lo / scale) within 0 .. 15, q = rint(x / scale) + zero within 0 .. 15;
+ *   without:    scale = max |x| / 7, q = rint(x / scale) + 8 within 0 .. 15;
+ * scale is rounded to its type before it divides, and 1 where that is 0.  rint
+ * takes ties to even.  A group with an infinity or a NaN, or whose scale would
+ * not be finite, becomes NaN (scale NaN, codes and zero 8).  The scales (1) and
+ * zeros (8) past the last group are written too. */
+int ngram_quant_int4(const void* x, int32_t x_dtype, int64_t n, int32_t d, const ngram_int4* q, ngram_stream_t stream);
+
+/* The values that q stands for, y[rows][cols] fp32 or bf16 (rounded once from
+ * the fp32 product), 16-byte aligned. */
+int ngram_dequant_int4(const ngram_int4* q, void* y, int32_t y_dtype, ngram_stream_t stream);
+
+/* y[i][o] = sum over j of x[i][j] w[o][j] for x[n][W.cols] fp32 or bf16, y
+ * [n][W.rows] fp32 or bf16 (rounded once from fp32), both 16-byte aligned: the
+ * layer's product where rows are few and the weights' bytes count (a decoding
+ * batch; rows in any number are taken).  Every product is exact and sums are
+ * fp32, in an order that is fixed for given sizes and types, on x times 16 + q
+ * with 16 + zero times the group's sum of x taken off: y can differ from
+ * another fp32 evaluation by about 2^-24 sum over groups of scale sum |x| (32 +
+ * group / 8).  A row of x that holds an infinity or a NaN, or values above 2^115,
+ * gives NaN or infinities; other rows are not touched by it.  n = 0 launches nothing. */
+int ngram_project_int4(const void* x, int32_t x_dtype, int64_t n, const ngram_int4* W, void* y, int32_t y_dtype,
+                       ngram_stream_t stream);
+
+/* One step of beam search.  Each of `batch` sequences has `beams` beams, row
+ * b of sequence e at e beams + b.  From logits[rows][V] (fp32 or bf16, any
+ * distance `ld` >= V elements between rows, element-aligned) and the beams'
+ * scores (log probabilities):
+ *   candidate (b, t): scores[b] + logits[b][t] - log sum over u of exp(logits[b][u]);
+ *   a finished beam has one candidate: (b, end_token), with its score.
+ * The `beams` largest candidates of a sequence become its beams, the largest
+ * first, ties to the lowest b V + t (two candidates of one beam compare by
+ * their logits, others by scores held in float64).  A candidate of -inf or NaN is
+ * none: logits of -inf are masked tokens, a row that is masked throughout or
+ * that holds a NaN or +inf has no candidates, and neither has a beam whose score
+ * is -inf or NaN (a search starts with one beam at 0 and the others at -inf).  Places
+ * that no candidate fills get score -inf, token, parent and history -1 (which the lookup
+ * takes as invalid), not finished.
+ * Per new beam: scores_out; tokens_out (int32, may be NULL) its token; parents_out its parent's
+ * b; finished_out (bytes 0 or 1) whether its parent was or its token is
+ * end_token; history_out[rows][2] the two tokens before its token, for
+ * ngram_forward's history: (history[parent][1], tokens[parent]), tokens being
+ * those fed at this step.  history, tokens and history_out are NULL together;
+ * finished and finished_out may be NULL (none is; not asked for).  Each
+ * output may be the memory of the input of its name.  end_token: -1 for none
+ * (then finished must be NULL).  1 <= beams <= NGRAM_MAX_BEAMS, 1 <= V <
+ * NGRAM_PAD_ID.  workspace: device, 16-byte aligned, ngram_beam_step_workspace_bytes
+ * bytes; calls that can overlap need one each. */
+#define NGRAM_MAX_BEAMS 32
+
+int64_t ngram_beam_step_workspace_bytes(int64_t batch, int32_t beams, int64_t V, int32_t dtype);
+int ngram_beam_step(const void* logits, int32_t dtype, int64_t batch, int32_t beams, int64_t V, int64_t ld,
+                    const float* scores, const int32_t* tokens, const int32_t* history, const uint8_t* finished,
+                    int32_t end_token, float* scores_out, int32_t* tokens_out, int32_t* parents_out,
+                    int32_t* history_out, uint8_t* finished_out, void* workspace, int64_t workspace_bytes,
+                    ngram_stream_t stream);
+
+/* What the beams carry follows them: for every state, sequence and beam, row
+ * e beams + b takes what row e beams + parents[e beams + b] held, in place; a
+ * parent outside [0, beams) leaves its row as it is.  A state is batch * beams
+ * rows of row_bytes bytes, `stride` >= row_bytes bytes apart, at any address;
+ * rows whose address, size and distance are multiples of 16 bytes move fastest.  The states
+ * (a HOST array, read before the call returns) must not overlap.  One launch for up to
+ * 64 states. */
+typedef struct {
+    void* data;
+    int64_t row_bytes;
+    int64_t stride;
+} ngram_beam_state;
+
+int ngram_beam_reorder(const ngram_beam_state* states, int32_t count, const int32_t* parents, int64_t batch,
+                       int32_t beams, ngram_stream_t stream);
+
+/* Distillation from a teacher's top logits.  Per row i, at temperature T, for
+ * the student's logits z[V] and the teacher's logits t[k] at tokens ids[k] (an
+ * id outside [0, V) is an empty place; k <= NGRAM_DISTILL_MAX_K):
+ *   q = softmax(z / T) over V;
+ *   p = softmax(t / T) over the places that are not empty, or, with
+ *     teacher_lse[i] = log sum exp(t / T) over the teacher's whole vocabulary,
+ *     p[j] = exp(t[j] / T - teacher_lse[i]), and the rest P = max(0, 1 - sum p) is the
+ *     teacher's mass off the list, Q the student's;
+ *   loss = T^2 (sum over j of p[j] log(p[j] / q[ids[j]])  (+ P log(P / Q), where P > 0));
+ *   dloss/dz[v] = T (a[v] q[v] - sum over j with ids[j] = v of p[j]), a[v] = sum of
+ *     p, or with the rest 1 on the list and 1 - P / Q off it (1 where P or Q is 0).
+ * With k = 1 and no teacher_lse this is the cross entropy of token ids[0].  A
+ * place with p = 0 adds nothing.  A row whose places are all empty (or all
+ * -inf) has loss and gradient 0, with teacher_lse too where no place is
+ * listed (P = Q = 1).  A token may be listed twice: its places add up.  A
+ * student that gives a token of p > 0 no chance has an infinite loss; a row of z that
+ * is -inf throughout, or holds a NaN or +inf, gives NaN.
+ * Roundings: exp and sums in fp32, sums of a fixed order; the teacher's side and
+ * the loss in float64, rounded once.
+ * Per row: loss_out; stats_out[n][3]: the largest logit m, log sum exp((z - m) / T),
+ * and log Q (0 without teacher_lse), which ngram_distill_grad reads; each fp32, 4-byte aligned, NULL
+ * if not wanted.  dlogits_out[n][V] (z's type, distance dld, may be z itself):
+ * weight[i] * scale * dloss/dz (weight NULL: 1), for a loss that is the sum of
+ * weight[i] * scale * loss[i]; a row with weight * scale 0 gets zeros, whatever its logits hold.
+ * z: any distance ld >= V elements between rows, element-aligned; t [n][k]
+ * and z have types of their own; weight, teacher_lse [n] fp32.  T positive and
+ * finite.  workspace: device, 16-byte aligned, ngram_distill_workspace_bytes bytes (may be 0). */
+#define NGRAM_DISTILL_MAX_K 1024
+
+typedef struct {
+    const void* logits;
+    const void* teacher;
+    const int32_t* ids;
+    const float* teacher_lse;   /* or NULL */
+    int64_t n;
+    int64_t V;                  /* at most 2^30 */
+    int64_t ld;
+    int32_t k;
+    int32_t dtype;              /* of logits and dlogits: ngram_value */
+    int32_t teacher_dtype;
+    float temperature;
+} ngram_distill_args;
+
+int64_t ngram_distill_workspace_bytes(int64_t n, int64_t V, int32_t dtype);
+int ngram_distill(const ngram_distill_args* a, float* loss_out, float* stats_out, const float* weight, float scale,
+                  void* dlogits_out, int64_t dld, void* workspace, int64_t workspace_bytes, ngram_stream_t stream);
+/* The gradient from the forward's stats_out, for a backward of its own. */
+int ngram_distill_grad(const ngram_distill_args* a, const float* stats, const float* weight, float scale,
+                       void* dlogits_out, int64_t dld, ngram_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
