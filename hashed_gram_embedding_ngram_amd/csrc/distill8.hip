@@ -308,6 +308,202 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
     }
 }
 
+// Loss and gradient of a row in one pass over memory: the row's vectors stay in
+// registers (NV a thread) between the sums and the gradient; what goes beyond them is
+// read again.  The teacher's side is one wavefront's work while the row's loads
+// are on their way.
+constexpr int kRowMarks = 1 << 18;      // tokens of a row at most
+
+template <bool F32, bool REST, int NV>
+__global__ void __launch_bounds__(kThreads) distill_row_kernel(const DistillArgs a) {
+    constexpr int E = Row<F32>::E;
+    extern __shared__ uint32_t marks[];                 // (v + 31) / 32
+    __shared__ Soft joined[2][kWaves];
+    __shared__ int32_t id_of[kMaxK];
+    __shared__ float t_of[kMaxK], z_of[kMaxK], p_of[kMaxK];
+    __shared__ int twice;
+    __shared__ Teacher teacher;
+    __shared__ double mass_;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t row = a.first + blockIdx.x;
+    const Row<F32> r(a.z, row * a.ld, a.v), w(a.dz, row * a.dld, a.v);
+    const float gs = (a.weight ? a.weight[row] : 1.0f) * a.scale;
+    const int whole = static_cast<int>(a.v) / E, all_vectors = r.vectors();
+    u32x4 raw[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = tid + j * kThreads;
+        if (i < whole) raw[j] = *reinterpret_cast<const Loose*>(r.base + static_cast<int64_t>(i) * 16);
+    }
+    for (int i = tid; i < (static_cast<int>(a.v) + 31) / 32; i += kThreads) marks[i] = 0;
+    if (tid == 0) twice = 0;
+    for (int j = tid; j < a.k; j += kThreads) {
+        const int id = a.ids[row * a.k + j];
+        const bool on = id >= 0 && id < a.v;
+        id_of[j] = on ? id : -1;
+        t_of[j] = teacher_at(a, row * a.k + j);
+        z_of[j] = on ? r.element(id) : 0.0f;
+    }
+    __syncthreads();
+    for (int j = tid; j < a.k; j += kThreads) {
+        const int id = id_of[j];
+        if (id < 0) continue;
+        const uint32_t mask = 1u << (id & 31);
+        if (atomicOr(&marks[id >> 5], mask) & mask) twice = 1;
+    }
+    if (REST) __syncthreads();
+    if (wave == 0) {
+        Teacher t{0, 0};
+        if (a.teacher_lse) {
+            t.log_sum = a.teacher_lse[row];
+        } else {
+            float m = kNegInf;
+            for (int j = lane; j < a.k; j += 64)
+                if (id_of[j] >= 0) m = t_of[j] == t_of[j] && m == m ? fmaxf(m, t_of[j]) : __builtin_nanf("");
+            const float top = wave_max(m);
+            const bool nan = __ballot(m != m) != 0;
+            double s = 0;
+            for (int j = lane; j < a.k; j += 64)
+                if (id_of[j] >= 0) s += exp((static_cast<double>(t_of[j]) - top) * a.inv_t);
+            s = wave_sum_f64(s);
+            if (nan) t.log_sum = __builtin_nan("");
+            else if (top == kNegInf) t.log_sum = __builtin_inf();
+            else t = {top, log(s)};
+        }
+        double mass = 0;
+        for (int j = lane; j < a.k; j += 64) {
+            const double p = id_of[j] >= 0 ? exp((t_of[j] - t.m) * a.inv_t - t.log_sum) : 0;
+            mass += p;
+            p_of[j] = static_cast<float>(p);
+        }
+        mass = wave_sum_f64(mass);
+        if (lane == 0) {
+            teacher = t;
+            mass_ = mass;
+        }
+    }
+    Soft all{kLowest, 0.0f};
+    float off = 0.0f;
+    const auto add = [&](const u32x4& v, int i) {
+        float x[E];
+        float top = kNegInf;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            x[k] = Row<F32>::at(v, k);
+            top = fmaxf(top, x[k]);
+        }
+        const float m = fmaxf(all.m, top);
+        const float f = exp2_fast((all.m - m) * a.c);
+        all.s *= f;
+        off *= f;
+        all.m = m;
+        const uint32_t listed = REST ? marks[(i * E) >> 5] >> ((i * E) & 31) : 0;
+#pragma unroll
+        for (int k = 0; k < E; ++k) {
+            const float e = exp2_fast((x[k] - m) * a.c);
+            all.s += e;
+            if (REST) off += listed & (1u << k) ? 0.0f : e;
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (tid + j * kThreads < whole) add(raw[j], tid + j * kThreads);
+    for (int i = tid + NV * kThreads; i < whole; i += kThreads) add(r.load(i), i);
+    if (whole < all_vectors && tid == kThreads - 1) add(r.load(whole), whole);
+    {
+        const float m = wave_max(all.m), f = exp2_fast((all.m - m) * a.c);
+        all.s = wave_sum(all.s * f);
+        if (REST) off = wave_sum(off * f);
+        if (lane == 0) {
+            joined[0][wave] = {m, all.s};
+            joined[1][wave] = {m, off};
+        }
+    }
+    __syncthreads();
+    Soft o = joined[1][0];
+    all = joined[0][0];
+#pragma unroll
+    for (int h = 1; h < kWaves; ++h) {
+        all = soft_join(all, joined[0][h], a.c);
+        if (REST) o = soft_join(o, joined[1][h], a.c);
+    }
+    if (wave == 0) {
+        const double log_s = log(static_cast<double>(all.s));
+        double sum = 0, log_rest = 0;
+        for (int j = lane; j < a.k; j += 64) {
+            if (id_of[j] < 0) continue;
+            const double log_p = (t_of[j] - teacher.m) * a.inv_t - teacher.log_sum, p = exp(log_p);
+            if (!(p == 0)) sum += p * (log_p - ((static_cast<double>(z_of[j]) - all.m) * a.inv_t - log_s));
+        }
+        sum = wave_sum_f64(sum);
+        if (REST) {
+            const double rest = 1 - mass_;
+            log_rest = (static_cast<double>(o.m) - all.m) * a.inv_t + log(static_cast<double>(o.s)) - log_s;
+            if (!(rest <= 0)) sum += rest * (log(rest) - log_rest);
+        }
+        if (lane == 0) {
+            if (a.loss) a.loss[row] = static_cast<float>(log_s - log_s == 0 ? sum * a.t2 : __builtin_nan(""));
+            a.stats[3 * row] = all.s == 0.0f ? kNegInf : all.m;
+            a.stats[3 * row + 1] = static_cast<float>(log_s);
+            a.stats[3 * row + 2] = static_cast<float>(log_rest);
+        }
+    }
+    float on_f = static_cast<float>(mass_), off_f = on_f;
+    if (REST) {
+        on_f = 1.0f;
+        const float rest = static_cast<float>(1 - mass_);
+        off_f = rest > 0.0f && o.s > 0.0f ? 1.0f - rest * (all.s / o.s) * exp2_fast((all.m - o.m) * a.c) : 1.0f;
+    }
+    const float L = __builtin_amdgcn_logf(all.s), m = all.m, gq = gs * off_f;
+    const auto q_of = [&](float x) { return exp2_fast(__builtin_fmaf(x - m, a.c, -L)); };
+    const auto grad = [&](const u32x4& v) {
+        u32x4 out;
+#pragma unroll
+        for (int k = 0; k < E; k += 2) {
+            const float g0 = q_of(Row<F32>::at(v, k)) * gq, g1 = q_of(Row<F32>::at(v, k + 1)) * gq;
+            if (F32) {
+                out[k & 3] = __float_as_uint(g0);
+                out[(k + 1) & 3] = __float_as_uint(g1);
+            } else {
+                out[(k >> 1) & 3] = bf16_pair(g0, g1);
+            }
+        }
+        return gs == 0.0f ? u32x4{0, 0, 0, 0} : out;
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = tid + j * kThreads;
+        if (i < whole) *reinterpret_cast<Loose*>(w.base + static_cast<int64_t>(i) * 16) = grad(raw[j]);
+    }
+    for (int i = tid + NV * kThreads; i < whole; i += kThreads) w.store(i, grad(r.load(i)));
+    if (whole < all_vectors && tid == kThreads - 1) w.store(whole, grad(r.load(whole)));
+    if (gs == 0.0f) return;
+    // what was stored above has arrived before it is written over
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    for (int j = tid; j < a.k; j += kThreads) {
+        const int id = id_of[j];
+        if (id < 0) continue;
+        float p = p_of[j];
+        bool first = true;
+        if (twice) {
+            double sum = 0;
+            for (int e = 0; e < a.k; ++e) {
+                if (id_of[e] != id) continue;
+                if (e < j) first = false;
+                sum += p_of[e];
+            }
+            p = static_cast<float>(sum);
+        }
+        if (!first) continue;
+        const float g = (q_of(z_of[j]) * on_f - p) * gs;
+        char* const at = w.base + static_cast<int64_t>(id) * (F32 ? 4 : 2);
+        if (F32) *reinterpret_cast<float*>(at) = g;
+        else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(bf16_pair(g, g));
+    }
+}
+
 // Workgroups a row: one where rows fill the card; few rows are cut into parts
 // of 512 vectors and more.
 int chunks_of(int64_t n, int64_t v, int dtype) {
@@ -375,6 +571,25 @@ void launch_grad(const DistillArgs& a, bool f32, hipStream_t st) {
     });
 }
 
+// Rows in one workgroup each: enough of them to fill the card, short enough for the marks.
+bool whole_rows(const DistillArgs& a) { return a.n >= 256 && a.v <= kRowMarks; }
+
+template <bool F32, bool REST, int NV>
+void launch_rows_of(const DistillArgs& a, hipStream_t st) {
+    const uint32_t lds = static_cast<uint32_t>((a.v + 31) / 32 * 4);
+    over_rows(a, a.n, 1, kThreads, 1, [&](const DistillArgs& b, dim3 grid) {
+        hipLaunchKernelGGL((distill_row_kernel<F32, REST, NV>), grid, dim3(kThreads), lds, st, b);
+    });
+}
+template <bool F32, bool REST>
+void launch_rows(const DistillArgs& a, hipStream_t st) {
+    const int64_t vectors = a.v / Row<F32>::E;
+    if (vectors <= 4 * kThreads) launch_rows_of<F32, REST, 4>(a, st);
+    else if (vectors <= 12 * kThreads) launch_rows_of<F32, REST, 12>(a, st);
+    else if (vectors <= 24 * kThreads) launch_rows_of<F32, REST, 24>(a, st);
+    else launch_rows_of<F32, REST, 38>(a, st);
+}
+
 }  // namespace
 }  // namespace ng8
 
@@ -405,6 +620,13 @@ int ngram_distill(const ngram_distill_args* p, float* loss_out, float* stats_out
     a.stats = stats_out ? stats_out : reinterpret_cast<float*>(static_cast<char*>(workspace) + parts);
     a.weight = weight; a.scale = static_cast<float>(static_cast<double>(scale) * p->temperature); a.dz = dlogits_out; a.dld = dld;
     const bool f32 = p->dtype == NGRAM_F32;
+    if (dlogits_out && whole_rows(a)) {
+        if (f32 && a.teacher_lse) launch_rows<true, true>(a, stream);
+        else if (f32) launch_rows<true, false>(a, stream);
+        else if (a.teacher_lse) launch_rows<false, true>(a, stream);
+        else launch_rows<false, false>(a, stream);
+        return hip_status("ngram_distill");
+    }
     over_rows(a, a.n, a.chunks, kThreads, 1, [&](const DistillArgs& b, dim3 grid) {
         const dim3 block(kThreads);
         if (f32 && b.teacher_lse) hipLaunchKernelGGL((distill_stats_kernel<true, true>), grid, block, 0, stream, b);

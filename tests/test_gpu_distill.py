@@ -264,3 +264,35 @@ def test_in_a_graph_and_on_another_stream():
     torch.cuda.current_stream().wait_stream(side)
     for x, y in zip(eager, other):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("dtype,V", [(BF, 30001), (BF, 50257), (BF, 99999), (BF, 151936), (BF, 170001), (F32, 8192), (F32, 24577), (F32, 90002)])
+def test_batches_that_fill_the_card(dtype, V, rest):
+    """Rows kept in registers, in every size of them and beyond; some rows against float64, all of them against the calls apart."""
+    say(f"distill full batch {V} {dtype} rest={rest}")
+    n, k = 260, 70
+    some = [0, 1, 100, 130, 257, 258, 259]
+    rng = np.random.default_rng(V)
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z = (torch.randn((n, V), generator=g, device=DEV) * 2).to(dtype)
+    a = inputs(rng, len(some), V, k, dtype, F32, rest, 2.0)
+    z[some] = dev(a["z"], dtype)
+    t, ids = torch.randn((n, k), generator=g, device=DEV), torch.randint(0, V, (n, k), generator=g, device=DEV, dtype=torch.int32)
+    t[some], ids[some] = dev(a["t"]), dev(a["ids"])
+    lse = torch.logsumexp(t / 2, dim=1) + 0.5 if rest else None
+    weight = torch.rand(n, generator=g, device=DEV) + 0.5
+    weight[some] = dev(a["weight"])
+    if rest:
+        lse[some] = dev(a["lse"])
+    kw = dict(temperature=2.0, teacher_lse=lse)
+    one = ng.ngram_distill(z, t, ids, grad=True, weight=weight, scale=0.5, keep_stats=True, **kw)
+    check(a, dtype, one.loss[some], one.dlogits[some], one.stats[some], 0.5)
+    fwd = ng.ngram_distill(z, t, ids, keep_stats=True, **kw)
+    dz = ng.ngram_distill_grad(z, t, ids, fwd.stats, weight=weight, scale=0.5, **kw)
+    # both within the bounds of one result, which for these rows are below 2^-14 (fp32 sums of some hundred terms a lane) and a bf16 step
+    assert torch.allclose(one.loss, fwd.loss, rtol=0, atol=4 * 2 * 2.0 ** -14) and torch.allclose(one.stats, fwd.stats, rtol=2.0 ** -22, atol=2 * 2.0 ** -14)
+    # listed tokens' q and p may cancel: an absolute part of the rows' largest possible difference
+    assert torch.allclose(one.dlogits.float(), dz.float(), rtol=2.0 ** -7 if dtype == BF else 2.0 ** -12, atol=2.0 ** -12)
+    ng.ngram_distill(z, t, ids, weight=weight, scale=0.5, dlogits_out=z, **kw)
+    assert torch.equal(z, one.dlogits)
