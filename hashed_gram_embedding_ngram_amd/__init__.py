@@ -144,7 +144,7 @@ _SIGNATURES = {
     "ngram_beam_step_workspace_bytes": (ctypes.c_int64, [_I64, _I32, _I64, _I32]),
     "ngram_beam_step": (ctypes.c_int, [_P, _I32, _I64, _I32, _I64, _I64, _P, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _I64, _P]),
     "ngram_beam_reorder": (ctypes.c_int, [ctypes.POINTER(_BeamState), _I32, _P, _I64, _I32, _P]),
-    "ngram_distill_workspace_bytes": (ctypes.c_int64, [_I64, _I64, _I32]),
+    "ngram_distill_workspace_bytes": (ctypes.c_int64, [_I64, _I64, _I32, _I32]),
     "ngram_distill": (ctypes.c_int, [ctypes.POINTER(_DistillArgs), _P, _P, _P, ctypes.c_float, _P, _I64, _P, _I64, _P]),
     "ngram_distill_grad": (ctypes.c_int, [ctypes.POINTER(_DistillArgs), _P, _P, ctypes.c_float, _P, _I64, _P]),
 }
@@ -1227,11 +1227,11 @@ class DistillOut(NamedTuple):
     dlogits: Optional[torch.Tensor]
 
 
-def distill_workspace(n: int, V: int, dtype=torch.float32, device="cuda:0", stream=None):
+def distill_workspace(n: int, V: int, k: int, dtype=torch.float32, device="cuda:0", stream=None):
     """Workspace of ngram_distill, on ``stream`` (by default the current one)."""
-    nbytes = lib().ngram_distill_workspace_bytes(n, V, F32 if dtype is torch.float32 else BF16)
+    nbytes = lib().ngram_distill_workspace_bytes(n, V, k, F32 if dtype is torch.float32 else BF16)
     if nbytes < 0:
-        raise NgramError(f"no distillation has n={n}, V={V}")
+        raise NgramError(f"no distillation has n={n}, V={V}, k={k}")
     return _new(nbytes, None, torch.uint8, device, stream)
 
 
@@ -1271,7 +1271,7 @@ def ngram_distill(logits, teacher, ids, temperature: float = 1.0, teacher_lse=No
     if grad or dlogits_out is not None:
         dlogits_out, pd, dld = _dlogits(logits, n, V, dlogits_out, stream)
     if workspace is None:
-        workspace = distill_workspace(n, V, logits.dtype, dev, stream)
+        workspace = distill_workspace(n, V, a.k, logits.dtype, dev, stream)
     ws, ws_bytes = _scratch(workspace)
     rc = lib().ngram_distill(a, _arg(loss_out, _F32, n, "loss_out"), _opt(stats_out, _F32, 3 * n, "stats_out"),
                              _opt(weight, _F32, n, "weight"), scale, pd, dld, ws, ws_bytes, _raw_stream(stream))

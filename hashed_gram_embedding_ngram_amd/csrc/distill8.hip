@@ -13,6 +13,12 @@ constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kBitVectors = 16384;      // vectors of a chunk at most: 16 KB of marks
+constexpr int kScan = 128;              // places of a short list
+// Gradients above this size are stored past the caches' usual keeping (1021 x 32003 fp32, forward and
+// backward: 83 us against 97; 4096 x 151936 bf16 497 against 523); smaller ones are read next where they lie.
+constexpr int64_t kStreamFrom = int64_t{64} << 20;
+
+struct Sums;
 
 struct DistillArgs {
     const void* z;
@@ -23,8 +29,9 @@ struct DistillArgs {
     float* stats;           // written by the forward, read by the gradient
     const float* weight;
     void* dz;
-    Soft* part;             // [n][chunks][2]: the whole row's, and the unlisted tokens'
+    Sums* part;             // [n][chunks], or NULL: statistics are given
     int64_t n, v, ld, dld;
+    float* z_at;            // [n][k]: listed tokens' logits for a loss that is written beside the gradient, or NULL
     int64_t first;          // the launch's first row
     int32_t k, t32;
     int32_t chunks;         // workgroups a row
@@ -45,30 +52,178 @@ __device__ __forceinline__ double wave_sum_f64(double x) {
     return x;
 }
 
+// ---------------------------------------------------------------------------
+// Sums of exp.  With c = log2(e) / T a set of logits is (m, s): m its largest
+// and s the sum of 2^(x c - R), R = m c rounded to fp32.  One fused multiply-add and
+// one exp2 an element: R is a reference like any other, so its rounding costs nothing as long as
+// whoever uses s takes the same R, and x c - R is rounded once, relative to its own size.
+// Where x c leaves fp32's range (logits beyond 1e30, c beyond 1e7; a set of masked logits among
+// them), s is the sum of 2^((x - m) c) instead.
+constexpr float kFloor = -1e30f;        // m of the empty set
+
+struct Sums {
+    float m, s, off;                    // off: the unlisted tokens' part of s
+};
+
+__device__ __forceinline__ bool usual(float m, float c) { return fabsf(m) < 1e30f && c < 1e7f; }
+// What a sum at `from` is multiplied with to be one at `to`.
+__device__ __forceinline__ float rescale(float from, float to, float c) {
+    return usual(from, c) && usual(to, c) ? exp2_fast(from * c - to * c) : exp2_fast((from - to) * c);
+}
+__device__ __forceinline__ Sums join(const Sums& x, const Sums& y, float c) {
+    const float m = fmaxf(x.m, y.m), f = rescale(x.m, m, c), g = rescale(y.m, m, c);
+    return {m, x.s * f + y.s * g, x.off * f + y.off * g};
+}
+__device__ __forceinline__ Sums join_wave(const Sums& x, float c) {
+    const float m = wave_max(x.m), f = rescale(x.m, m, c);
+    return {m, wave_sum(x.s * f), wave_sum(x.off * f)};
+}
+// log of the sum of exp((x - m) / T)
+__device__ __forceinline__ double log_of(float s, float m, float c) {
+    const double l = log(static_cast<double>(s));
+    return usual(m, c) ? l + (static_cast<double>(m * c) - static_cast<double>(m) * c) * 0.69314718055994530942 : l;
+}
+
+// Adds the elements of G vectors; `listed` has a bit for each listed one.  USUAL:
+// x c - R, else (x - m) c.  One rescaling for all of them, and sums by pairs, so
+// that few of the instructions wait for each other.
+template <bool F32, bool REST, bool USUAL, int G>
+__device__ __forceinline__ void add_vectors(Sums& t, const u32x4 (&v)[G], const uint32_t (&listed)[G], float c) {
+    constexpr int E = Row<F32>::E;
+    float x[G * E];
+    float top = t.m;
+#pragma unroll
+    for (int k = 0; k < G * E; ++k) {
+        x[k] = Row<F32>::at(v[k / E], k % E);
+        top = fmaxf(top, x[k]);
+    }
+    const float R = top * c, f = USUAL ? exp2_fast(t.m * c - R) : exp2_fast((t.m - top) * c);
+    t.m = top;
+#pragma unroll
+    for (int k = 0; k < G * E; ++k) x[k] = USUAL ? exp2_fast(__builtin_fmaf(x[k], c, -R)) : exp2_fast((x[k] - top) * c);
+    if (REST) {
+        float y[G * E];
+#pragma unroll
+        for (int k = 0; k < G * E; ++k) y[k] = listed[k / E] & (1u << (k % E)) ? 0.0f : x[k];
+#pragma unroll
+        for (int n = G * E / 2; n > 0; n /= 2)
+#pragma unroll
+            for (int k = 0; k < n; ++k) y[k] += y[k + n];
+        t.off = __builtin_fmaf(t.off, f, y[0]);
+    }
+#pragma unroll
+    for (int n = G * E / 2; n > 0; n /= 2)
+#pragma unroll
+        for (int k = 0; k < n; ++k) x[k] += x[k + n];
+    t.s = __builtin_fmaf(t.s, f, x[0]);
+}
+template <bool F32, bool REST, bool USUAL>
+__device__ __forceinline__ void add_vector(Sums& t, const u32x4& v, uint32_t listed, float c) {
+    add_vectors<F32, REST, USUAL, 1>(t, {v}, {listed}, c);
+}
+
+// A workgroup's sums joined, in every thread.
+template <int WAVES>
+__device__ __forceinline__ Sums join_group(const Sums& x, Sums* room, int lane, int wave, float c) {
+    const Sums w = join_wave(x, c);
+    if (lane == 0) room[wave] = w;
+    __syncthreads();
+    Sums t = room[0];
+#pragma unroll
+    for (int h = 1; h < WAVES; ++h) t = join(t, room[h], c);
+    return t;
+}
+
+// This thread's vectors of from .. to - 1, kAhead loads at a time in flight;
+// the first are asked for before anything else is done.
+constexpr int kAhead = 4;
+template <bool F32, int THREADS = kThreads>
+struct Vectors {
+    const Row<F32>& r;
+    int i, to, whole;
+    u32x4 v[kAhead];
+    __device__ __forceinline__ Vectors(const Row<F32>& row, int from, int end)
+        : r(row), i(from + static_cast<int>(threadIdx.x)), to(end), whole(min(end, static_cast<int>(row.v / Row<F32>::E))) {
+        fetch(i);
+    }
+    __device__ __forceinline__ void fetch(int at) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (at + u * THREADS < whole) v[u] = r.load_whole(at + u * THREADS);
+    }
+    // f(vector, its number)
+    template <typename F>
+    __device__ __forceinline__ void each(F f) {
+        while (i < whole) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (i + u * THREADS < whole) f(v[u], i + u * THREADS);
+            i += kAhead * THREADS;
+            fetch(i);
+        }
+        if (whole < to && threadIdx.x == THREADS - 1) f(r.load(whole), whole);
+    }
+};
+
+// ---------------------------------------------------------------------------
 // The teacher of a row, by one wavefront: log p = (t - m) / T - log_sum.  m is
-// the largest listed logit (0 with a given log sum); log_sum +inf where nothing
-// is listed (every p is 0).
+// the largest listed logit (0 with a given log sum); log_sum is +inf where
+// nothing is listed, so that every p is 0.  t(j) and on(j): place j's logit, and
+// whether it names a token.
 struct Teacher {
     double m, log_sum;
-    __device__ __forceinline__ double log_p(const DistillArgs& a, int64_t i) const { return (teacher_at(a, i) - m) * a.inv_t - log_sum; }
+    __device__ __forceinline__ double log_p(double inv_t, float t) const { return (t - m) * inv_t - log_sum; }
 };
-__device__ Teacher teacher_of(const DistillArgs& a, int64_t row, int lane) {
+template <typename T, typename On>
+__device__ __forceinline__ Teacher teacher_of(const DistillArgs& a, int64_t row, int lane, T t, On on) {
     if (a.teacher_lse) return {0, a.teacher_lse[row]};
     float m = kNegInf;
-    for (int j = lane; j < a.k; j += 64) {
-        const int id = a.ids[row * a.k + j];
-        const float t = teacher_at(a, row * a.k + j);
-        if (id >= 0 && id < a.v) m = t == t && m == m ? fmaxf(m, t) : __builtin_nanf("");
-    }
+    for (int j = lane; j < a.k; j += 64)
+        if (on(j)) m = t(j) == t(j) && m == m ? fmaxf(m, t(j)) : __builtin_nanf("");
     const float top = wave_max(m);
     if (__ballot(m != m)) return {0, __builtin_nan("")};
     if (top == kNegInf) return {0, __builtin_inf()};
     double s = 0;
-    for (int j = lane; j < a.k; j += 64) {
-        const int id = a.ids[row * a.k + j];
-        if (id >= 0 && id < a.v) s += exp((static_cast<double>(teacher_at(a, row * a.k + j)) - top) * a.inv_t);
-    }
+    for (int j = lane; j < a.k; j += 64)
+        if (on(j)) s += exp((static_cast<double>(t(j)) - top) * a.inv_t);
     return {top, log(wave_sum_f64(s))};
+}
+
+// Loss and statistics of a row, by one wavefront.  z(j): the student's logit of place j.
+template <typename T, typename On, typename Z>
+__device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, const Sums& s, const Teacher& teacher, int lane, T t, On on, Z z) {
+    const double log_s = log_of(s.s, s.m, a.c);                 // log q = (z - m) / T - log_s
+    double sum = 0, mass = 0, log_rest = 0;
+    for (int j = lane; j < a.k; j += 64) {
+        if (!on(j)) continue;
+        const double log_p = teacher.log_p(a.inv_t, t(j)), p = exp(log_p);
+        mass += p;
+        if (!(p == 0)) sum += p * (log_p - ((static_cast<double>(z(j)) - s.m) * a.inv_t - log_s));
+    }
+    sum = wave_sum_f64(sum);
+    if (a.teacher_lse) {
+        const double rest = 1 - wave_sum_f64(mass);
+        log_rest = log(static_cast<double>(s.off)) - log(static_cast<double>(s.s));
+        if (!(rest <= 0)) sum += rest * (log(rest) - log_rest);
+    }
+    if (lane == 0) {
+        // a student that is not a distribution has no loss, also where nothing is listed
+        if (a.loss) a.loss[row] = static_cast<float>(log_s - log_s == 0 ? sum * a.t2 : __builtin_nan(""));
+        if (a.stats) {
+            a.stats[3 * row] = s.s == 0.0f ? kNegInf : s.m;
+            a.stats[3 * row + 1] = static_cast<float>(log_s);
+            a.stats[3 * row + 2] = static_cast<float>(log_rest);
+        }
+    }
+}
+template <bool F32>
+__device__ void write_loss_of(const DistillArgs& a, int64_t row, const Sums& s, int lane) {
+    const Row<F32> r(a.z, row * a.ld, a.v);
+    const int32_t* const ids = a.ids + row * a.k;
+    const auto t = [&](int j) { return teacher_at(a, row * a.k + j); };
+    const auto on = [&](int j) { return ids[j] >= 0 && ids[j] < a.v; };
+    const Teacher teacher = teacher_of(a, row, lane, t, on);
+    write_loss(a, row, s, teacher, lane, t, on, [&](int j) { return r.element(ids[j]); });
 }
 
 // Marks of the listed tokens among vectors from .. to - 1 of a row, E bits a
@@ -76,10 +231,10 @@ __device__ Teacher teacher_of(const DistillArgs& a, int64_t row, int lane) {
 template <int E>
 __device__ __forceinline__ void mark_listed(const DistillArgs& a, int64_t row, int from, int to, uint32_t* marks, int* twice) {
     const int words = (max(0, to - from) * E + 31) / 32;
-    for (int i = threadIdx.x; i < words; i += blockDim.x) marks[i] = 0;
+    for (int i = threadIdx.x; i < words; i += kThreads) marks[i] = 0;
     if (threadIdx.x == 0) *twice = 0;
     __syncthreads();
-    for (int j = threadIdx.x; j < a.k; j += blockDim.x) {
+    for (int j = threadIdx.x; j < a.k; j += kThreads) {
         const int id = a.ids[row * a.k + j];
         if (id >= 0 && id < a.v && id / E >= from && id / E < to) {
             const uint32_t bit = static_cast<uint32_t>(id - from * E), mask = 1u << (bit & 31);
@@ -88,13 +243,14 @@ __device__ __forceinline__ void mark_listed(const DistillArgs& a, int64_t row, i
     }
     __syncthreads();
 }
+template <int E>
+__device__ __forceinline__ uint32_t marks_of(const uint32_t* marks, int vector) { return marks[(vector * E) >> 5] >> ((vector * E) & 31); }
 
-// Maximum and sum of a chunk of a row, and, with the teacher's rest, the same
-// of the tokens that are not listed.
+// The sums of a chunk of a row; the row's loss where it is one chunk.
 template <bool F32, bool REST>
 __global__ void __launch_bounds__(kThreads) distill_stats_kernel(const DistillArgs a) {
     constexpr int E = Row<F32>::E;
-    __shared__ Soft joined[2][kWaves];
+    __shared__ Sums room[2][kWaves];
     __shared__ uint32_t marks[REST ? kBitVectors * E / 32 : 1];
     __shared__ int twice;
     const int lane = threadIdx.x & 63;
@@ -103,176 +259,69 @@ __global__ void __launch_bounds__(kThreads) distill_stats_kernel(const DistillAr
     const int chunk = static_cast<int>(blockIdx.x % a.chunks);
     const Row<F32> r(a.z, row * a.ld, a.v);
     const int from = chunk * a.per, to = min(r.vectors(), from + a.per);
+    Vectors<F32> mine(r, from, to);
     if (REST) mark_listed<E>(a, row, from, to, marks, &twice);
-    Soft all{kLowest, 0.0f};
-    float off = 0.0f;                   // the unlisted tokens' part of the sum, at the same maximum
-    for (int i = from + static_cast<int>(threadIdx.x); i < to; i += kThreads) {
-        const u32x4 raw = r.load(i);
-        float x[E];
-        float top = kNegInf;
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-            x[k] = Row<F32>::at(raw, k);
-            top = fmaxf(top, x[k]);
-        }
-        const float m = fmaxf(all.m, top);
-        const float f = exp2_fast((all.m - m) * a.c);
-        all.s *= f;
-        off *= f;
-        all.m = m;
-        if (!REST) {
-#pragma unroll
-            for (int k = 0; k < E; ++k) all.s += exp2_fast((x[k] - m) * a.c);
-        } else {
-            const int b = (i - from) * E;
-            const uint32_t listed = marks[b >> 5] >> (b & 31);
-#pragma unroll
-            for (int k = 0; k < E; ++k) {
-                const float e = exp2_fast((x[k] - m) * a.c);
-                all.s += e;
-                off += listed & (1u << k) ? 0.0f : e;
-            }
+    if (a.z_at) {                       // the gradient may take the logits' place
+        for (int j = threadIdx.x; j < a.k; j += kThreads) {
+            const int id = a.ids[row * a.k + j];
+            if (id >= 0 && id < a.v && id / E >= from && id / E < to) a.z_at[row * a.k + j] = r.element(id);
         }
     }
-    const float m = wave_max(all.m), f = exp2_fast((all.m - m) * a.c);
-    all.s = wave_sum(all.s * f);
-    if (REST) off = wave_sum(off * f);
-    if (lane == 0) {
-        joined[0][wave] = {m, all.s};
-        joined[1][wave] = {m, off};
+    Sums t{kFloor, 0.0f, 0.0f};
+    mine.each([&](const u32x4& v, int i) { add_vector<F32, REST, true>(t, v, REST ? marks_of<E>(marks, i - from) : 0, a.c); });
+    t = join_group<kWaves>(t, room[0], lane, wave, a.c);
+    if (!usual(t.m, a.c) || t.m == kFloor) {
+        t = {kLowest, 0.0f, 0.0f};
+        Vectors<F32> again(r, from, to);
+        again.each([&](const u32x4& v, int i) { add_vector<F32, REST, false>(t, v, REST ? marks_of<E>(marks, i - from) : 0, a.c); });
+        t = join_group<kWaves>(t, room[1], lane, wave, a.c);
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        Soft* const out = a.part + (row * a.chunks + chunk) * 2;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            Soft s = joined[h][0];
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w) s = soft_join(s, joined[h][w], a.c);
-            out[h] = s;
-        }
-    }
+    if (wave != 0) return;
+    if (a.chunks == 1) write_loss_of<F32>(a, row, t, lane);
+    else if (lane == 0) a.part[row * a.chunks + chunk] = t;
 }
 
-// Loss and statistics of a row, by one wavefront.
-template <bool F32>
-__device__ void finish_row(const DistillArgs& a, int64_t row, Soft all, Soft off, int lane) {
-    const double log_s = log(static_cast<double>(all.s));       // log q = (z - all.m) / T - log_s
-    const Teacher t = teacher_of(a, row, lane);
-    const Row<F32> r(a.z, row * a.ld, a.v);
-    double sum = 0, mass = 0;
-    for (int j = lane; j < a.k; j += 64) {
-        const int id = a.ids[row * a.k + j];
-        if (id < 0 || id >= a.v) continue;
-        const double log_p = t.log_p(a, row * a.k + j), p = exp(log_p);
-        mass += p;
-        if (!(p == 0)) sum += p * (log_p - ((static_cast<double>(r.element(id)) - all.m) * a.inv_t - log_s));
-    }
-    sum = wave_sum_f64(sum);
-    double log_rest = 0;
-    if (a.teacher_lse) {
-        const double rest = 1 - wave_sum_f64(mass);
-        log_rest = (static_cast<double>(off.m) - all.m) * a.inv_t + log(static_cast<double>(off.s)) - log_s;
-        if (!(rest <= 0)) sum += rest * (log(rest) - log_rest);
-    }
-    if (lane == 0) {
-        // a student that is not a distribution has no loss, also where nothing is listed
-        if (a.loss) a.loss[row] = static_cast<float>(log_s - log_s == 0 ? sum * a.t2 : __builtin_nan(""));
-        if (a.stats) {
-            a.stats[3 * row] = all.s == 0.0f ? kNegInf : all.m;
-            a.stats[3 * row + 1] = static_cast<float>(log_s);
-            a.stats[3 * row + 2] = static_cast<float>(log_rest);
-        }
-    }
+__device__ __forceinline__ Sums join_chunks(const DistillArgs& a, int64_t row, int lane) {
+    Sums t{kLowest, 0.0f, 0.0f};
+    for (int c = lane; c < a.chunks; c += 64) t = join(t, a.part[row * a.chunks + c], a.c);
+    return join_wave(t, a.c);
 }
 
 template <bool F32>
 __global__ void __launch_bounds__(256) distill_finish_kernel(const DistillArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t row = a.first + static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (row >= a.n) return;
-    Soft all{kLowest, 0.0f}, off{kLowest, 0.0f};
-    for (int c = lane; c < a.chunks; c += 64) {
-        const Soft* const p = a.part + (row * a.chunks + c) * 2;
-        all = soft_join(all, p[0], a.c);
-        off = soft_join(off, p[1], a.c);
-    }
-    all = soft_wave(all, a.c);
-    off = soft_wave(off, a.c);
-    finish_row<F32>(a, row, all, off, lane);
+    if (row < a.n) write_loss_of<F32>(a, row, join_chunks(a, row, lane), lane);
 }
 
-// The gradient of a chunk of a row: a q everywhere, then the listed tokens
-// once more.  Their logits are read before anything is written, since dz may be z.
-template <bool F32, bool REST>
-__global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArgs a) {
-    constexpr int E = Row<F32>::E;
-    __shared__ uint32_t marks[kBitVectors * E / 32];
-    __shared__ int32_t id_of[kMaxK];
-    __shared__ float p_of[kMaxK];
-    __shared__ int twice;
-    __shared__ Teacher teacher;
-    __shared__ double mass_;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t row = a.first + blockIdx.x / a.chunks;
-    const int chunk = static_cast<int>(blockIdx.x % a.chunks);
-    const Row<F32> r(a.z, row * a.ld, a.v), w(a.dz, row * a.dld, a.v);
-    const float gs = (a.weight ? a.weight[row] : 1.0f) * a.scale;
-    const int from = chunk * a.per, to = min(w.vectors(), from + a.per);
-    if (gs == 0.0f) {
-        for (int i = from + static_cast<int>(threadIdx.x); i < to; i += kThreads) w.store(i, u32x4{0, 0, 0, 0});
-        return;
+// ---------------------------------------------------------------------------
+// The gradient: gs (a q - p), gs the row's factor.  q = 2^(x c - K), K = m c +
+// log2 of the sum: for bf16, whose result rounds by 2^-9, K as one fp32 number that takes the factor
+// too; for fp32 as 2^((x - m) c - L), which loses nothing to K's size.
+struct Slope {
+    float m, L;             // L = log2 of the sum of 2^((x - m) c)
+    float gs, on, off;      // the row's factor; a of listed and of other tokens
+};
+
+template <bool F32>
+struct Gradient {
+    float m, c, L, K, factor;
+    uint32_t sign;
+    bool zero, wide;
+    __device__ __forceinline__ Gradient(const Slope& s, float c_) : m(s.m), c(c_), L(s.L), factor(s.gs * s.off) {
+        // the logarithm of a factor that is neither finite nor positive is no exponent
+        wide = F32 || !usual(s.m, c) || !(fabsf(factor) > 1e-30f && fabsf(factor) < 1e30f);
+        K = m * c + (L - __builtin_amdgcn_logf(fabsf(factor)));
+        sign = factor < 0.0f ? 0x80008000u : 0;
+        zero = s.gs == 0.0f;
     }
-    if (wave == 0) {
-        const Teacher t = teacher_of(a, row, lane);
-        double mass = 0;
-        for (int j = lane; j < a.k; j += 64) {
-            const int id = a.ids[row * a.k + j];
-            if (id >= 0 && id < a.v) mass += exp(t.log_p(a, row * a.k + j));
-        }
-        mass = wave_sum_f64(mass);
-        if (lane == 0) {
-            teacher = t;
-            mass_ = mass;
-        }
-    }
-    mark_listed<E>(a, row, from, to, marks, &twice);
-    const double mass = mass_, rest = 1 - mass;
-    const float m = a.stats[3 * row], log_s = a.stats[3 * row + 1];
-    float on_f = static_cast<float>(mass), off_f = on_f;
-    if (REST) {
-        on_f = 1.0f;
-        const double log_rest = a.stats[3 * row + 2];
-        off_f = rest > 0 && log_rest > -__builtin_inf() ? static_cast<float>(1 - exp(log(rest) - log_rest)) : 1.0f;
-    }
-    const float L = log_s * kLog2e;
-    const auto q_of = [&](float x) { return exp2_fast(__builtin_fmaf(x - m, a.c, -L)); };
-    // this thread's listed tokens
-    constexpr int PER = kMaxK / kThreads;
-    float listed[PER];
-    bool mine[PER];
-#pragma unroll
-    for (int h = 0; h < PER; ++h) {
-        const int j = threadIdx.x + h * kThreads;
-        mine[h] = false;
-        if (j >= a.k) continue;
-        const int id = a.ids[row * a.k + j];
-        const bool on = id >= 0 && id < a.v && id / E >= from && id / E < to;
-        const float p = on ? static_cast<float>(exp(teacher.log_p(a, row * a.k + j))) : 0.0f;
-        id_of[j] = on ? id : -1;
-        p_of[j] = p;
-        mine[h] = on;
-        if (on) listed[h] = r.element(id);
-    }
-    __syncthreads();
-    const float gq = gs * off_f;
-    for (int i = from + static_cast<int>(threadIdx.x); i < to; i += kThreads) {
-        const u32x4 raw = r.load(i);
+    __device__ __forceinline__ float q(float x) const { return exp2_fast(__builtin_fmaf(x - m, c, -L)); }
+    __device__ __forceinline__ u32x4 of_wide(const u32x4& v) const {
+        constexpr int E = Row<F32>::E;
         u32x4 out;
 #pragma unroll
         for (int k = 0; k < E; k += 2) {
-            const float g0 = q_of(Row<F32>::at(raw, k)) * gq, g1 = q_of(Row<F32>::at(raw, k + 1)) * gq;
+            const float g0 = q(Row<F32>::at(v, k)) * factor, g1 = q(Row<F32>::at(v, k + 1)) * factor;
             if (F32) {
                 out[k & 3] = __float_as_uint(g0);
                 out[(k + 1) & 3] = __float_as_uint(g1);
@@ -280,65 +329,198 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
                 out[(k >> 1) & 3] = bf16_pair(g0, g1);
             }
         }
-        w.store(i, out);
+        return zero ? u32x4{0, 0, 0, 0} : out;
     }
+    // where not `wide`
+    __device__ __forceinline__ u32x4 of_usual(const u32x4& v) const {
+        u32x4 out;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            out[k] = sign ^ bf16_pair(exp2_fast(__builtin_fmaf(Row<F32>::at(v, 2 * k), c, -K)),
+                                      exp2_fast(__builtin_fmaf(Row<F32>::at(v, 2 * k + 1), c, -K)));
+        return out;
+    }
+    __device__ __forceinline__ u32x4 of(const u32x4& v) const {
+        if (F32) return of_wide(v);
+        return wide ? of_wide(v) : of_usual(v);
+    }
+};
+
+__device__ __forceinline__ float row_factor(const DistillArgs& a, int64_t row) { return (a.weight ? a.weight[row] : 1.0f) * a.scale; }
+
+// Writes a listed token's gradient over what stands there.
+template <bool F32>
+__device__ __forceinline__ void put_listed(const Row<F32>& w, const Slope& s, float c, int id, float p, float z) {
+    const float g = (exp2_fast(__builtin_fmaf(z - s.m, c, -s.L)) * s.on - p) * s.gs;
+    char* const at = w.base + static_cast<int64_t>(id) * (F32 ? 4 : 2);
+    if (F32) *reinterpret_cast<float*>(at) = g;
+    else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(bf16_pair(g, g));
+}
+// The same for place j of a list that may name a token twice.
+template <bool F32>
+__device__ __forceinline__ void write_listed(const Row<F32>& w, const Slope& s, float c, const int32_t* id_of, const float* p_of, int j, int k, int twice,
+                                             float z) {
+    const int id = id_of[j];
+    float p = p_of[j];
+    if (twice) {
+        double sum = 0;
+        for (int e = 0; e < k; ++e) {
+            if (id_of[e] != id) continue;
+            if (e < j) return;              // the token's first place writes
+            sum += p_of[e];
+        }
+        p = static_cast<float>(sum);
+    }
+    put_listed<F32>(w, s, c, id, p, z);
+}
+
+// a of the tokens off the list: `ratio` = P / Q
+__device__ __forceinline__ float off_list(float rest, float ratio) { return rest > 0.0f && ratio < __builtin_inff() ? 1.0f - ratio : 1.0f; }
+
+// From a row's sums; mass = sum of p.
+template <bool REST>
+__device__ __forceinline__ Slope slope_of(const DistillArgs& a, float gs, const Sums& t, double mass) {
+    Slope s{t.m, __builtin_amdgcn_logf(t.s), gs, static_cast<float>(mass), static_cast<float>(mass)};
+    if (usual(t.m, a.c)) s.L += __builtin_fmaf(-t.m, a.c, t.m * a.c);       // the rounding of R
+    if (REST) {
+        s.on = 1.0f;
+        s.off = off_list(static_cast<float>(1 - mass), static_cast<float>((1 - mass) * (static_cast<double>(t.s) / t.off)));
+    }
+    return s;
+}
+
+// The gradient of a chunk of a row, from the forward's statistics or from the
+// chunks' sums (then the row's first workgroup writes its loss): a q
+// everywhere, then the listed tokens once more.  Their logits are read before anything is
+// written, since dz may be z.
+template <bool F32, bool REST, bool STREAM>
+__global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArgs a) {
+    constexpr int E = Row<F32>::E;
+    __shared__ uint32_t marks[kBitVectors * E / 32];
+    __shared__ int32_t id_of[kMaxK];
+    __shared__ float p_of[kMaxK];
+    __shared__ int twice;
+    __shared__ Teacher teacher_;
+    __shared__ double mass_;
+    __shared__ Slope slope_;
+    __shared__ Sums sums_;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t row = a.first + blockIdx.x / a.chunks;
+    const int chunk = static_cast<int>(blockIdx.x % a.chunks);
+    const Row<F32> r(a.z, row * a.ld, a.v), w(a.dz, row * a.dld, a.v);
+    const int from = chunk * a.per, to = min(w.vectors(), from + a.per);
+    Vectors<F32> mine(r, from, to);
+    const int32_t* const ids = a.ids + row * a.k;
+    const auto t_at = [&](int j) { return teacher_at(a, row * a.k + j); };
+    const auto on = [&](int j) { return ids[j] >= 0 && ids[j] < a.v; };
+    if (wave == 0) {
+        const Teacher teacher = teacher_of(a, row, lane, t_at, on);
+        double mass = 0;
+        for (int j = lane; j < a.k; j += 64)
+            if (on(j)) mass += exp(teacher.log_p(a.inv_t, t_at(j)));
+        mass = wave_sum_f64(mass);
+        if (lane == 0) {
+            teacher_ = teacher;
+            mass_ = mass;
+        }
+    } else if (wave == 1) {
+        Slope s{0, 0, row_factor(a, row), 0, 0};
+        Sums sums{0, 0, 0};
+        if (a.part) {
+            sums = join_chunks(a, row, lane);
+            s.m = sums.m;
+            s.L = static_cast<float>(log_of(sums.s, sums.m, a.c) * 1.4426950408889634074);
+            s.off = static_cast<float>(static_cast<double>(sums.s) / sums.off);     // 1 / Q for now
+        } else {
+            s.m = a.stats[3 * row];
+            s.L = a.stats[3 * row + 1] * kLog2e;
+            s.off = static_cast<float>(exp(-static_cast<double>(a.stats[3 * row + 2])));
+        }
+        if (lane == 0) {
+            slope_ = s;
+            sums_ = sums;
+        }
+    }
+    if (a.k > kScan) {
+        mark_listed<E>(a, row, from, to, marks, &twice);
+    } else {
+        if (threadIdx.x == 0) twice = 0;
+        __syncthreads();
+    }
+    Slope s = slope_;
+    s.on = static_cast<float>(mass_);
+    s.off = REST ? off_list(static_cast<float>(1 - mass_), static_cast<float>((1 - mass_) * s.off)) : s.on;
+    if (REST) s.on = 1.0f;
+    const Teacher teacher = teacher_;
+    // this thread's listed tokens
+    constexpr int PER = kMaxK / kThreads;
+    float listed[PER];
+    bool write[PER];
+#pragma unroll
+    for (int h = 0; h < PER; ++h) {
+        const int j = threadIdx.x + h * kThreads;
+        write[h] = false;
+        if (j >= a.k) continue;
+        const int id = ids[j];
+        const bool here = id >= 0 && id < a.v && id / E >= from && id / E < to && s.gs != 0.0f;
+        id_of[j] = here ? id : -1;
+        p_of[j] = here ? static_cast<float>(exp(teacher.log_p(a.inv_t, t_at(j)))) : 0.0f;
+        write[h] = here;
+        if (here) listed[h] = r.element(id);
+    }
+    __syncthreads();
+    if (a.k <= kScan && write[0]) {             // a short list is compared place by place
+        for (int e = 0; e < static_cast<int>(threadIdx.x); ++e)
+            if (id_of[e] == id_of[threadIdx.x]) twice = 1;
+    }
+    const Gradient<F32> g(s, a.c);
+    mine.each([&](const u32x4& v, int i) { w.template put<STREAM>(i, g.of(v)); });
     // what was stored above has arrived before it is written over
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
 #pragma unroll
-    for (int h = 0; h < PER; ++h) {
-        if (!mine[h]) continue;
-        const int j = threadIdx.x + h * kThreads, id = id_of[j];
-        float p = p_of[j];
-        bool first = true;
-        if (twice) {
-            double sum = 0;
-            for (int e = 0; e < a.k; ++e) {
-                if (id_of[e] != id) continue;
-                if (e < j) first = false;
-                sum += p_of[e];
-            }
-            p = static_cast<float>(sum);
-        }
-        if (!first) continue;
-        const float g = (q_of(listed[h]) * on_f - p) * gs;
-        char* const at = w.base + static_cast<int64_t>(id) * (F32 ? 4 : 2);
-        if (F32) *reinterpret_cast<float*>(at) = g;
-        else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(bf16_pair(g, g));
-    }
+    for (int h = 0; h < PER; ++h)
+        if (write[h]) write_listed<F32>(w, s, a.c, id_of, p_of, threadIdx.x + h * kThreads, a.k, twice, listed[h]);
+    if (a.part && chunk == 0 && wave == kWaves - 1)
+        write_loss(a, row, sums_, teacher, lane, t_at, on, [&](int j) { return a.z_at[row * a.k + j]; });
 }
 
-// Loss and gradient of a row in one pass over memory: the row's vectors stay in
-// registers (NV a thread) between the sums and the gradient; what goes beyond them is
-// read again.  The teacher's side is one wavefront's work while the row's loads
-// are on their way.
+// ---------------------------------------------------------------------------
+// Loss and gradient in one pass over memory: a row's vectors stay in registers
+// (NV a thread) between its sums and its gradient.
+// A row in registers between both would read memory once, but leaves eight
+// wavefronts a compute unit: 4096 x 151936 bf16 took 546 us with all of a row in
+// registers (512 threads, 38 vectors each), 560 as one stream that asks for the next row as it stores this
+// one, 586 with nothing kept (read twice, from the last-level cache the second time); 1024 threads with 14
+// vectors each and the rest read again 497.  Rows of up to 6144 vectors fit whole: 512 threads, two or three
+// workgroups a unit.
 constexpr int kRowMarks = 1 << 18;      // tokens of a row at most
 
-template <bool F32, bool REST, int NV>
-__global__ void __launch_bounds__(kThreads) distill_row_kernel(const DistillArgs a) {
+// The teacher's side is one wavefront's work while the row's loads are on
+// their way.  Vectors beyond those in registers are read again.
+template <bool F32, bool REST, bool STREAM, int THREADS, int NV>
+__global__ void __launch_bounds__(THREADS) distill_row_kernel(const DistillArgs a) {
     constexpr int E = Row<F32>::E;
-    extern __shared__ uint32_t marks[];                 // (v + 31) / 32
-    __shared__ Soft joined[2][kWaves];
+    extern __shared__ uint32_t marks[];                 // v / 32 + 1
+    __shared__ Sums room[2][THREADS / 64];
     __shared__ int32_t id_of[kMaxK];
     __shared__ float t_of[kMaxK], z_of[kMaxK], p_of[kMaxK];
     __shared__ int twice;
-    __shared__ Teacher teacher;
+    __shared__ Teacher teacher_;
     __shared__ double mass_;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t row = a.first + blockIdx.x;
     const Row<F32> r(a.z, row * a.ld, a.v), w(a.dz, row * a.dld, a.v);
-    const float gs = (a.weight ? a.weight[row] : 1.0f) * a.scale;
-    const int whole = static_cast<int>(a.v) / E, all_vectors = r.vectors();
+    const int whole = static_cast<int>(a.v) / E, vectors = r.vectors();
     u32x4 raw[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = tid + j * kThreads;
-        if (i < whole) raw[j] = *reinterpret_cast<const Loose*>(r.base + static_cast<int64_t>(i) * 16);
-    }
-    for (int i = tid; i < (static_cast<int>(a.v) + 31) / 32; i += kThreads) marks[i] = 0;
+    for (int j = 0; j < NV; ++j)
+        if (tid < whole - j * THREADS) raw[j] = r.load_whole(tid + j * THREADS);
+    for (int i = tid; i < static_cast<int>(a.v) / 32 + 1; i += THREADS) marks[i] = 0;
     if (tid == 0) twice = 0;
-    for (int j = tid; j < a.k; j += kThreads) {
+    for (int j = tid; j < a.k; j += THREADS) {
         const int id = a.ids[row * a.k + j];
         const bool on = id >= 0 && id < a.v;
         id_of[j] = on ? id : -1;
@@ -346,169 +528,66 @@ __global__ void __launch_bounds__(kThreads) distill_row_kernel(const DistillArgs
         z_of[j] = on ? r.element(id) : 0.0f;
     }
     __syncthreads();
-    for (int j = tid; j < a.k; j += kThreads) {
+    for (int j = tid; j < a.k; j += THREADS) {
         const int id = id_of[j];
         if (id < 0) continue;
         const uint32_t mask = 1u << (id & 31);
         if (atomicOr(&marks[id >> 5], mask) & mask) twice = 1;
     }
     if (REST) __syncthreads();
+    const auto t_at = [&](int j) { return t_of[j]; };
+    const auto on = [&](int j) { return id_of[j] >= 0; };
     if (wave == 0) {
-        Teacher t{0, 0};
-        if (a.teacher_lse) {
-            t.log_sum = a.teacher_lse[row];
-        } else {
-            float m = kNegInf;
-            for (int j = lane; j < a.k; j += 64)
-                if (id_of[j] >= 0) m = t_of[j] == t_of[j] && m == m ? fmaxf(m, t_of[j]) : __builtin_nanf("");
-            const float top = wave_max(m);
-            const bool nan = __ballot(m != m) != 0;
-            double s = 0;
-            for (int j = lane; j < a.k; j += 64)
-                if (id_of[j] >= 0) s += exp((static_cast<double>(t_of[j]) - top) * a.inv_t);
-            s = wave_sum_f64(s);
-            if (nan) t.log_sum = __builtin_nan("");
-            else if (top == kNegInf) t.log_sum = __builtin_inf();
-            else t = {top, log(s)};
-        }
+        const Teacher teacher = teacher_of(a, row, lane, t_at, on);
         double mass = 0;
         for (int j = lane; j < a.k; j += 64) {
-            const double p = id_of[j] >= 0 ? exp((t_of[j] - t.m) * a.inv_t - t.log_sum) : 0;
+            const double p = on(j) ? exp(teacher.log_p(a.inv_t, t_of[j])) : 0;
             mass += p;
             p_of[j] = static_cast<float>(p);
         }
         mass = wave_sum_f64(mass);
         if (lane == 0) {
-            teacher = t;
+            teacher_ = teacher;
             mass_ = mass;
         }
     }
-    Soft all{kLowest, 0.0f};
-    float off = 0.0f;
-    const auto add = [&](const u32x4& v, int i) {
-        float x[E];
-        float top = kNegInf;
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-            x[k] = Row<F32>::at(v, k);
-            top = fmaxf(top, x[k]);
-        }
-        const float m = fmaxf(all.m, top);
-        const float f = exp2_fast((all.m - m) * a.c);
-        all.s *= f;
-        off *= f;
-        all.m = m;
-        const uint32_t listed = REST ? marks[(i * E) >> 5] >> ((i * E) & 31) : 0;
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-            const float e = exp2_fast((x[k] - m) * a.c);
-            all.s += e;
-            if (REST) off += listed & (1u << k) ? 0.0f : e;
-        }
-    };
+    Sums t{kFloor, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-        if (tid + j * kThreads < whole) add(raw[j], tid + j * kThreads);
-    for (int i = tid + NV * kThreads; i < whole; i += kThreads) add(r.load(i), i);
-    if (whole < all_vectors && tid == kThreads - 1) add(r.load(whole), whole);
-    {
-        const float m = wave_max(all.m), f = exp2_fast((all.m - m) * a.c);
-        all.s = wave_sum(all.s * f);
-        if (REST) off = wave_sum(off * f);
-        if (lane == 0) {
-            joined[0][wave] = {m, all.s};
-            joined[1][wave] = {m, off};
-        }
+        if (tid < whole - j * THREADS) add_vector<F32, REST, true>(t, raw[j], REST ? marks_of<E>(marks, tid + j * THREADS) : 0, a.c);
+    Vectors<F32, THREADS> beyond(r, NV * THREADS, vectors);
+    beyond.each([&](const u32x4& v, int i) { add_vector<F32, REST, true>(t, v, REST ? marks_of<E>(marks, i) : 0, a.c); });
+    t = join_group<THREADS / 64>(t, room[0], lane, wave, a.c);
+    if (!usual(t.m, a.c) || t.m == kFloor) {
+        t = {kLowest, 0.0f, 0.0f};
+        for (int i = tid; i < vectors; i += THREADS) add_vector<F32, REST, false>(t, r.load(i), REST ? marks_of<E>(marks, i) : 0, a.c);
+        t = join_group<THREADS / 64>(t, room[1], lane, wave, a.c);
     }
-    __syncthreads();
-    Soft o = joined[1][0];
-    all = joined[0][0];
+    if (wave == 0) write_loss(a, row, t, teacher_, lane, t_at, on, [&](int j) { return z_of[j]; });
+    const Slope s = slope_of<REST>(a, row_factor(a, row), t, mass_);
+    const Gradient<F32> g(s, a.c);
+    if (!F32 && g.wide) {                               // rare, and short
+        for (int i = tid; i < min(whole, NV * THREADS); i += THREADS) w.store_whole(i, g.of_wide(r.load_whole(i)));
+    } else {
 #pragma unroll
-    for (int h = 1; h < kWaves; ++h) {
-        all = soft_join(all, joined[0][h], a.c);
-        if (REST) o = soft_join(o, joined[1][h], a.c);
+        for (int j = 0; j < NV; ++j)
+            if (tid < whole - j * THREADS) w.template put<STREAM>(tid + j * THREADS, F32 ? g.of_wide(raw[j]) : g.of_usual(raw[j]));
     }
-    if (wave == 0) {
-        const double log_s = log(static_cast<double>(all.s));
-        double sum = 0, log_rest = 0;
-        for (int j = lane; j < a.k; j += 64) {
-            if (id_of[j] < 0) continue;
-            const double log_p = (t_of[j] - teacher.m) * a.inv_t - teacher.log_sum, p = exp(log_p);
-            if (!(p == 0)) sum += p * (log_p - ((static_cast<double>(z_of[j]) - all.m) * a.inv_t - log_s));
-        }
-        sum = wave_sum_f64(sum);
-        if (REST) {
-            const double rest = 1 - mass_;
-            log_rest = (static_cast<double>(o.m) - all.m) * a.inv_t + log(static_cast<double>(o.s)) - log_s;
-            if (!(rest <= 0)) sum += rest * (log(rest) - log_rest);
-        }
-        if (lane == 0) {
-            if (a.loss) a.loss[row] = static_cast<float>(log_s - log_s == 0 ? sum * a.t2 : __builtin_nan(""));
-            a.stats[3 * row] = all.s == 0.0f ? kNegInf : all.m;
-            a.stats[3 * row + 1] = static_cast<float>(log_s);
-            a.stats[3 * row + 2] = static_cast<float>(log_rest);
-        }
-    }
-    float on_f = static_cast<float>(mass_), off_f = on_f;
-    if (REST) {
-        on_f = 1.0f;
-        const float rest = static_cast<float>(1 - mass_);
-        off_f = rest > 0.0f && o.s > 0.0f ? 1.0f - rest * (all.s / o.s) * exp2_fast((all.m - o.m) * a.c) : 1.0f;
-    }
-    const float L = __builtin_amdgcn_logf(all.s), m = all.m, gq = gs * off_f;
-    const auto q_of = [&](float x) { return exp2_fast(__builtin_fmaf(x - m, a.c, -L)); };
-    const auto grad = [&](const u32x4& v) {
-        u32x4 out;
-#pragma unroll
-        for (int k = 0; k < E; k += 2) {
-            const float g0 = q_of(Row<F32>::at(v, k)) * gq, g1 = q_of(Row<F32>::at(v, k + 1)) * gq;
-            if (F32) {
-                out[k & 3] = __float_as_uint(g0);
-                out[(k + 1) & 3] = __float_as_uint(g1);
-            } else {
-                out[(k >> 1) & 3] = bf16_pair(g0, g1);
-            }
-        }
-        return gs == 0.0f ? u32x4{0, 0, 0, 0} : out;
-    };
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int i = tid + j * kThreads;
-        if (i < whole) *reinterpret_cast<Loose*>(w.base + static_cast<int64_t>(i) * 16) = grad(raw[j]);
-    }
-    for (int i = tid + NV * kThreads; i < whole; i += kThreads) w.store(i, grad(r.load(i)));
-    if (whole < all_vectors && tid == kThreads - 1) w.store(whole, grad(r.load(whole)));
-    if (gs == 0.0f) return;
+    Vectors<F32, THREADS> again(r, NV * THREADS, vectors);
+    again.each([&](const u32x4& v, int i) { w.template put<STREAM>(i, g.of(v)); });
+    if (s.gs == 0.0f) return;
     // what was stored above has arrived before it is written over
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    for (int j = tid; j < a.k; j += kThreads) {
-        const int id = id_of[j];
-        if (id < 0) continue;
-        float p = p_of[j];
-        bool first = true;
-        if (twice) {
-            double sum = 0;
-            for (int e = 0; e < a.k; ++e) {
-                if (id_of[e] != id) continue;
-                if (e < j) first = false;
-                sum += p_of[e];
-            }
-            p = static_cast<float>(sum);
-        }
-        if (!first) continue;
-        const float g = (q_of(z_of[j]) * on_f - p) * gs;
-        char* const at = w.base + static_cast<int64_t>(id) * (F32 ? 4 : 2);
-        if (F32) *reinterpret_cast<float*>(at) = g;
-        else *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(bf16_pair(g, g));
-    }
+    for (int j = tid; j < a.k; j += THREADS)
+        if (id_of[j] >= 0) write_listed<F32>(w, s, a.c, id_of, p_of, j, a.k, twice, z_of[j]);
 }
 
 // Workgroups a row: one where rows fill the card; few rows are cut into parts
 // of 512 vectors and more.
 int chunks_of(int64_t n, int64_t v, int dtype) {
     const int64_t e = dtype == NGRAM_F32 ? 4 : 8, vectors = (v + e - 1) / e;
-    const int64_t want = (1024 + n - 1) / std::max<int64_t>(n, 1);
+    const int64_t want = 1024 / std::max<int64_t>(n, 1);
     return static_cast<int>(std::max<int64_t>((vectors + kBitVectors - 1) / kBitVectors, std::min<int64_t>(want, vectors / 512)));
 }
 
@@ -561,33 +640,62 @@ void over_rows(DistillArgs a, int64_t units, int64_t per_row, int threads, int64
     }
 }
 
-void launch_grad(const DistillArgs& a, bool f32, hipStream_t st) {
+bool streams(const DistillArgs& a, bool f32) { return a.n * a.v * (f32 ? 4 : 2) > kStreamFrom; }
+
+template <bool F32, bool REST>
+void launch_grad_of(const DistillArgs& a, hipStream_t st) {
     over_rows(a, a.n, a.chunks, kThreads, 1, [&](const DistillArgs& b, dim3 grid) {
-        const dim3 block(kThreads);
-        if (f32 && b.teacher_lse) hipLaunchKernelGGL((distill_grad_kernel<true, true>), grid, block, 0, st, b);
-        else if (f32) hipLaunchKernelGGL((distill_grad_kernel<true, false>), grid, block, 0, st, b);
-        else if (b.teacher_lse) hipLaunchKernelGGL((distill_grad_kernel<false, true>), grid, block, 0, st, b);
-        else hipLaunchKernelGGL((distill_grad_kernel<false, false>), grid, block, 0, st, b);
+        if (streams(a, F32)) hipLaunchKernelGGL((distill_grad_kernel<F32, REST, true>), grid, dim3(kThreads), 0, st, b);
+        else hipLaunchKernelGGL((distill_grad_kernel<F32, REST, false>), grid, dim3(kThreads), 0, st, b);
     });
+}
+void launch_grad(const DistillArgs& a, bool f32, hipStream_t st) {
+    if (f32 && a.teacher_lse) launch_grad_of<true, true>(a, st);
+    else if (f32) launch_grad_of<true, false>(a, st);
+    else if (a.teacher_lse) launch_grad_of<false, true>(a, st);
+    else launch_grad_of<false, false>(a, st);
 }
 
 // Rows in one workgroup each: enough of them to fill the card, short enough for the marks.
 bool whole_rows(const DistillArgs& a) { return a.n >= 256 && a.v <= kRowMarks; }
 
-template <bool F32, bool REST, int NV>
-void launch_rows_of(const DistillArgs& a, hipStream_t st) {
-    const uint32_t lds = static_cast<uint32_t>((a.v + 31) / 32 * 4);
-    over_rows(a, a.n, 1, kThreads, 1, [&](const DistillArgs& b, dim3 grid) {
-        hipLaunchKernelGGL((distill_row_kernel<F32, REST, NV>), grid, dim3(kThreads), lds, st, b);
+template <bool F32, bool REST, bool STREAM, int THREADS, int NV>
+void launch_row(const DistillArgs& a, hipStream_t st) {
+    const uint32_t lds = static_cast<uint32_t>((a.v / 32 + 1) * 4);
+    over_rows(a, a.n, 1, THREADS, 1, [&](const DistillArgs& b, dim3 grid) {
+        hipLaunchKernelGGL((distill_row_kernel<F32, REST, STREAM, THREADS, NV>), grid, dim3(THREADS), lds, st, b);
     });
+}
+template <bool F32, bool REST, bool STREAM>
+void launch_rows_of(const DistillArgs& a, hipStream_t st) {
+    const int64_t vectors = a.v / Row<F32>::E;
+    if (vectors <= 4 * 512) launch_row<F32, REST, STREAM, 512, 4>(a, st);
+    else if (vectors <= 12 * 512) launch_row<F32, REST, STREAM, 512, 12>(a, st);
+    else launch_row<F32, REST, STREAM, 1024, 14>(a, st);
 }
 template <bool F32, bool REST>
 void launch_rows(const DistillArgs& a, hipStream_t st) {
-    const int64_t vectors = a.v / Row<F32>::E;
-    if (vectors <= 4 * kThreads) launch_rows_of<F32, REST, 4>(a, st);
-    else if (vectors <= 12 * kThreads) launch_rows_of<F32, REST, 12>(a, st);
-    else if (vectors <= 24 * kThreads) launch_rows_of<F32, REST, 24>(a, st);
-    else launch_rows_of<F32, REST, 38>(a, st);
+    if (streams(a, F32)) launch_rows_of<F32, REST, true>(a, st);
+    else launch_rows_of<F32, REST, false>(a, st);
+}
+
+// Bytes of a workspace: the chunks' sums, statistics that the caller does not
+// ask for, and the listed tokens' logits.
+struct Room {
+    int64_t part, stats, z_at, total;
+};
+Room room_of(int64_t n, int64_t v, int64_t k, int dtype) {
+    DistillArgs a = {};
+    a.n = n;
+    a.v = v;
+    Room r;
+    const auto round = [](int64_t b) { return (b + 15) / 16 * 16; };
+    const int64_t chunks = chunks_of(n, v, dtype);
+    r.part = 0;
+    r.stats = chunks > 1 ? round(n * chunks * static_cast<int64_t>(sizeof(Sums))) : 0;
+    r.z_at = r.stats + round(n * 12);
+    r.total = r.z_at + (chunks > 1 ? round(n * k * 4) : 0);
+    return r;
 }
 
 }  // namespace
@@ -597,9 +705,10 @@ using namespace ng8;
 
 extern "C" {
 
-int64_t ngram_distill_workspace_bytes(int64_t n, int64_t V, int32_t dtype) {
-    if (n < 0 || n > NGRAM_FP8_MAX || V < 1 || V > NGRAM_FP8_MAX || (dtype != NGRAM_F32 && dtype != NGRAM_BF16)) return -1;
-    return n * chunks_of(n, V, dtype) * 2 * static_cast<int64_t>(sizeof(Soft)) + n * 12;
+int64_t ngram_distill_workspace_bytes(int64_t n, int64_t V, int32_t k, int32_t dtype) {
+    if (n < 0 || n > NGRAM_FP8_MAX || V < 1 || V > NGRAM_FP8_MAX || k < 1 || k > NGRAM_DISTILL_MAX_K || (dtype != NGRAM_F32 && dtype != NGRAM_BF16))
+        return -1;
+    return room_of(n, V, k, dtype).total;
 }
 
 int ngram_distill(const ngram_distill_args* p, float* loss_out, float* stats_out, const float* weight, float scale,
@@ -612,12 +721,13 @@ int ngram_distill(const ngram_distill_args* p, float* loss_out, float* stats_out
     if (dlogits_out && (rc = check_grad(p, weight, scale, dlogits_out, dld))) return rc;
     if (p->n == 0) return NGRAM_OK;
     DistillArgs a = device_args(p);
-    const int64_t parts = a.n * a.chunks * 2 * static_cast<int64_t>(sizeof(Soft)), need = parts + a.n * 12;
-    if (!workspace || workspace_bytes < need || !aligned(workspace, 16))
-        return fail(NGRAM_EINVAL, "workspace must hold %lld bytes, 16-byte aligned", (long long)need);
+    const Room room = room_of(a.n, a.v, a.k, p->dtype);
+    if (!workspace || workspace_bytes < room.total || !aligned(workspace, 16))
+        return fail(NGRAM_EINVAL, "workspace must hold %lld bytes, 16-byte aligned", (long long)room.total);
+    char* const at = static_cast<char*>(workspace);
     a.loss = loss_out;
-    a.part = static_cast<Soft*>(workspace);
-    a.stats = stats_out ? stats_out : reinterpret_cast<float*>(static_cast<char*>(workspace) + parts);
+    a.part = reinterpret_cast<Sums*>(at + room.part);
+    a.stats = stats_out ? stats_out : reinterpret_cast<float*>(at + room.stats);
     a.weight = weight; a.scale = static_cast<float>(static_cast<double>(scale) * p->temperature); a.dz = dlogits_out; a.dld = dld;
     const bool f32 = p->dtype == NGRAM_F32;
     if (dlogits_out && whole_rows(a)) {
@@ -627,6 +737,7 @@ int ngram_distill(const ngram_distill_args* p, float* loss_out, float* stats_out
         else launch_rows<false, false>(a, stream);
         return hip_status("ngram_distill");
     }
+    if (dlogits_out && a.chunks > 1) a.z_at = reinterpret_cast<float*>(at + room.z_at);
     over_rows(a, a.n, a.chunks, kThreads, 1, [&](const DistillArgs& b, dim3 grid) {
         const dim3 block(kThreads);
         if (f32 && b.teacher_lse) hipLaunchKernelGGL((distill_stats_kernel<true, true>), grid, block, 0, stream, b);
@@ -634,11 +745,14 @@ int ngram_distill(const ngram_distill_args* p, float* loss_out, float* stats_out
         else if (b.teacher_lse) hipLaunchKernelGGL((distill_stats_kernel<false, true>), grid, block, 0, stream, b);
         else hipLaunchKernelGGL((distill_stats_kernel<false, false>), grid, block, 0, stream, b);
     });
-    over_rows(a, (a.n + 3) / 4, 1, 256, 4, [&](const DistillArgs& b, dim3 grid) {
+    if (a.chunks > 1 && !dlogits_out) over_rows(a, (a.n + 3) / 4, 1, 256, 4, [&](const DistillArgs& b, dim3 grid) {
         if (f32) hipLaunchKernelGGL(distill_finish_kernel<true>, grid, dim3(256), 0, stream, b);
         else hipLaunchKernelGGL(distill_finish_kernel<false>, grid, dim3(256), 0, stream, b);
     });
-    if (dlogits_out) launch_grad(a, f32, stream);
+    if (dlogits_out) {
+        if (a.chunks == 1) a.part = nullptr;        // the loss and the statistics are there
+        launch_grad(a, f32, stream);
+    }
     return hip_status("ngram_distill");
 }
 

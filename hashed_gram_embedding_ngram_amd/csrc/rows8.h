@@ -29,10 +29,16 @@ struct Row {
         return F32 ? *reinterpret_cast<const float*>(p)
                    : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) << 16);
     }
+    __device__ __forceinline__ u32x4 load_whole(int i) const { return *reinterpret_cast<const Loose*>(base + static_cast<int64_t>(i) * 16); }
+    __device__ __forceinline__ void store_whole(int i, const u32x4& x) const { *reinterpret_cast<Loose*>(base + static_cast<int64_t>(i) * 16) = x; }
+    // past the caches' usual keeping
+    __device__ __forceinline__ void store_stream(int i, const u32x4& x) const {
+        __builtin_nontemporal_store(x, reinterpret_cast<Loose*>(base + static_cast<int64_t>(i) * 16));
+    }
     // The 16 bytes of vector i; places past the row are -inf, and no byte past
     // it is read.
     __device__ __forceinline__ u32x4 load(int i) const {
-        if (whole(i)) return *reinterpret_cast<const Loose*>(base + static_cast<int64_t>(i) * 16);
+        if (whole(i)) return load_whole(i);
         u32x4 r;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -49,7 +55,7 @@ struct Row {
     }
     __device__ __forceinline__ void store(int i, const u32x4& x) const {
         if (whole(i)) {
-            *reinterpret_cast<Loose*>(base + static_cast<int64_t>(i) * 16) = x;
+            store_whole(i, x);
             return;
         }
 #pragma unroll
@@ -59,6 +65,12 @@ struct Row {
             if (F32) reinterpret_cast<uint32_t*>(base)[j] = x[k & 3];
             else reinterpret_cast<uint16_t*>(base)[j] = static_cast<uint16_t>(x[(k >> 1) & 3] >> (16 * (k & 1)));
         }
+    }
+    template <bool STREAM>
+    __device__ __forceinline__ void put(int i, const u32x4& x) const {
+        if (!whole(i)) store(i, x);
+        else if (STREAM) store_stream(i, x);
+        else store_whole(i, x);
     }
     static __device__ __forceinline__ float at(const u32x4& r, int k) {      // k a constant once unrolled
         if (F32) return __uint_as_float(r[k & 3]);

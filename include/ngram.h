@@ -708,7 +708,7 @@ int ngram_beam_reorder(const ngram_beam_state* states, int32_t count, const int3
  * weight[i] * scale * loss[i]; a row with weight * scale 0 gets zeros, whatever its logits hold.
  * z: any distance ld >= V elements between rows, element-aligned; t [n][k]
  * and z have types of their own; weight, teacher_lse [n] fp32.  T positive and
- * finite.  workspace: device, 16-byte aligned, ngram_distill_workspace_bytes bytes (may be 0). */
+ * finite.  workspace: device, 16-byte aligned, ngram_distill_workspace_bytes bytes; calls that can overlap need one each. */
 #define NGRAM_DISTILL_MAX_K 1024
 
 typedef struct {
@@ -725,7 +725,7 @@ typedef struct {
     float temperature;
 } ngram_distill_args;
 
-int64_t ngram_distill_workspace_bytes(int64_t n, int64_t V, int32_t dtype);
+int64_t ngram_distill_workspace_bytes(int64_t n, int64_t V, int32_t k, int32_t dtype);
 int ngram_distill(const ngram_distill_args* a, float* loss_out, float* stats_out, const float* weight, float scale,
                   void* dlogits_out, int64_t dld, void* workspace, int64_t workspace_bytes, ngram_stream_t stream);
 /* The gradient from the forward's stats_out, for a backward of its own. */

@@ -29,8 +29,8 @@ def test_sizes():
     assert L.ngram_beam_step_workspace_bytes(1, 4, 1000, 0) > 0
     for bad in ((-1, 4, 1000, 0), (1, 0, 1000, 0), (1, 33, 1000, 0), (1, 4, 0, 0), (1, 4, ng.PAD_ID, 0), (1, 4, 1000, 2)):
         assert L.ngram_beam_step_workspace_bytes(*bad) == -1
-    assert L.ngram_distill_workspace_bytes(0, 5, 0) >= 0 and L.ngram_distill_workspace_bytes(3, 5, 1) > 0
-    for bad in ((-1, 5, 0), (1, 0, 0), (1, (1 << 30) + 1, 0), ((1 << 30) + 1, 5, 0), (1, 5, 2)):
+    assert L.ngram_distill_workspace_bytes(0, 5, 1, 0) >= 0 and L.ngram_distill_workspace_bytes(3, 5, 1, 1) > 0
+    for bad in ((-1, 5, 1, 0), (1, 0, 1, 0), (1, (1 << 30) + 1, 1, 0), ((1 << 30) + 1, 5, 1, 0), (1, 5, 1, 2), (1, 5, 0, 0), (1, 5, 1025, 0)):
         assert L.ngram_distill_workspace_bytes(*bad) == -1
 
 

@@ -233,7 +233,7 @@ def test_in_a_graph_and_on_another_stream():
     n, V, k = 40, 5001, 9
     sets = [inputs(np.random.default_rng(30 + i), n, V, k, BF, BF, True, 1.0) for i in range(3)]
     g = gpu(sets[0], BF, BF)
-    ws = ng.distill_workspace(n, V, BF)
+    ws = ng.distill_workspace(n, V, k, BF)
     call = lambda **kw: ng.ngram_distill(g["z"], g["t"], g["ids"], 1.0, g["lse"], grad=True, weight=g["weight"], keep_stats=True, **kw)  # noqa: E731
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
