@@ -224,15 +224,20 @@ __device__ __forceinline__ void transpose4(u32x4& w) {
     w = u32x4{a, b, c, d};
 }
 
-// Eight codes as the bf16 numbers 16 + q, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ bf16x8 widen4(uint32_t w) {
-    u32x4 r;
-    r[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
-    r[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
-    r[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
-    r[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
-    return __builtin_bit_cast(bf16x8, r);
-}
+// Eight codes as the bf16 numbers 16 + q, in the order 0 4 1 5 2 6 3 7: two
+// instructions for two codes, with both constants in registers.
+struct Widen {
+    uint32_t mask = 0x00780078u, sixteen = 0x41804180u;
+    __device__ __forceinline__ Widen() { asm("" : "+s"(mask), "+v"(sixteen)); }
+    __device__ __forceinline__ bf16x8 operator()(uint32_t w) const {
+        u32x4 r;
+        r[0] = ((w << 3) & mask) | sixteen;
+        r[1] = ((w >> 1) & mask) | sixteen;
+        r[2] = ((w >> 5) & mask) | sixteen;
+        r[3] = ((w >> 9) & mask) | sixteen;
+        return __builtin_bit_cast(bf16x8, r);
+    }
+};
 
 // Eight values of x, as 1 or 3 bf16 operands in the order 0 4 1 5 2 6 3 7.
 template <bool F32>
@@ -265,32 +270,52 @@ __device__ __forceinline__ void parts_of(const Raw8<F32>& x, bf16x8* out) {
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
 // What a lane holds of a chunk of its weight row: codes, and the scales and
-// -(16 + zero) of the chunk's groups.
+// -(16 + zero) of the chunk's groups.  16 rows' addresses are one uniform base and
+// a 32-bit distance.
+struct WeightRows {
+    const uint8_t* codes;
+    const char* scales;
+    const uint8_t* zeros;
+    uint32_t row, srow;         // the lane's row from the base, in bytes and in scales
+    uint32_t ld, quarter;
+    int sf32;
+    __device__ __forceinline__ WeightRows(const ProductArgs& a, int64_t tile, int lane) {
+        const int64_t r0 = min(tile * 16, a.o - 1);
+        const uint32_t r = static_cast<uint32_t>(min(tile * 16 + (lane & 15), a.o - 1) - r0);
+        sf32 = a.sf32;
+        codes = a.codes + r0 * a.ld;
+        scales = static_cast<const char*>(a.scales) + r0 * a.sld * (sf32 ? 4 : 2);
+        zeros = a.zeros ? a.zeros + r0 * a.sld : nullptr;
+        ld = static_cast<uint32_t>(a.ld);
+        row = r * ld;
+        srow = r * static_cast<uint32_t>(a.sld);
+        quarter = static_cast<uint32_t>(lane >> 4) * 16;
+    }
+};
 template <int GROUP>
 struct Weights {
     static constexpr int G = kChunk / GROUP;
     u32x4 w;
     u32x4 s;
     uint32_t z;
-    // `row` is clamped by the caller; `col` the lane's first of 32 columns
-    __device__ __forceinline__ void load(const ProductArgs& a, int64_t row, int chunk, int quarter) {
-        const int at = chunk * 64 + quarter * 16;
-        if (at < a.ld) w = *reinterpret_cast<const u32x4*>(a.codes + row * a.ld + at); else w = u32x4{0, 0, 0, 0};
-        const int64_t g = row * a.sld + chunk * G;
-        if (a.sf32) {
-            const float* const p = static_cast<const float*>(a.scales) + g;
+    __device__ __forceinline__ void load(const WeightRows& r, int chunk) {
+        // past the row's last 16 bytes: any codes will do, x is 0 there
+        w = *reinterpret_cast<const u32x4*>(r.codes + (r.row + min(static_cast<uint32_t>(chunk) * 64 + r.quarter, r.ld - 16)));
+        const uint32_t g = r.srow + static_cast<uint32_t>(chunk) * G;
+        if (r.sf32) {
+            const char* const p = r.scales + g * 4;
             if (G == 4) s = *reinterpret_cast<const u32x4*>(p);
             else if (G == 2) { const u32x2 v = *reinterpret_cast<const u32x2*>(p); s[0] = v[0]; s[1] = v[1]; }
             else s[0] = *reinterpret_cast<const uint32_t*>(p);
         } else {
-            const uint16_t* const p = static_cast<const uint16_t*>(a.scales) + g;
+            const char* const p = r.scales + g * 2;
             if (G == 4) { const u32x2 v = *reinterpret_cast<const u32x2*>(p); s[0] = v[0]; s[1] = v[1]; }
             else if (G == 2) s[0] = *reinterpret_cast<const uint32_t*>(p);
-            else s[0] = *p;
+            else s[0] = *reinterpret_cast<const uint16_t*>(p);
         }
         z = 0x08080808u;
-        if (a.zeros) {
-            const uint8_t* const p = a.zeros + g;
+        if (r.zeros) {
+            const uint8_t* const p = r.zeros + g;
             z = G == 4 ? *reinterpret_cast<const uint32_t*>(p) : G == 2 ? *reinterpret_cast<const uint16_t*>(p) : *p;
         }
     }
@@ -320,7 +345,8 @@ __global__ void __launch_bounds__(64 * kSplitWaves) project_int4_split_kernel(co
     const int lr = lane & 15, quarter = lane >> 4;
     const int64_t mtile = a.first + blockIdx.x / a.otiles, otile = blockIdx.x % a.otiles;
     const int64_t wrow = otile * 16 + lr;
-    const int64_t row = min(wrow, a.o - 1);
+    const WeightRows rows(a, otile, lane);
+    const Widen widen4;
     const int64_t m0 = mtile * 16 * MT;
     bf16x8 ones;
 #pragma unroll
@@ -330,7 +356,7 @@ __global__ void __launch_bounds__(64 * kSplitWaves) project_int4_split_kernel(co
     for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     for (int c = wave; c < a.chunks; c += kSplitWaves) {
         Weights<GROUP> w;
-        w.load(a, row, c, quarter);
+        w.load(rows, c);
         Raw8<F32> x[MT][4];
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -381,114 +407,320 @@ __global__ void __launch_bounds__(64 * kSplitWaves) project_int4_split_kernel(co
     }
 }
 
+// Few rows of x: they stay in registers.  The wavefronts of a workgroup share
+// the columns, PER chunks each, and walk over tiles of 16 weight rows; a tile's
+// sums are joined in LDS, in a fixed order, by MT of the wavefronts in turn.
+//
+// Each wavefront brings its own codes, scales and zeros into LDS, SLOTS - 1
+// tiles ahead, so that nothing but its own loads is waited for.  Through LDS
+// because the matrix operand wants neighbouring lanes in different rows, and a load whose
+// neighbouring lanes lie in different rows takes four times as long: here four
+// lanes read the 64 bytes of a row.  A row's four parts lie rotated by half its
+// number, so that reads have no bank conflicts.
+template <int MT, int GROUP, bool F32, bool SF32, int PER>
+struct RowsShape {
+    static constexpr int G = kChunk / GROUP, PARTS = F32 ? 3 : 1, F = GROUP / 32;
+    static constexpr int SLOTS = PER == 4 ? 2 : PER == 2 ? 3 : 4;
+    static constexpr int SD = PER * G * (SF32 ? 4 : 2) < 4 ? 1 : PER * G * (SF32 ? 4 : 2) / 4;      // words of scales a row
+    static constexpr int ZD = PER * G < 4 ? 1 : PER * G / 4;                                        // words of zeros a row
+    static constexpr int SL = (16 * SD + 63) / 64, ZL = (16 * ZD + 63) / 64;                        // loads of them
+    static constexpr int Slot = PER * 1024 + (SL + ZL) * 256;
+    static constexpr int Part = MT * 1024;
+    static constexpr int bytes(int waves) { return waves * (SLOTS * Slot + 2 * Part); }
+};
+
+template <int MT, int GROUP, bool F32, bool SF32, int PER, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) project_int4_rows_kernel(const ProductArgs a) {
+    typedef RowsShape<MT, GROUP, F32, SF32, PER> S;
+    constexpr int G = S::G, PARTS = S::PARTS, F = S::F, SLOTS = S::SLOTS;
+    extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int lr = lane & 15, quarter = lane >> 4;
+    uint8_t* const mine = lds + wave * SLOTS * S::Slot;
+    uint8_t* const part = lds + waves * SLOTS * S::Slot;            // [2][waves][MT][64 lanes][16]
+    const int64_t m0 = a.first * 16 * MT;
+    const Widen widen4;
+    const int c0 = wave * PER;
+    const uint32_t ld = static_cast<uint32_t>(a.ld), sld = static_cast<uint32_t>(a.sld);
+    // this lane's place in its row of codes, for each chunk, and in the rows of scales and zeros
+    uint32_t at[PER];
+#pragma unroll
+    for (int c = 0; c < PER; ++c)       // past the row's last 16 bytes: any codes will do, x is 0 there
+        at[c] = min(static_cast<uint32_t>(c0 + c) * 64 + 16 * ((lane & 3) ^ ((lane >> 3) & 3)), ld - 16);
+    const auto load = [&](int64_t tile, int slot) {
+        const int64_t r0 = min(tile, a.otiles - 1) * 16;
+        const uint32_t last = static_cast<uint32_t>(min(a.o - 1 - r0, INT64_C(15)));
+        uint8_t* const to = mine + slot * S::Slot;
+        const uint8_t* const codes = a.codes + r0 * a.ld;
+        const uint32_t row = min(static_cast<uint32_t>(lane >> 2), last) * ld;
+#pragma unroll
+        for (int h = 0; h < S::SL; ++h) {
+            const uint32_t i = h * 64 + lane, r = min(i / S::SD, last), words = sld * (SF32 ? 4 : 2) / 4;
+            const uint32_t w = min(static_cast<uint32_t>(c0) * G * (SF32 ? 4 : 2) / 4 + i % S::SD, words - 1);
+            const char* const s = static_cast<const char*>(a.scales) + r0 * a.sld * (SF32 ? 4 : 2);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(s + (r * words + w) * 4),
+                                             (__attribute__((address_space(3))) void*)(to + PER * 1024 + h * 256), 4, 0, 0);
+        }
+        if (a.zeros) {
+#pragma unroll
+            for (int h = 0; h < S::ZL; ++h) {
+                const uint32_t i = h * 64 + lane, r = min(i / S::ZD, last);
+                const uint32_t w = min(static_cast<uint32_t>(c0) * G / 4 + i % S::ZD, sld / 4 - 1);
+                const uint8_t* const s = a.zeros + r0 * a.sld;
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(s + r * sld + w * 4),
+                                                 (__attribute__((address_space(3))) void*)(to + PER * 1024 + (S::SL + h) * 256), 4, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(codes + (row + at[c])),
+                                             (__attribute__((address_space(3))) void*)(to + c * 1024), 16, 0, 0);
+    };
+    bf16x8 x[PER][MT][4][PARTS];
+    f32x4 sx[PER][G][MT];
+    {
+        Raw8<F32> raw[PER][MT][4];
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int f = 0; f < 4; ++f) {
+                    const int64_t m = m0 + 16 * t + lr;
+                    const int col = (c0 + c) * kChunk + 32 * f + 8 * quarter;
+                    if (m < a.n && col < a.k) raw[c][t][f].load(a.x, m * a.k + col); else raw[c][t][f].zero();
+                }
+        bf16x8 ones;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ones[i] = static_cast<__bf16>(1.0f);
+#pragma unroll
+        for (int c = 0; c < PER; ++c)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int f = 0; f < F; ++f) {
+                        parts_of<F32>(raw[c][t][g * F + f], x[c][t][g * F + f]);
+#pragma unroll
+                        for (int q = 0; q < PARTS; ++q) s = mfma(x[c][t][g * F + f][q], ones, s);
+                    }
+                    sx[c][g][t] = s;
+                }
+    }
+    int64_t tile = blockIdx.x;
+#pragma unroll
+    for (int h = 0; h + 1 < SLOTS; ++h) load(tile + h * static_cast<int64_t>(gridDim.x), h);
+    int slot = 0, turn = 0;
+    for (; tile < a.otiles; tile += gridDim.x, ++turn) {
+        // the reads of the slot's tile before last ended with their products; zeros' loads may be missing from the count
+        load(tile + (SLOTS - 1) * static_cast<int64_t>(gridDim.x), (slot + SLOTS - 1) % SLOTS);
+        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"i"((SLOTS - 1) * (PER + S::SL)) : "memory");
+        const uint8_t* const from = mine + slot * S::Slot;
+        f32x4 acc[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const uint8_t* const sp = from + PER * 1024 + lr * S::SD * 4 + (PER * G * (SF32 ? 4 : 2) < 4 ? (c0 * G * (SF32 ? 4 : 2)) & 3 : 0);
+        const uint8_t* const zp = from + PER * 1024 + S::SL * 256 + lr * S::ZD * 4 + (PER * G < 4 ? (c0 * G) & 3 : 0);
+#pragma unroll
+        for (int c = 0; c < PER; ++c) {
+            u32x4 w = *reinterpret_cast<const u32x4*>(from + c * 1024 + lr * 64 + 16 * (quarter ^ ((lr >> 1) & 3)));
+            transpose4(w);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int i = c * G + g;
+                const float sv = SF32 ? *reinterpret_cast<const float*>(sp + 4 * i)
+                                      : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sp + 2 * i)) << 16);
+                const float z = -16.0f - (a.zeros ? static_cast<float>(zp[i]) : 8.0f);
+                bf16x8 b[F];
+#pragma unroll
+                for (int f = 0; f < F; ++f) b[f] = widen4(w[g * F + f]);
+                // past the last group there may be anything
+                const float s = (c0 + c) * kChunk + g * GROUP < a.k ? sv : 0.0f;
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    f32x4 d = sx[c][g][t] * z;
+#pragma unroll
+                    for (int f = 0; f < F; ++f)
+#pragma unroll
+                        for (int q = 0; q < PARTS; ++q) d = mfma(x[c][t][g * F + f][q], b[f], d);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(s, d[e], acc[t][e]);
+                }
+            }
+        }
+        f32x4* const sum = reinterpret_cast<f32x4*>(part + (turn & 1) * waves * S::Part);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) sum[(wave * MT + t) * 64 + lane] = acc[t];
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            if ((turn * MT + t) % waves != wave) continue;
+            f32x4 v = sum[t * 64 + lane];
+            for (int h = 1; h < waves; ++h) v += sum[(h * MT + t) * 64 + lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) store_y(a, m0 + 16 * t + 4 * quarter + e, tile * 16 + lr, v[e]);
+        }
+        slot = slot + 1 == SLOTS ? 0 : slot + 1;
+    }
+    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");            // loads into LDS end before the workgroup does
+}
+
 constexpr int kTileWaves = 8;
 
-// Many weight rows: a workgroup has 128 of them, 16 a wavefront, and walks
-// the columns; x goes through LDS in operand order, with its sums over
-// 32 columns, one chunk ahead.
-template <int MT, int GROUP, bool F32>
+// Many weight rows and more rows of x than registers hold: a workgroup has 128
+// weight rows, 16 a wavefront, and walks the columns KS chunks at a time; x
+// goes through LDS in operand order, with its sums over groups, one step ahead,
+// and the weights' loads are a step ahead too.
+template <int MT, int GROUP, bool F32, int KS>
 __global__ void __launch_bounds__(64 * kTileWaves) project_int4_tile_kernel(const ProductArgs a) {
-    constexpr int G = kChunk / GROUP, PARTS = F32 ? 3 : 1, F = GROUP / 32, ITEMS = 4 * MT, PER = (ITEMS + kTileWaves - 1) / kTileWaves;
-    __shared__ bf16x8 xs[2][ITEMS][PARTS][64];
-    __shared__ float sums[2][ITEMS][16];
+    constexpr int G = kChunk / GROUP, PARTS = F32 ? 3 : 1, F = GROUP / 32;
+    constexpr int PAIRS = KS * G * MT, PER = (PAIRS + kTileWaves - 1) / kTileWaves;     // groups of 16 rows of x: (group in the step, rows)
+    __shared__ bf16x8 xs[2][PAIRS][F][PARTS][64];
+    __shared__ f32x4 sums[2][PAIRS][4];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lr = lane & 15, quarter = lane >> 4;
-    const int64_t mtile = a.first + blockIdx.x / a.otiles, otile = blockIdx.x % a.otiles;
-    const int64_t wrow = (otile * kTileWaves + wave) * 16 + lr;
-    const int64_t row = min(wrow, a.o - 1);
+    const int64_t mtile = a.first + blockIdx.x / a.otiles, otile = (blockIdx.x % a.otiles) * kTileWaves + wave;
+    const WeightRows rows(a, otile, lane);
+    const Widen widen4;
     const int64_t m0 = mtile * 16 * MT;
-    Raw8<F32> x[PER];
-    const auto fetch = [&](int c) {
+    const int steps = (a.chunks + KS - 1) / KS;
+    Raw8<F32> x[PER][F];
+    const auto fetch = [&](int step) {
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int item = wave + j * kTileWaves;
-            const int64_t m = m0 + 16 * (item >> 2) + lr;
-            const int col = c * kChunk + 32 * (item & 3) + 8 * quarter;
-            if (item < ITEMS && m < a.n && col < a.k) x[j].load(a.x, m * a.k + col); else x[j].zero();
+            const int pair = wave + j * kTileWaves;
+            const int64_t m = m0 + 16 * (pair % MT) + lr;
+#pragma unroll
+            for (int f = 0; f < F; ++f) {
+                const int col = step * KS * kChunk + (pair / MT) * GROUP + 32 * f + 8 * quarter;
+                if (pair < PAIRS && m < a.n && col < a.k) x[j][f].load(a.x, m * a.k + col); else x[j][f].zero();
+            }
         }
     };
     const auto put = [&](int buf) {
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-            const int item = wave + j * kTileWaves;
-            if (item >= ITEMS) break;
-            bf16x8 p[PARTS];
-            parts_of<F32>(x[j], p);
+            const int pair = wave + j * kTileWaves;
+            if (pair >= PAIRS) break;
+            float s = 0.0f;
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q) xs[buf][item][q][lane] = p[q];
-            float v[8];
-            x[j].get(v);
-            float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+            for (int f = 0; f < F; ++f) {
+                bf16x8 p[PARTS];
+                parts_of<F32>(x[j][f], p);
+#pragma unroll
+                for (int q = 0; q < PARTS; ++q) xs[buf][pair][f][q][lane] = p[q];
+                float v[8];
+                x[j][f].get(v);
+                s += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+            }
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
-            if (quarter == 0) sums[buf][item][lr] = s;
+            if (quarter == 0) reinterpret_cast<float*>(&sums[buf][pair][0])[lr] = s;
         }
     };
     f32x4 acc[MT];
 #pragma unroll
     for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    Weights<GROUP> w, next;
-    next.load(a, row, 0, quarter);
+    // loads come back in order: x, which is waited for first, is asked for before the weights
+    Weights<GROUP> w[KS], next[KS];
     fetch(0);
+#pragma unroll
+    for (int c = 0; c < KS; ++c) next[c].load(rows, min(c, a.chunks - 1));
     put(0);
     __syncthreads();
-    for (int c = 0; c < a.chunks; ++c) {
-        w = next;
-        if (c + 1 < a.chunks) {
-            next.load(a, row, c + 1, quarter);
-            fetch(c + 1);
+    for (int step = 0; step < steps; ++step) {
+#pragma unroll
+        for (int c = 0; c < KS; ++c) w[c] = next[c];
+        if (step + 1 < steps) {
+            fetch(step + 1);
+#pragma unroll
+            for (int c = 0; c < KS; ++c) next[c].load(rows, min((step + 1) * KS + c, a.chunks - 1));
         }
-        const int buf = c & 1;
-        transpose4(w.w);
+        const int buf = step & 1;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-            bf16x8 b[F];
+        for (int c = 0; c < KS; ++c) {
+            transpose4(w[c].w);
 #pragma unroll
-            for (int f = 0; f < F; ++f) b[f] = widen4(w.w[g * F + f]);
-            // past the last group there may be anything
-            const float s = c * kChunk + g * GROUP < a.k ? w.scale(g, a.sf32) : 0.0f, z = w.start(g);
+            for (int g = 0; g < G; ++g) {
+                bf16x8 b[F];
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-                f32x4 d = *reinterpret_cast<const f32x4*>(&sums[buf][4 * t + g * F][4 * quarter]);
+                for (int f = 0; f < F; ++f) b[f] = widen4(w[c].w[g * F + f]);
+                // past the last group there may be anything
+                const float s = (step * KS + c) * kChunk + g * GROUP < a.k ? w[c].scale(g, a.sf32) : 0.0f, z = w[c].start(g);
 #pragma unroll
-                for (int f = 1; f < F; ++f) d += *reinterpret_cast<const f32x4*>(&sums[buf][4 * t + g * F + f][4 * quarter]);
-                d *= z;
+                for (int t = 0; t < MT; ++t) {
+                    const int pair = (c * G + g) * MT + t;
+                    f32x4 d = sums[buf][pair][quarter] * z;
 #pragma unroll
-                for (int f = 0; f < F; ++f)
+                    for (int f = 0; f < F; ++f)
 #pragma unroll
-                    for (int q = 0; q < PARTS; ++q) d = mfma(xs[buf][4 * t + g * F + f][q][lane], b[f], d);
+                        for (int q = 0; q < PARTS; ++q) d = mfma(xs[buf][pair][f][q][lane], b[f], d);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(s, d[i], acc[t][i]);
+                    for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(s, d[i], acc[t][i]);
+                }
             }
         }
-        if (c + 1 < a.chunks) put(buf ^ 1);
+        if (step + 1 < steps) put(buf ^ 1);
         __syncthreads();
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store_y(a, m0 + 16 * t + 4 * quarter + i, wrow, acc[t][i]);
+        for (int i = 0; i < 4; ++i) store_y(a, m0 + 16 * t + 4 * quarter + i, otile * 16 + lr, acc[t][i]);
 }
 
 template <int MT, int GROUP, bool F32>
-int launch_product(ProductArgs a, bool split, hipStream_t st) {
+int launch_product(ProductArgs a, hipStream_t st) {
+    const bool split = a.o < 128 * 256;
     const int threads = split ? 64 * kSplitWaves : 64 * kTileWaves;
     a.otiles = split ? (a.o + 15) / 16 : (a.o + 16 * kTileWaves - 1) / (16 * kTileWaves);
     const int64_t mtiles = (a.n + 16 * MT - 1) / (16 * MT), most = most_groups(threads) / a.otiles;
     for (a.first = 0; a.first < mtiles; a.first += most) {
         const dim3 grid(static_cast<uint32_t>(std::min(most, mtiles - a.first) * a.otiles));
         if (split) hipLaunchKernelGGL((project_int4_split_kernel<MT, GROUP, F32>), grid, dim3(threads), 0, st, a);
-        else hipLaunchKernelGGL((project_int4_tile_kernel<MT, GROUP, F32>), grid, dim3(threads), 0, st, a);
+        else hipLaunchKernelGGL((project_int4_tile_kernel<MT, GROUP, F32, MT * (F32 ? 2 : 1) >= 4 ? 1 : 2>), grid, dim3(threads), 0, st, a);
     }
     return hip_status("ngram_project_int4");
 }
 
-template <int MT, bool F32>
-int launch_group(const ProductArgs& a, int group, bool split, hipStream_t st) {
-    if (group == 32) return launch_product<MT, 32, F32>(a, split, st);
-    if (group == 64) return launch_product<MT, 64, F32>(a, split, st);
-    return launch_product<MT, 128, F32>(a, split, st);
+template <int MT, int GROUP, bool F32, bool SF32, int PER, int WAVES>
+int launch_rows_of(ProductArgs a, hipStream_t st) {
+    const int waves = (a.chunks + PER - 1) / PER, lds = RowsShape<MT, GROUP, F32, SF32, PER>::bytes(waves);
+    static_assert(RowsShape<MT, GROUP, F32, SF32, PER>::bytes(WAVES) <= 160 * 1024, "LDS");
+    const auto kernel = project_int4_rows_kernel<MT, GROUP, F32, SF32, PER, WAVES>;
+    a.otiles = (a.o + 15) / 16;
+    const int64_t at_once = 256 * std::max(1, std::min(12 / waves, 160 * 1024 / lds));
+    const dim3 grid(static_cast<uint32_t>(std::min(a.otiles, at_once))), block(64 * waves);
+    for (a.first = 0; a.first * 16 * MT < a.n; ++a.first) hipLaunchKernelGGL(kernel, grid, block, lds, st, a);
+    return hip_status("ngram_project_int4");
+}
+template <int MT, int GROUP, bool F32, int PER, int WAVES>
+int launch_rows(const ProductArgs& a, hipStream_t st) {
+    return a.sf32 ? launch_rows_of<MT, GROUP, F32, true, PER, WAVES>(a, st) : launch_rows_of<MT, GROUP, F32, false, PER, WAVES>(a, st);
+}
+
+template <int GROUP, bool F32>
+int launch_group(const ProductArgs& a, hipStream_t st) {
+    if (F32) {
+        if (a.n <= 16 && a.chunks <= 12) return launch_rows<1, GROUP, true, 1, 12>(a, st);
+        if (a.n <= 16 && a.chunks <= 24) return launch_rows<1, GROUP, true, 2, 12>(a, st);
+        return a.n <= 16 ? launch_product<1, GROUP, true>(a, st) : launch_product<2, GROUP, true>(a, st);
+    }
+    if (a.n <= 16) {
+        if (a.chunks <= 12) return launch_rows<1, GROUP, false, 1, 12>(a, st);
+        if (a.chunks <= 24) return launch_rows<1, GROUP, false, 2, 12>(a, st);
+        if (a.chunks <= 48) return launch_rows<1, GROUP, false, 4, 12>(a, st);
+        return launch_product<1, GROUP, false>(a, st);
+    }
+    if (a.n <= 64) {
+        if (a.chunks <= 12) return launch_rows<2, GROUP, false, 1, 12>(a, st);
+        if (a.chunks <= 24) return launch_rows<2, GROUP, false, 2, 12>(a, st);
+    }
+    return a.n <= 32 ? launch_product<2, GROUP, false>(a, st) : launch_product<4, GROUP, false>(a, st);
 }
 
 // A launch for the rows from row0 on; fills magic and shift.
@@ -579,11 +811,12 @@ int ngram_project_int4(const void* x, int32_t x_dtype, int64_t n, const ngram_in
     a.n = n; a.o = W->rows; a.ld = int4_ld(W->cols); a.sld = int4_sld(W->cols, W->group);
     a.k = static_cast<int32_t>(W->cols); a.chunks = static_cast<int32_t>((W->cols + kChunk - 1) / kChunk);
     a.sf32 = W->scale_dtype == NGRAM_F32; a.yf32 = y_dtype == NGRAM_F32;
-    const bool split = W->rows < 128 * 256;
-    if (x_dtype == NGRAM_F32) return n <= 16 ? launch_group<1, true>(a, W->group, split, stream) : launch_group<2, true>(a, W->group, split, stream);
-    if (n <= 16) return launch_group<1, false>(a, W->group, split, stream);
-    if (n <= 32) return launch_group<2, false>(a, W->group, split, stream);
-    return launch_group<4, false>(a, W->group, split, stream);
+    if (x_dtype == NGRAM_F32) {
+        if (W->group == 32) return launch_group<32, true>(a, stream);
+        return W->group == 64 ? launch_group<64, true>(a, stream) : launch_group<128, true>(a, stream);
+    }
+    if (W->group == 32) return launch_group<32, false>(a, stream);
+    return W->group == 64 ? launch_group<64, false>(a, stream) : launch_group<128, false>(a, stream);
 }
 
 }  // extern "C"
