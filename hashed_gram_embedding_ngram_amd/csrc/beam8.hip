@@ -59,6 +59,7 @@ struct StepArgs {
 __device__ __forceinline__ bool alive(const StepArgs& a, int64_t row) { return a.scores[row] > kNegInf; }
 
 constexpr int kScanWaves = 4;
+constexpr int kAhead = 4;           // vectors of a lane at a time
 constexpr int kRoom = 640;          // keys of a wavefront's buffer: below 128 kept plus 512 of one vector
 
 // The `keep` largest keys of buf[0 .. count) to buf[0 .. keep), falling; 0 past
@@ -88,8 +89,9 @@ __device__ __forceinline__ void compress(uint64_t* buf, int count, int keep, int
 // the running maximum and sum of the softmax in each lane, and the `beams`
 // largest logits in a buffer in LDS: an element above the threshold (the
 // smallest kept so far) is appended, and the buffer is cut to the largest when
-// it fills, which raises the threshold.  A wavefront walks upwards, so an
-// element equal to the threshold has a higher token than those kept.
+// it fills, which raises the threshold.  A wavefront's steps go upwards, so an
+// element equal to the threshold has a higher token than those kept; within a step
+// vectors go upwards too.
 template <bool F32>
 __global__ void __launch_bounds__(64 * kScanWaves) beam_scan_kernel(const StepArgs a) {
     constexpr int E = Row<F32>::E;
@@ -107,45 +109,73 @@ __global__ void __launch_bounds__(64 * kScanWaves) beam_scan_kernel(const StepAr
     const int from = list * per * 64, to = min(vectors, from + per * 64);
     Soft soft{kLowest, 0.0f};
     float thr = kNegInf;
+    float low = kNegInf;                // of this step's elements, those below are not among the largest
     int count = 0;
-    for (int i0 = from; i0 < to; i0 += 64) {
-        const int i = i0 + lane;
-        u32x4 raw;
-        float x[E];
-        float top = kNegInf;
-        if (i < to) {
-            raw = r.load(i);
+    constexpr uint32_t kNothing = F32 ? 0xFF800000u : 0xFF80FF80u;
+    u32x4 ahead[kAhead];
+    const auto fetch = [&](int i0) {
 #pragma unroll
-            for (int k = 0; k < E; ++k) {
-                x[k] = Row<F32>::at(raw, k);
-                top = fmaxf(top, x[k]);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < E; ++k) x[k] = kNegInf;
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + 64 * u + lane;
+            ahead[u] = u32x4{kNothing, kNothing, kNothing, kNothing};
+            if (i < to) ahead[u] = r.load(i);
         }
+    };
+    fetch(from);
+    for (int i0 = from; i0 < to; i0 += 64 * kAhead) {
+        u32x4 raw[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) raw[u] = ahead[u];
+        fetch(i0 + 64 * kAhead);
+        float top = kNegInf;
+#pragma unroll
+        for (int k = 0; k < kAhead * E; ++k) top = fmaxf(top, Row<F32>::at(raw[k / E], k % E));
         const float m = fmaxf(soft.m, top);
         soft.s *= exp2_fast((soft.m - m) * c);
         soft.m = m;
+        float e[kAhead * E];
 #pragma unroll
-        for (int k = 0; k < E; ++k) soft.s += exp2_fast((x[k] - m) * c);
+        for (int k = 0; k < kAhead * E; ++k) e[k] = exp2_fast((Row<F32>::at(raw[k / E], k % E) - m) * c);
+#pragma unroll
+        for (int n = kAhead * E / 2; n > 0; n /= 2)
+#pragma unroll
+            for (int k = 0; k < n; ++k) e[k] += e[k + n];
+        soft.s += e[0];
         if (__ballot(top > thr) == 0) continue;
-#pragma unroll
-        for (int k = 0; k < E; ++k) {
-            const uint64_t hit = __ballot(x[k] > thr);
-            if (x[k] > thr) {
-                const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(hit >> 32),
-                                                             __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(hit), 0));
-                buf[count + before] = key_of(x[k], i * E + k);
+        if (thr == kNegInf) {
+            // nothing kept yet: the `beams` largest lane maxima bound the threshold from below
+            float rest = top, t = kNegInf;
+            for (int n = 0; n < a.beams;) {
+                t = wave_max(rest);
+                if (t == kNegInf) break;
+                const uint64_t at = __ballot(rest == t);
+                n += __popcll(at);
+                if (rest == t) rest = kNegInf;
             }
-            count += __popcll(hit);
+            low = t;
         }
-        if (count >= 64) {
-            __builtin_amdgcn_wave_barrier();
-            compress(buf, count, a.beams, lane);
-            count = min(count, a.beams);
-            if (count == a.beams) thr = key_logit(buf[count - 1]);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+            for (int k = 0; k < E; ++k) {
+                const float x = Row<F32>::at(raw[u], k);
+                const bool in = x > thr && x >= low;
+                const uint64_t hit = __ballot(in);
+                if (in) {
+                    const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(hit >> 32),
+                                                                 __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(hit), 0));
+                    buf[count + before] = key_of(x, (i0 + 64 * u + lane) * E + k);
+                }
+                count += __popcll(hit);
+            }
+            if (count >= 64) {
+                __builtin_amdgcn_wave_barrier();
+                compress(buf, count, a.beams, lane);
+                count = min(count, a.beams);
+                if (count == a.beams) thr = key_logit(buf[count - 1]);
+            }
         }
+        low = kNegInf;
     }
     __builtin_amdgcn_wave_barrier();
     compress(buf, count, a.beams, lane);
@@ -161,6 +191,7 @@ __global__ void __launch_bounds__(64 * kScanWaves) beam_scan_kernel(const StepAr
 constexpr int kJoinWaves = 8;
 
 __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(const StepArgs a) {
+    extern __shared__ uint64_t lists[];             // a row's lists, for each wavefront
     __shared__ uint64_t best[NGRAM_MAX_BEAMS][NGRAM_MAX_BEAMS];
     // a candidate's score is score + ((logit - max) - log sum exp(logits - max)), in an order that keeps
     // the differences of huge logits
@@ -170,7 +201,7 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(const StepAr
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row0 = (a.first + blockIdx.x) * a.beams;
-    for (int b = wave; b < a.beams; b += kJoinWaves) {
+    for (int b = wave; b < a.beams; b += static_cast<int>(blockDim.x >> 6)) {
         const int64_t row = row0 + b;
         const double score = a.scores[row];
         const bool fin = a.finished && a.finished[row];
@@ -185,7 +216,9 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(const StepAr
             Soft s{kLowest, 0.0f};
             uint64_t head = 0;
             int taken = 0;
-            const uint64_t* mine = a.keys + (row * a.lists + lane) * a.beams;
+            uint64_t* const room = lists + static_cast<int64_t>(wave) * a.lists * a.beams;
+            const uint64_t* const mine = room + lane * a.beams;
+            for (int i = lane; i < a.lists * a.beams; i += 64) room[i] = a.keys[row * a.lists * a.beams + i];
             if (lane < a.lists) {
                 s = a.soft[row * a.lists + lane];
                 head = mine[0];
@@ -218,48 +251,47 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(const StepAr
     int taken = 0;
     double mine = 0;
     uint64_t head = lane < a.beams ? best[lane][0] : 0;
-    const auto value = [&](uint64_t k) { return score_of[lane] + ((key_logit(k) - max_of[lane]) - log_sum[lane]); };
-    if (head) mine = value(head);
+    // scores in an order that whole numbers keep; 0 for none
+    const auto rank = [&](uint64_t k) -> uint64_t {
+        if (!k) return 0;
+        mine = score_of[lane] + ((key_logit(k) - max_of[lane]) - log_sum[lane]) + 0.0;
+        if (!(mine > -__builtin_inf())) return 0;
+        const uint64_t u = __builtin_bit_cast(uint64_t, mine);
+        return u >> 63 ? ~u : u | (UINT64_C(1) << 63);
+    };
+    uint64_t order = rank(head);
+    int from = -1, token = -1, marked = 0, h0 = -1, h1 = -1;     // lane r: place r
+    float score = kNegInf;
     for (int r = 0; r < a.beams; ++r) {
-        // the largest score, ties to the lowest beam
-        double top = head ? mine : -__builtin_inf();
-        int who = head && mine > -__builtin_inf() ? lane : 64;
-#pragma unroll
-        for (int step = 1; step < 64; step *= 2) {
-            const double other = __shfl_xor(top, step);
-            const int ow = __shfl_xor(who, step);
-            if (other > top || (other == top && ow < who)) {
-                top = other;
-                who = ow;
-            }
-        }
-        const int64_t to = row0 + r;
-        if (who == 64) {
-            if (lane == 0) {
-                a.scores_out[to] = kNegInf;
-                if (a.tokens_out) a.tokens_out[to] = -1;
-                a.parents_out[to] = -1;
-                if (a.finished_out) a.finished_out[to] = 0;
-                if (a.history_out) {
-                    a.history_out[2 * to] = -1;
-                    a.history_out[2 * to + 1] = -1;
-                }
-            }
-            continue;
+        const uint64_t top = wave_max64(order);
+        if (top == 0) break;
+        const int who = __builtin_ctzll(__ballot(order == top));            // ties to the lowest beam
+        const uint64_t k = lane64(head, who);
+        const float s = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(static_cast<float>(mine)), who));
+        if (lane == r) {
+            from = who;
+            token = key_token(k);
+            score = s;
         }
         if (lane == who) {
-            const int token = key_token(head);
-            a.scores_out[to] = static_cast<float>(mine);
-            if (a.tokens_out) a.tokens_out[to] = token;
-            a.parents_out[to] = lane;
-            if (a.finished_out) a.finished_out[to] = done[lane] || token == a.end;
-            if (a.history_out) {
-                a.history_out[2 * to] = last[lane][0];
-                a.history_out[2 * to + 1] = last[lane][1];
-            }
             head = ++taken < a.beams ? best[lane][taken] : 0;
-            if (head) mine = value(head);
+            order = rank(head);
         }
+    }
+    if (lane >= a.beams) return;
+    const int64_t to = row0 + lane;
+    if (from >= 0) {
+        marked = done[from] || token == a.end;
+        h0 = last[from][0];
+        h1 = last[from][1];
+    }
+    a.scores_out[to] = score;
+    if (a.tokens_out) a.tokens_out[to] = token;
+    a.parents_out[to] = from;
+    if (a.finished_out) a.finished_out[to] = static_cast<uint8_t>(marked);
+    if (a.history_out) {
+        a.history_out[2 * to] = h0;
+        a.history_out[2 * to + 1] = h1;
     }
 }
 
@@ -293,16 +325,16 @@ struct ReorderArgs {
 };
 
 template <int B, typename T>
-__device__ __forceinline__ void reorder_columns(const ReorderArgs& a, char* base, int64_t stride, int64_t columns, int64_t col, const int* parent) {
-    if (col >= columns) return;
-    char* const p = base + col * static_cast<int64_t>(sizeof(T));
+__device__ __forceinline__ void reorder_columns(char* base, int64_t stride, bool on, const int* parent) {
+    const uint32_t at = threadIdx.x * static_cast<uint32_t>(sizeof(T));
     T v[B];
+    if (!on) return;
 #pragma unroll
     for (int b = 0; b < B; ++b)
-        if (parent[b] >= 0) v[b] = *reinterpret_cast<const T*>(p + parent[b] * stride);
+        if (parent[b] >= 0) v[b] = *reinterpret_cast<const T*>(base + parent[b] * stride + at);
 #pragma unroll
     for (int b = 0; b < B; ++b)
-        if (parent[b] >= 0) *reinterpret_cast<T*>(p + b * stride) = v[b];
+        if (parent[b] >= 0) *reinterpret_cast<T*>(base + b * stride + at) = v[b];
 }
 
 inline __host__ __device__ int unit_of(const ngram_beam_state& s) {
@@ -317,22 +349,24 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(const ReorderArgs a) 
     while (s + 1 < a.count && wg >= a.start[s + 1]) ++s;
     const ngram_beam_state st = a.state[s];
     const int unit = unit_of(st);
-    const int64_t columns = st.row_bytes / unit, blocks = (columns + 255) / 256;
-    const int64_t at = wg - a.start[s], seq = at / blocks, col = at % blocks * 256 + threadIdx.x;
-    // the parent of each row that changes, or -1
+    const int64_t columns = st.row_bytes / unit;
+    const uint32_t blocks = static_cast<uint32_t>((columns + 255) / 256), at = static_cast<uint32_t>(wg - a.start[s]);
+    const uint32_t seq = at / blocks, block = at - seq * blocks;
+    // the parent of each row that changes, or -1; addresses are uniform but for the thread's distance
     int parent[B];
 #pragma unroll
     for (int b = 0; b < B; ++b) {
         parent[b] = -1;
         if (b < a.beams) {
-            const int p = a.parents[seq * a.beams + b];
+            const int p = __builtin_amdgcn_readfirstlane(a.parents[static_cast<int64_t>(seq) * a.beams + b]);
             if (p >= 0 && p < a.beams && p != b) parent[b] = p;
         }
     }
-    char* const base = static_cast<char*>(st.data) + seq * a.beams * st.stride;
-    if (unit == 16) reorder_columns<B, u32x4>(a, base, st.stride, columns, col, parent);
-    else if (unit == 4) reorder_columns<B, uint32_t>(a, base, st.stride, columns, col, parent);
-    else reorder_columns<B, uint8_t>(a, base, st.stride, columns, col, parent);
+    char* const base = static_cast<char*>(st.data) + static_cast<int64_t>(seq) * a.beams * st.stride + static_cast<int64_t>(block) * 256 * unit;
+    const bool on = static_cast<int64_t>(block) * 256 + threadIdx.x < columns;
+    if (unit == 16) reorder_columns<B, u32x4>(base, st.stride, on, parent);
+    else if (unit == 4) reorder_columns<B, uint32_t>(base, st.stride, on, parent);
+    else reorder_columns<B, uint8_t>(base, st.stride, on, parent);
 }
 
 }  // namespace
@@ -385,9 +419,10 @@ int ngram_beam_step(const void* logits, int32_t dtype, int64_t batch, int32_t be
         if (dtype == NGRAM_F32) hipLaunchKernelGGL(beam_scan_kernel<true>, grid, dim3(64 * kScanWaves), 0, stream, a);
         else hipLaunchKernelGGL(beam_scan_kernel<false>, grid, dim3(64 * kScanWaves), 0, stream, a);
     }
-    for (a.first = 0; a.first < batch; a.first += most_groups(64 * kJoinWaves))
-        hipLaunchKernelGGL(beam_join_kernel, dim3(static_cast<uint32_t>(std::min(most_groups(64 * kJoinWaves), batch - a.first))),
-                           dim3(64 * kJoinWaves), 0, stream, a);
+    const int waves = std::min(beams, kJoinWaves), room = waves * a.lists * beams * 8;
+    for (a.first = 0; a.first < batch; a.first += most_groups(64 * waves))
+        hipLaunchKernelGGL(beam_join_kernel, dim3(static_cast<uint32_t>(std::min(most_groups(64 * waves), batch - a.first))),
+                           dim3(64 * waves), room, stream, a);
     return hip_status("ngram_beam_step");
 }
 
@@ -402,7 +437,9 @@ int ngram_beam_reorder(const ngram_beam_state* states, int32_t count, const int3
         const ngram_beam_state& s = states[i];
         if (s.row_bytes < 0 || s.stride < s.row_bytes)
             return fail(NGRAM_EINVAL, "state %d: row_bytes=%lld must not be negative nor above stride=%lld", i, (long long)s.row_bytes, (long long)s.stride);
-        if (s.row_bytes > (INT64_C(1) << 40)) return fail(NGRAM_ERANGE, "state %d: row_bytes=%lld above 2^40", i, (long long)s.row_bytes);
+        // a state's workgroups are counted in 32 bits
+        if (s.row_bytes > (INT64_C(1) << 40) || (s.row_bytes / unit_of(s) / 256 + 1) * std::max<int64_t>(batch, 1) > INT64_C(0x7FFFFFFF))
+            return fail(NGRAM_ERANGE, "state %d: row_bytes=%lld for %lld sequences is out of range", i, (long long)s.row_bytes, (long long)batch);
         if (s.row_bytes > 0 && batch > 0 && !s.data) return fail(NGRAM_EINVAL, "state %d: data is NULL", i);
     }
     if (batch == 0 || count == 0) return NGRAM_OK;
@@ -424,7 +461,6 @@ int ngram_beam_reorder(const ngram_beam_state* states, int32_t count, const int3
         for (a.first = 0; a.first < total; a.first += most_groups(256)) {
             const dim3 grid(static_cast<uint32_t>(std::min(most_groups(256), total - a.first))), block(256);
             if (beams <= 4) hipLaunchKernelGGL(beam_reorder_kernel<4>, grid, block, 0, stream, a);
-            else if (beams <= 8) hipLaunchKernelGGL(beam_reorder_kernel<8>, grid, block, 0, stream, a);
             else if (beams <= 16) hipLaunchKernelGGL(beam_reorder_kernel<16>, grid, block, 0, stream, a);
             else hipLaunchKernelGGL(beam_reorder_kernel<32>, grid, block, 0, stream, a);
         }
