@@ -74,7 +74,7 @@ template <bool F32, bool ASYM>
 __global__ void __launch_bounds__(256) quant_int4_kernel(const QuantArgs a) {
     const uint32_t t = blockIdx.x * 256 + threadIdx.x;
     const bool on = t < a.count;                            // whole groups are on or off
-    const uint32_t r = on ? div_units(a, t) : 0, u = on ? t - r * a.units : 0;
+    const uint32_t r = div_units(a, t), u = t - r * a.units;
     const int64_t row = a.row0 + r;
     const int col = static_cast<int>(u) * kVec;
     Raw8<F32> raw;
@@ -103,12 +103,37 @@ __global__ void __launch_bounds__(256) quant_int4_kernel(const QuantArgs a) {
     if (s == 0.0f) s = 1.0f;
     float z = 8.0f;
     if (ASYM) z = fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f);
-    uint32_t code = 0;
+    // w / s correctly rounded from y = 1 / s, which is: a product, and twice the remainder times y.  The first
+    // makes the quotient one of the two fp32 numbers around the true one, and from such a one and a correctly
+    // rounded y the second gives the nearest (Markstein's theorem).  A division for each of 151936 x 2560
+    // weights takes 325 us, this way 255.  (Dividing only
+    // where a quotient lies near a half saves nothing: bf16 weights over bf16 scales lie on halves often.)
+    const float y = 1.0f / s;
+    float q[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float q = fminf(fmaxf(rintf(w[k] / s) + z, 0.0f), 15.0f);
-        code |= static_cast<uint32_t>(q) << (4 * k);
+        float v = w[k] * y;
+        v = __builtin_fmaf(__builtin_fmaf(-v, s, w[k]), y, v);
+        v = __builtin_fmaf(__builtin_fmaf(-v, s, w[k]), y, v);
+        q[k] = rintf(v);
     }
+    if (__builtin_expect(__ballot(!(s > 0x1p-100f && s < 0x1p100f)) != 0, 0)) {     // where 1 / s or a remainder leaves the range
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = rintf(w[k] / s);
+    }
+    // four codes in a whole number below 2^16, Horner's way, the zero added to all of them at once
+    float half[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+            const float c = __builtin_amdgcn_fmed3f(q[4 * h + k], -z, 15.0f - z);
+            v = k == 3 ? c : __builtin_fmaf(v, 16.0f, c);
+        }
+        half[h] = __builtin_fmaf(z, 4369.0f, v);
+    }
+    uint32_t code = static_cast<uint32_t>(half[0]) | static_cast<uint32_t>(half[1]) << 16;
     if (nan) {
         s = __uint_as_float(0x7FC00000u);
         z = 8.0f;
@@ -412,7 +437,7 @@ __global__ void __launch_bounds__(64 * kSplitWaves) project_int4_split_kernel(co
 // sums are joined in LDS, in a fixed order, by MT of the wavefronts in turn.
 //
 // Each wavefront brings its own codes, scales and zeros into LDS, SLOTS - 1
-// tiles ahead, so that nothing but its own loads is waited for.  Through LDS
+// tiles ahead, so that its products wait for nothing but its own loads.  Through LDS
 // because the matrix operand wants neighbouring lanes in different rows, and a load whose
 // neighbouring lanes lie in different rows takes four times as long: here four
 // lanes read the 64 bytes of a row.  A row's four parts lie rotated by half its
@@ -510,46 +535,62 @@ __global__ void __launch_bounds__(64 * WAVES) project_int4_rows_kernel(const Pro
                     sx[c][g][t] = s;
                 }
     }
+    const int64_t step = static_cast<int64_t>(gridDim.x);
     int64_t tile = blockIdx.x;
 #pragma unroll
-    for (int h = 0; h + 1 < SLOTS; ++h) load(tile + h * static_cast<int64_t>(gridDim.x), h);
+    for (int h = 0; h < SLOTS - 1; ++h)
+        if (tile + h * step < a.otiles) load(tile + h * step, h);
     int slot = 0, turn = 0;
-    for (; tile < a.otiles; tile += gridDim.x, ++turn) {
-        // the reads of the slot's tile before last ended with their products; zeros' loads may be missing from the count
-        load(tile + (SLOTS - 1) * static_cast<int64_t>(gridDim.x), (slot + SLOTS - 1) % SLOTS);
-        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"i"((SLOTS - 1) * (PER + S::SL)) : "memory");
-        const uint8_t* const from = mine + slot * S::Slot;
+    for (; tile < a.otiles; tile += step, ++turn) {
         f32x4 acc[MT];
+        {
+            // into the slot whose reads ended with the last tile's products; loads of zeros may be missing from the count
+            if (tile + (SLOTS - 1) * step < a.otiles) {
+                load(tile + (SLOTS - 1) * step, (slot + SLOTS - 1) % SLOTS);
+                __asm__ volatile("s_waitcnt vmcnt(%0)" ::"i"((SLOTS - 1) * (PER + S::SL)) : "memory");
+            } else {
+                __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
+            const uint8_t* const from = mine + slot * S::Slot;
+            // this lane's scales and zeros; one alone in its word is moved to the word's start
+            constexpr int SB = PER * G * (SF32 ? 4 : 2), ZB = PER * G;
+            uint32_t sw[S::SD], zw[S::ZD];
 #pragma unroll
-        for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        const uint8_t* const sp = from + PER * 1024 + lr * S::SD * 4 + (PER * G * (SF32 ? 4 : 2) < 4 ? (c0 * G * (SF32 ? 4 : 2)) & 3 : 0);
-        const uint8_t* const zp = from + PER * 1024 + S::SL * 256 + lr * S::ZD * 4 + (PER * G < 4 ? (c0 * G) & 3 : 0);
+            for (int i = 0; i < S::SD; ++i) sw[i] = reinterpret_cast<const uint32_t*>(from + PER * 1024 + lr * S::SD * 4)[i];
 #pragma unroll
-        for (int c = 0; c < PER; ++c) {
-            u32x4 w = *reinterpret_cast<const u32x4*>(from + c * 1024 + lr * 64 + 16 * (quarter ^ ((lr >> 1) & 3)));
-            transpose4(w);
+            for (int i = 0; i < S::ZD; ++i)
+                zw[i] = a.zeros ? reinterpret_cast<const uint32_t*>(from + PER * 1024 + S::SL * 256 + lr * S::ZD * 4)[i] : 0x08080808u;
+            if (SB < 4) sw[0] >>= 8 * ((c0 * G * (SF32 ? 4 : 2)) & 3);
+            if (ZB < 4) zw[0] >>= 8 * ((c0 * G) & 3);
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const int i = c * G + g;
-                const float sv = SF32 ? *reinterpret_cast<const float*>(sp + 4 * i)
-                                      : __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(sp + 2 * i)) << 16);
-                const float z = -16.0f - (a.zeros ? static_cast<float>(zp[i]) : 8.0f);
-                bf16x8 b[F];
+            for (int t = 0; t < MT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int f = 0; f < F; ++f) b[f] = widen4(w[g * F + f]);
-                // past the last group there may be anything
-                const float s = (c0 + c) * kChunk + g * GROUP < a.k ? sv : 0.0f;
+            for (int c = 0; c < PER; ++c) {
+                u32x4 w = *reinterpret_cast<const u32x4*>(from + c * 1024 + lr * 64 + 16 * (quarter ^ ((lr >> 1) & 3)));
+                transpose4(w);
 #pragma unroll
-                for (int t = 0; t < MT; ++t) {
-                    f32x4 d = sx[c][g][t] * z;
+                for (int g = 0; g < G; ++g) {
+                    const int i = c * G + g;
+                    const float sv = __uint_as_float(SF32 ? sw[SF32 ? i : 0] : i & 1 ? sw[i >> 1] & 0xFFFF0000u : sw[i >> 1] << 16);
+                    const float z = -16.0f - static_cast<float>((zw[i >> 2] >> (8 * (i & 3))) & 255);
+                    bf16x8 b[F];
 #pragma unroll
-                    for (int f = 0; f < F; ++f)
+                    for (int f = 0; f < F; ++f) b[f] = widen4(w[g * F + f]);
+                    // past the last group there may be anything
+                    const float s = (c0 + c) * kChunk + g * GROUP < a.k ? sv : 0.0f;
 #pragma unroll
-                        for (int q = 0; q < PARTS; ++q) d = mfma(x[c][t][g * F + f][q], b[f], d);
+                    for (int t = 0; t < MT; ++t) {
+                        f32x4 d = sx[c][g][t] * z;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(s, d[e], acc[t][e]);
+                        for (int f = 0; f < F; ++f)
+#pragma unroll
+                            for (int q = 0; q < PARTS; ++q) d = mfma(x[c][t][g * F + f][q], b[f], d);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[t][e] = __builtin_fmaf(s, d[e], acc[t][e]);
+                    }
                 }
             }
+            slot = slot + 1 == SLOTS ? 0 : slot + 1;
         }
         f32x4* const sum = reinterpret_cast<f32x4*>(part + (turn & 1) * waves * S::Part);
 #pragma unroll
@@ -559,11 +600,10 @@ __global__ void __launch_bounds__(64 * WAVES) project_int4_rows_kernel(const Pro
         for (int t = 0; t < MT; ++t) {
             if ((turn * MT + t) % waves != wave) continue;
             f32x4 v = sum[t * 64 + lane];
-            for (int h = 1; h < waves; ++h) v += sum[(h * MT + t) * 64 + lane];
+            for (int i = 1; i < waves; ++i) v += sum[(i * MT + t) * 64 + lane];
 #pragma unroll
             for (int e = 0; e < 4; ++e) store_y(a, m0 + 16 * t + 4 * quarter + e, tile * 16 + lr, v[e]);
         }
-        slot = slot + 1 == SLOTS ? 0 : slot + 1;
     }
     __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");            // loads into LDS end before the workgroup does
 }
@@ -690,7 +730,7 @@ int launch_product(ProductArgs a, hipStream_t st) {
 template <int MT, int GROUP, bool F32, bool SF32, int PER, int WAVES>
 int launch_rows_of(ProductArgs a, hipStream_t st) {
     const int waves = (a.chunks + PER - 1) / PER, lds = RowsShape<MT, GROUP, F32, SF32, PER>::bytes(waves);
-    static_assert(RowsShape<MT, GROUP, F32, SF32, PER>::bytes(WAVES) <= 160 * 1024, "LDS");
+    if (lds > 160 * 1024) return 1;             // the caller takes another kernel
     const auto kernel = project_int4_rows_kernel<MT, GROUP, F32, SF32, PER, WAVES>;
     a.otiles = (a.o + 15) / 16;
     const int64_t at_once = 256 * std::max(1, std::min(12 / waves, 160 * 1024 / lds));
@@ -705,22 +745,18 @@ int launch_rows(const ProductArgs& a, hipStream_t st) {
 
 template <int GROUP, bool F32>
 int launch_group(const ProductArgs& a, hipStream_t st) {
-    if (F32) {
-        if (a.n <= 16 && a.chunks <= 12) return launch_rows<1, GROUP, true, 1, 12>(a, st);
-        if (a.n <= 16 && a.chunks <= 24) return launch_rows<1, GROUP, true, 2, 12>(a, st);
-        return a.n <= 16 ? launch_product<1, GROUP, true>(a, st) : launch_product<2, GROUP, true>(a, st);
-    }
+    int rc = 1;
     if (a.n <= 16) {
-        if (a.chunks <= 12) return launch_rows<1, GROUP, false, 1, 12>(a, st);
-        if (a.chunks <= 24) return launch_rows<1, GROUP, false, 2, 12>(a, st);
-        if (a.chunks <= 48) return launch_rows<1, GROUP, false, 4, 12>(a, st);
-        return launch_product<1, GROUP, false>(a, st);
+        if (a.chunks <= 12) rc = launch_rows<1, GROUP, F32, 1, 12>(a, st);
+        else if (a.chunks <= 24) rc = launch_rows<1, GROUP, F32, 2, 12>(a, st);
+        else if (!F32 && a.chunks <= 48) rc = launch_rows<1, GROUP, false, 4, 12>(a, st);
+    } else if (!F32 && a.n <= 64) {
+        if (a.chunks <= 12) rc = launch_rows<2, GROUP, false, 1, 12>(a, st);
+        else if (a.chunks <= 24) rc = launch_rows<2, GROUP, false, 2, 12>(a, st);
     }
-    if (a.n <= 64) {
-        if (a.chunks <= 12) return launch_rows<2, GROUP, false, 1, 12>(a, st);
-        if (a.chunks <= 24) return launch_rows<2, GROUP, false, 2, 12>(a, st);
-    }
-    return a.n <= 32 ? launch_product<2, GROUP, false>(a, st) : launch_product<4, GROUP, false>(a, st);
+    if (rc != 1) return rc;
+    if (a.n <= 16) return launch_product<1, GROUP, F32>(a, st);
+    return F32 || a.n <= 32 ? launch_product<2, GROUP, F32>(a, st) : launch_product<F32 ? 2 : 4, GROUP, F32>(a, st);
 }
 
 // A launch for the rows from row0 on; fills magic and shift.
@@ -732,7 +768,7 @@ int in_rows(QuantArgs a, int64_t rows, L launch, const char* what) {
         a.magic = 0x80000000u;
         a.shift -= 1;
     }
-    const int64_t most = INT64_C(0x7FFFFF00) / a.units;
+    const int64_t most = INT64_C(0x7FFF0000) / a.units;
     for (int64_t r = 0; r < rows; r += most) {
         a.row0 = r;
         a.count = static_cast<uint32_t>(std::min(most, rows - r) * a.units);
