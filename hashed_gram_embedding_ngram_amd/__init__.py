@@ -1046,6 +1046,12 @@ def _here(stream, *tensors):
         raise NgramError(f"a stream of cuda:{stream.device_index} in a call on cuda:{d}")
 
 
+def _one_device(*tensors):
+    """Refuse tensors that are meant to be used together but lie on several devices."""
+    if len({t.get_device() for t in tensors if t is not None}) > 1:
+        raise NgramError("the tensors lie on several devices")
+
+
 def _rows_arg(t, dtypes, name):
     """(pointer, rows, columns, distance of rows in elements) of a device matrix whose rows are contiguous."""
     n, v = _matrix(t, name)
@@ -1071,6 +1077,7 @@ class Int4:
         ld, sld = _int4_shape(rows, cols, group)
         self.rows, self.cols, self.group = rows, cols, group
         self.codes, self.scales, self.zeros = codes, scales, zeros
+        _one_device(codes, scales, zeros)
         self.c = _Int4(_arg(codes, (torch.uint8,), rows * ld, "codes"), _arg(scales, _VALUES, rows * sld, "scales"),
                        _opt(zeros, (torch.uint8,), rows * sld, "zeros"), rows, cols, group, _value(scales))
 
@@ -1079,9 +1086,20 @@ class Int4:
               stream=None) -> "Int4":
         if torch.device(device).type != "cuda":
             raise NgramError(f"a 4-bit matrix lies on a GPU, not on device {device}")
+        if scale_dtype not in (torch.float32, torch.bfloat16):
+            raise NgramError(f"scales are fp32 or bf16, not {scale_dtype}")
+        return cls._empty(rows, cols, group, zeros, scale_dtype, device, stream)
+
+    @classmethod
+    def _empty(cls, rows, cols, group, zeros, scale_dtype, device, stream):
         ld, sld = _int4_shape(rows, cols, group)
-        return cls(_new(rows, ld, torch.uint8, device, stream), _new(rows, sld, scale_dtype, device, stream), rows, cols, group,
-                   _new(rows, sld, torch.uint8, device, stream) if zeros else None)
+        self = cls.__new__(cls)
+        self.rows, self.cols, self.group = rows, cols, group
+        self.codes, self.scales = _new(rows, ld, torch.uint8, device, stream), _new(rows, sld, scale_dtype, device, stream)
+        self.zeros = _new(rows, sld, torch.uint8, device, stream) if zeros else None
+        self.c = _Int4(self.codes.data_ptr(), self.scales.data_ptr(), self.zeros.data_ptr() if zeros else None, rows, cols, group,
+                       _value(self.scales))
+        return self
 
 
 def _int4_shape(rows, cols, group):
@@ -1096,10 +1114,13 @@ def ngram_quant_int4(x, group: int = 128, zeros: bool = True, scale_dtype=torch.
     and scales' type then count."""
     n, d = _matrix(x, "x")
     px = _arg(x, _VALUES, n * d, "x")
-    _here(stream, x)
     if out is None:
-        out = Int4.empty(n, d, group, zeros, scale_dtype, x.device, stream)
-    _here(stream, out.codes, out.scales, out.zeros)
+        _here(stream, x)
+        if scale_dtype not in (torch.float32, torch.bfloat16):
+            raise NgramError(f"scales are fp32 or bf16, not {scale_dtype}")
+        out = Int4._empty(n, d, group, zeros, scale_dtype, x.device, stream)
+    else:
+        _here(stream, x, out.codes)
     rc = lib().ngram_quant_int4(px, _value(x), n, d, out.c, _raw_stream(stream))
     if rc:
         _check(rc, "ngram_quant_int4")
@@ -1108,7 +1129,7 @@ def ngram_quant_int4(x, group: int = 128, zeros: bool = True, scale_dtype=torch.
 
 def ngram_dequant_int4(q: Int4, out=None, dtype=torch.float32, stream=None):
     """The values of q, [q.rows][q.cols] fp32 or bf16 (see ngram_dequant_int4 in ngram.h)."""
-    _here(stream, q.codes, q.scales, q.zeros, out)
+    _here(stream, q.codes, out)
     if out is None:
         out = _new(q.rows, q.cols, dtype, q.codes.device, stream)
     rc = lib().ngram_dequant_int4(q.c, _arg(out, _VALUES, q.rows * q.cols, "out"), _value(out), _raw_stream(stream))
@@ -1191,6 +1212,7 @@ class BeamStates:
         if any(t.dim() == 0 for t in self.tensors) or len(rows) > 1:
             raise NgramError("every state must have the same rows as its first dimension")
         self.rows = rows.pop() if rows else 0
+        _one_device(*self.tensors)
         c = []
         for i, t in enumerate(self.tensors):
             if not t.is_cuda:

@@ -599,7 +599,8 @@ int check_args(const ngram_distill_args* p) {
     if (p->k > NGRAM_DISTILL_MAX_K || p->V < 1 || p->V > NGRAM_FP8_MAX || p->n > NGRAM_FP8_MAX)
         return fail(NGRAM_ERANGE, "k=%d (to %d), V=%lld or n=%lld (to 2^30) out of range", p->k, NGRAM_DISTILL_MAX_K, (long long)p->V, (long long)p->n);
     if (p->ld < p->V) return fail(NGRAM_EINVAL, "ld=%lld is below V=%lld", (long long)p->ld, (long long)p->V);
-    if (!(p->temperature > 0.0f) || std::isinf(p->temperature)) return fail(NGRAM_EINVAL, "temperature=%g must be positive and finite", p->temperature);
+    if (!(p->temperature >= 0x1p-120f) || std::isinf(p->temperature))
+        return fail(NGRAM_EINVAL, "temperature=%g must be finite and at least 2^-120", p->temperature);
     if (p->n == 0) return NGRAM_OK;
     if (!p->logits || !p->teacher || !p->ids) return fail(NGRAM_EINVAL, "logits, teacher or ids is NULL");
     const uintptr_t ze = p->dtype == NGRAM_F32 ? 4 : 2, te = p->teacher_dtype == NGRAM_F32 ? 4 : 2;

@@ -707,8 +707,8 @@ int ngram_beam_reorder(const ngram_beam_state* states, int32_t count, const int3
  * weight[i] * scale * dloss/dz (weight NULL: 1), for a loss that is the sum of
  * weight[i] * scale * loss[i]; a row with weight * scale 0 gets zeros, whatever its logits hold.
  * z: any distance ld >= V elements between rows, element-aligned; t [n][k]
- * and z have types of their own; weight, teacher_lse [n] fp32.  T positive and
- * finite.  workspace: device, 16-byte aligned, ngram_distill_workspace_bytes bytes; calls that can overlap need one each. */
+ * and z have types of their own; weight, teacher_lse [n] fp32.  T finite, at
+ * least 2^-120.  workspace: device, 16-byte aligned, ngram_distill_workspace_bytes bytes; calls that can overlap need one each. */
 #define NGRAM_DISTILL_MAX_K 1024
 
 typedef struct {

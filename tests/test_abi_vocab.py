@@ -100,7 +100,7 @@ def test_beam_reorder_refuses(kw, code):
 BAD_DISTILL = [
     (dict(n=-1), EINVAL), (dict(k=0), EINVAL), (dict(k=1025), ERANGE), (dict(V=0, ld=0), ERANGE), (dict(V=(1 << 30) + 1, ld=1 << 31), ERANGE),
     (dict(ld=99), EINVAL), (dict(dtype=2), EINVAL), (dict(tdtype=-1), EINVAL), (dict(T=0.0), EINVAL), (dict(T=-1.0), EINVAL),
-    (dict(T=NAN), EINVAL), (dict(T=INF), EINVAL), (dict(z=None), EINVAL), (dict(t=None), EINVAL), (dict(ids=None), EINVAL),
+    (dict(T=NAN), EINVAL), (dict(T=INF), EINVAL), (dict(T=1e-40), EINVAL), (dict(z=None), EINVAL), (dict(t=None), EINVAL), (dict(ids=None), EINVAL),
     (dict(z=A + 1), EALIGN), (dict(z=A + 2, dtype=0), EALIGN), (dict(t=A + 1), EALIGN), (dict(ids=A + 2), EALIGN), (dict(lse=A + 2), EALIGN),
 ]
 
@@ -204,6 +204,10 @@ STREAM1 = type("S", (), {"device_index": 1, "cuda_stream": 0})()
     (lambda: ng.ngram_project_int4(Dev(torch.zeros(4, 64), device=1), w4()), "current"),
     (lambda: ng.ngram_project_int4(f32(4, 64), w4(), stream=STREAM1), "stream of cuda:1"),
     (lambda: ng.Int4(Dev(torch.zeros(4, dtype=torch.uint8)), f32(64), 16, 64), "codes"),
+    (lambda: ng.Int4(Dev(torch.zeros((16, 32), dtype=torch.uint8)), Dev(torch.zeros((16, 4)), device=1), 16, 64, 64), "several devices"),
+    (lambda: ng.Int4.empty(4, 64, scale_dtype=torch.float16), "fp32 or bf16"),
+    (lambda: ng.ngram_quant_int4(f32(4, 64), scale_dtype=torch.float16), "fp32 or bf16"),
+    (lambda: ng.BeamStates([f32(8, 3), Dev(torch.zeros(8, 3), device=1)]), "several devices"),
     (lambda: ng.Int4.empty(4, 12), "no 4-bit matrix"), (lambda: ng.Int4.empty(4, 64, 48), "no 4-bit matrix"),
     (lambda: ng.Int4.empty(4, 64, device="cpu"), "lies on a GPU"),
     (lambda: ng.ngram_quant_int4(f32(4, 5, 6)), "two dimensions"),
@@ -224,7 +228,7 @@ STREAM1 = type("S", (), {"device_index": 1, "cuda_stream": 0})()
     (lambda: ng.ngram_distill(f32(4, 50), f32(4, 3), i32(4, 3), teacher_lse=f32(3)), "teacher_lse"),
     (lambda: ng.ngram_distill(f32(4, 50), f32(4, 3), i32(4, 3), weight=OTHER), "current"),
     (lambda: ng.ngram_distill_grad(f32(4, 50), f32(4, 3), i32(4, 3), f32(4)), "stats"),
-], ids=range(27))
+], ids=range(31))
 def test_binding_refuses(call, match, no_launch):
     with pytest.raises(ng.NgramError, match=match):
         call()

@@ -49,7 +49,7 @@ def check(a, out, beams, end, least_gap=True):
 
 
 SHAPES = [(1, 1, 1), (1, 1, 1000), (1, 2, 1), (3, 4, 3), (2, 5, 2), (2, 4, 50257), (1, 4, 151936), (5, 3, 4099), (1, 32, 700), (40, 8, 1003),
-          (3, 32, 8193), (2, 7, 20001), (300, 4, 513)]
+          (3, 32, 8193), (2, 7, 20001), (300, 4, 513), (1, 32, 151936), (1, 17, 70001)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])

@@ -59,7 +59,7 @@ def check(x, w, values, scales, group, ydtype):
 
 
 SHAPES = [(1, 8, 1), (1, 2560, 2560), (2, 40, 300), (3, 136, 37), (16, 1032, 4103), (17, 264, 130), (31, 648, 16), (33, 128, 517), (64, 2568, 520),
-          (65, 40, 7), (100, 1160, 33)]
+          (65, 40, 7), (100, 1160, 33), (7, 4232, 70), (16, 6144, 17), (3, 6152, 40), (30, 3000, 40), (20, 8192, 264), (60, 1536, 100), (2, 16392, 9)]
 
 
 @pytest.mark.parametrize("kind", range(len(KINDS)))
@@ -76,7 +76,8 @@ def test_product(n, k, o, kind):
         assert np.linalg.norm(err) <= 4e-6 * np.linalg.norm(want)
 
 
-@pytest.mark.parametrize("n,k,o", [(1, 264, 33000), (5, 8, 33000), (20, 136, 32900), (40, 392, 33001), (70, 136, 32770), (4, 1032, 40001)])
+@pytest.mark.parametrize("n,k,o", [(1, 264, 33000), (5, 8, 33000), (20, 136, 32900), (40, 392, 33001), (70, 136, 32770), (4, 1032, 40001), (2, 6200, 33000),
+                                   (40, 4104, 32801), (33, 2600, 32790), (9, 3208, 33333)])
 def test_many_weight_rows(n, k, o):
     for kind in (0, 2, 5):
         group, zeros, xt, st, yt = KINDS[kind]
@@ -208,3 +209,18 @@ def test_reused_buffers_and_a_given_stream():
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(again.codes, plain.codes) and torch.equal(again.zeros, plain.zeros)
     assert torch.equal(y, ng.ngram_project_int4(x, plain, dtype=F32))
+
+
+def test_quotients_are_those_of_a_division():
+    """33 million fp32 weights in groups of every spread, and bf16 ones, whose quotients lie on halves often: the codes that
+    correctly rounded divisions give."""
+    say("4-bit quotients")
+    g = torch.Generator(device=DEV).manual_seed(1)
+    for dtype in (F32, BF):
+        x = (torch.randn((4096, 8192), generator=g, device=DEV) * torch.exp2(torch.randint(-90, 90, (4096, 1), generator=g, device=DEV).float())).to(dtype)
+        for st in (F32, BF):
+            got = ng.ngram_quant_int4(x, 32, zeros=True, scale_dtype=st)
+            s, z = got.scales.float()[:, :, None], got.zeros.float()[:, :, None]
+            want = (torch.round(x.float().view(4096, 256, 32) / s) + z).clamp(0, 15).to(torch.uint8).view(4096, -1)
+            codes = torch.stack((got.codes & 15, got.codes >> 4), dim=2).view(4096, -1)
+            assert torch.equal(codes, want)
