@@ -20,20 +20,90 @@ __device__ __forceinline__ float key_logit(uint64_t k) {
 }
 __device__ __forceinline__ int key_token(uint64_t k) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(k)); }
 
-template <int CTRL>
-__device__ __forceinline__ uint64_t dpp64(uint64_t x) {
-    return static_cast<uint64_t>(dpp<CTRL>(static_cast<uint32_t>(x >> 32))) << 32 | dpp<CTRL>(static_cast<uint32_t>(x));
+// The value of lane ^ X.  Within 16 lanes by lane moves; 16 and 32 by the
+// exchange of rows, whose two results hold each pair's even and odd row.
+template <int X>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t x) {
+    if constexpr (X == 1) return dpp<0xB1>(x);
+    else if constexpr (X == 2) return dpp<0x4E>(x);
+    else if constexpr (X == 3) return dpp<0x1B>(x);
+    else if constexpr (X == 7) return dpp<0x141>(x);
+    else if constexpr (X == 8) return dpp<0x128>(x);
+    else if constexpr (X == 15) return dpp<0x140>(x);
+    else if constexpr (X == 4) return lane_xor<3>(lane_xor<7>(x));
+    else if constexpr (X == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        return threadIdx.x & 16 ? r[0] : r[1];
+    } else if constexpr (X == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        return threadIdx.x & 32 ? r[0] : r[1];
+    } else if constexpr (X == 31) return lane_xor<16>(lane_xor<15>(x));
+    else return lane_xor<32>(lane_xor<31>(x));          // 63
+}
+template <int X>
+__device__ __forceinline__ uint64_t lane_xor64(uint64_t x) {
+    return static_cast<uint64_t>(lane_xor<X>(static_cast<uint32_t>(x >> 32))) << 32 | lane_xor<X>(static_cast<uint32_t>(x));
 }
 __device__ __forceinline__ uint64_t lane64(uint64_t x, int lane) {
     return static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x >> 32), lane))) << 32 |
            static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(static_cast<uint32_t>(x)), lane));
 }
 __device__ __forceinline__ uint64_t wave_max64(uint64_t x) {
-    x = max(x, dpp64<0xB1>(x));
-    x = max(x, dpp64<0x4E>(x));
-    x = max(x, dpp64<0x141>(x));
-    x = max(x, dpp64<0x140>(x));
-    return max(max(lane64(x, 0), lane64(x, 16)), max(lane64(x, 32), lane64(x, 48)));
+    x = max(x, lane_xor64<1>(x));
+    x = max(x, lane_xor64<2>(x));
+    x = max(x, lane_xor64<7>(x));
+    x = max(x, lane_xor64<15>(x));
+    x = max(x, lane_xor64<16>(x));
+    return max(x, lane_xor64<32>(x));
+}
+
+// One step of a sorting network, falling: of lanes i and i ^ X the one without BIT
+// keeps the larger.
+template <int X, int BIT>
+__device__ __forceinline__ void exchange(uint64_t& k) {
+    const uint64_t other = lane_xor64<X>(k);
+    if ((other > k) == ((threadIdx.x & BIT) == 0)) k = other;
+}
+template <int X, int BIT>
+__device__ __forceinline__ void exchange(float& x) {
+    const float other = __uint_as_float(lane_xor<X>(__float_as_uint(x)));
+    x = threadIdx.x & BIT ? fminf(x, other) : fmaxf(x, other);
+}
+// 64 values that rise and fall at most once, by halving distances.
+template <typename T>
+__device__ __forceinline__ void merge64(T& k) {
+    exchange<32, 32>(k);
+    exchange<16, 16>(k);
+    exchange<8, 8>(k);
+    exchange<4, 4>(k);
+    exchange<2, 2>(k);
+    exchange<1, 1>(k);
+}
+// 64 values in any order: sorted runs of 2, 4, .. 64, each the merge of two of
+// half its length, the second taken backwards.
+template <typename T>
+__device__ __forceinline__ void sort64(T& k) {
+    exchange<1, 1>(k);
+    exchange<3, 2>(k);
+    exchange<1, 1>(k);
+    exchange<7, 4>(k);
+    exchange<2, 2>(k);
+    exchange<1, 1>(k);
+    exchange<15, 8>(k);
+    exchange<4, 4>(k);
+    exchange<2, 2>(k);
+    exchange<1, 1>(k);
+    exchange<31, 16>(k);
+    exchange<8, 8>(k);
+    exchange<4, 4>(k);
+    exchange<2, 2>(k);
+    exchange<1, 1>(k);
+    exchange<63, 32>(k);
+    exchange<16, 16>(k);
+    exchange<8, 8>(k);
+    exchange<4, 4>(k);
+    exchange<2, 2>(k);
+    exchange<1, 1>(k);
 }
 
 struct StepArgs {
@@ -62,26 +132,23 @@ constexpr int kScanWaves = 4;
 constexpr int kAhead = 4;           // vectors of a lane at a time
 constexpr int kRoom = 640;          // keys of a wavefront's buffer: below 128 kept plus 512 of one vector
 
-// The `keep` largest keys of buf[0 .. count) to buf[0 .. keep), falling; 0 past
-// the last.  Each lane watches the places lane, lane + 64, ...
-__device__ __forceinline__ void compress(uint64_t* buf, int count, int keep, int lane) {
-    uint64_t best = 0;
-    for (int i = lane; i < count; i += 64) best = max(best, buf[i]);
-    uint64_t out = 0;
-    for (int r = 0; r < keep; ++r) {
-        const uint64_t top = wave_max64(best);
-        if (lane == r) out = top;
-        if (top == 0) break;
-        if (best == top) {
-            best = 0;
-            for (int i = lane; i < count; i += 64) {
-                const uint64_t k = buf[i];
-                if (k < top) best = max(best, k);
-            }
-        }
+// The 64 largest keys of buf[0 .. count), lane l the l-th; 0 past the last.
+__device__ __forceinline__ uint64_t largest(const uint64_t* buf, int count, int lane) {
+    uint64_t best = lane < count ? buf[lane] : 0;
+    sort64(best);
+    for (int i = 64; i < count; i += 64) {
+        uint64_t more = i + lane < count ? buf[i + lane] : 0;
+        sort64(more);
+        best = max(best, lane_xor64<63>(more));         // the 64 largest of both, falling and rising once
+        merge64(best);
     }
+    return best;
+}
+// The `keep` largest keys of buf[0 .. count) to buf[0 .. keep).
+__device__ __forceinline__ void compress(uint64_t* buf, int count, int keep, int lane) {
+    const uint64_t best = largest(buf, count, lane);
     __builtin_amdgcn_wave_barrier();
-    if (lane < keep) buf[lane] = out;
+    if (lane < keep) buf[lane] = best;
     __builtin_amdgcn_wave_barrier();
 }
 
@@ -144,15 +211,9 @@ __global__ void __launch_bounds__(64 * kScanWaves) beam_scan_kernel(const StepAr
         if (__ballot(top > thr) == 0) continue;
         if (thr == kNegInf) {
             // nothing kept yet: the `beams` largest lane maxima bound the threshold from below
-            float rest = top, t = kNegInf;
-            for (int n = 0; n < a.beams;) {
-                t = wave_max(rest);
-                if (t == kNegInf) break;
-                const uint64_t at = __ballot(rest == t);
-                n += __popcll(at);
-                if (rest == t) rest = kNegInf;
-            }
-            low = t;
+            float t = top;
+            sort64(t);
+            low = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(t), a.beams - 1));
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
@@ -175,27 +236,27 @@ __global__ void __launch_bounds__(64 * kScanWaves) beam_scan_kernel(const StepAr
                 if (count == a.beams) thr = key_logit(buf[count - 1]);
             }
         }
+        // `beams` or more elements of this step reach `low`, and a later one equal to it has a higher token
+        thr = fmaxf(thr, low);
         low = kNegInf;
     }
     __builtin_amdgcn_wave_barrier();
-    compress(buf, count, a.beams, lane);
+    const uint64_t best = largest(buf, count, lane);
     const int64_t at = row * a.lists + list;
-    if (lane < a.beams) a.keys[at * a.beams + lane] = buf[lane];
+    if (lane < a.beams) a.keys[at * a.beams + lane] = best;
     soft = soft_wave(soft, c);
     if (lane == 0) a.soft[at] = soft;
 }
 
-// A sequence's lists joined: a wavefront a beam merges its sorted lists (a
-// lane holds the head of one), then one wavefront merges the beams, each lane
-// holding the head of one beam's list.
-constexpr int kJoinWaves = 8;
+// A sequence's lists joined.  A wavefront a beam: the `beams`th largest of its
+// lists' heads bounds its largest keys from below, so `beams` lists at most hold
+// keys that reach it; those are gathered and sorted.  Then one wavefront merges the
+// beams by score, each lane at the next place of one beam's list.
+constexpr int kJoinWaves = 16;
 
 __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(const StepArgs a) {
-    extern __shared__ uint64_t lists[];             // a row's lists, for each wavefront
-    __shared__ uint64_t best[NGRAM_MAX_BEAMS][NGRAM_MAX_BEAMS];
-    // a candidate's score is score + ((logit - max) - log sum exp(logits - max)), in an order that keeps
-    // the differences of huge logits
-    __shared__ double score_of[NGRAM_MAX_BEAMS], log_sum[NGRAM_MAX_BEAMS], max_of[NGRAM_MAX_BEAMS];
+    extern __shared__ uint64_t gathered[];          // min(lists, beams) lists' keys, for each wavefront
+    __shared__ uint64_t best[NGRAM_MAX_BEAMS][NGRAM_MAX_BEAMS], order_of[NGRAM_MAX_BEAMS][NGRAM_MAX_BEAMS];
     __shared__ int done[NGRAM_MAX_BEAMS];
     __shared__ int last[NGRAM_MAX_BEAMS][2];
     const int lane = threadIdx.x & 63;
@@ -203,7 +264,6 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(const StepAr
     const int64_t row0 = (a.first + blockIdx.x) * a.beams;
     for (int b = wave; b < a.beams; b += static_cast<int>(blockDim.x >> 6)) {
         const int64_t row = row0 + b;
-        const double score = a.scores[row];
         const bool fin = a.finished && a.finished[row];
         double log_s = 0, m = 0;
         uint64_t out = 0;
@@ -213,32 +273,43 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(const StepAr
             if (lane == 0) out = key_of(0.0f, a.end);       // its score and no more
         } else {
             // lists of this row: at most 64
+            const uint64_t* const keys = a.keys + row * a.lists * a.beams;
             Soft s{kLowest, 0.0f};
             uint64_t head = 0;
-            int taken = 0;
-            uint64_t* const room = lists + static_cast<int64_t>(wave) * a.lists * a.beams;
-            const uint64_t* const mine = room + lane * a.beams;
-            for (int i = lane; i < a.lists * a.beams; i += 64) room[i] = a.keys[row * a.lists * a.beams + i];
             if (lane < a.lists) {
                 s = a.soft[row * a.lists + lane];
-                head = mine[0];
+                head = keys[lane * a.beams];
             }
             s = soft_wave(s, 1.44269504088896340736f);
             m = s.m;
             log_s = log(static_cast<double>(s.s));
-            if (!(log_s == log_s)) head = 0;                // a NaN or +inf in the row
-            for (int r = 0; r < a.beams; ++r) {
-                const uint64_t top = wave_max64(head);
-                if (top == 0) break;
-                if (lane == r) out = top;
-                if (head == top) head = ++taken < a.beams ? mine[taken] : 0;
+            if (log_s == log_s) {                           // no NaN or +inf in the row
+                sort64(head);
+                const uint64_t least = lane64(head, a.beams - 1);
+                uint64_t* const buf = gathered + static_cast<int64_t>(wave) * min(a.lists, a.beams) * a.beams;
+                int count = 0;
+                for (int i = 0; i < a.lists * a.beams; i += 64) {
+                    const uint64_t k = i + lane < a.lists * a.beams ? keys[i + lane] : 0;
+                    const uint64_t hit = __ballot(k != 0 && k >= least);
+                    const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(hit >> 32),
+                                                                 __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(hit), 0));
+                    if (k != 0 && k >= least) buf[count + before] = k;
+                    count += __popcll(hit);
+                }
+                __builtin_amdgcn_wave_barrier();
+                out = largest(buf, count, lane);
+                __builtin_amdgcn_wave_barrier();
             }
         }
-        if (lane < a.beams) best[b][lane] = out;
+        if (lane < a.beams) {
+            // score + ((logit - max) - log sum exp(logits - max)), in an order that keeps the differences of
+            // huge logits, as a number that orders candidates; 0 for none
+            const double score = a.scores[row] + ((key_logit(out) - m) - log_s) + 0.0;
+            const uint64_t u = __builtin_bit_cast(uint64_t, score);
+            best[b][lane] = out;
+            order_of[b][lane] = out && score > -__builtin_inf() ? u >> 63 ? ~u : u | (UINT64_C(1) << 63) : 0;
+        }
         if (lane == 0) {
-            score_of[b] = score;
-            log_sum[b] = log_s;
-            max_of[b] = m;
             done[b] = fin;
             if (a.history) {
                 last[b][0] = a.history[2 * row + 1];
@@ -248,39 +319,27 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(const StepAr
     }
     __syncthreads();
     if (wave != 0) return;
-    int taken = 0;
-    double mine = 0;
-    uint64_t head = lane < a.beams ? best[lane][0] : 0;
-    // scores in an order that whole numbers keep; 0 for none
-    const auto rank = [&](uint64_t k) -> uint64_t {
-        if (!k) return 0;
-        mine = score_of[lane] + ((key_logit(k) - max_of[lane]) - log_sum[lane]) + 0.0;
-        if (!(mine > -__builtin_inf())) return 0;
-        const uint64_t u = __builtin_bit_cast(uint64_t, mine);
-        return u >> 63 ? ~u : u | (UINT64_C(1) << 63);
-    };
-    uint64_t order = rank(head);
-    int from = -1, token = -1, marked = 0, h0 = -1, h1 = -1;     // lane r: place r
-    float score = kNegInf;
+    int taken = 0, from = -1, place = 0;                    // from, place: lane r's candidate
+    uint64_t order = lane < a.beams ? order_of[lane][0] : 0, won = 0;
     for (int r = 0; r < a.beams; ++r) {
         const uint64_t top = wave_max64(order);
         if (top == 0) break;
         const int who = __builtin_ctzll(__ballot(order == top));            // ties to the lowest beam
-        const uint64_t k = lane64(head, who);
-        const float s = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(static_cast<float>(mine)), who));
+        const int at = __builtin_amdgcn_readlane(taken, who);
         if (lane == r) {
             from = who;
-            token = key_token(k);
-            score = s;
+            place = at;
+            won = top;
         }
-        if (lane == who) {
-            head = ++taken < a.beams ? best[lane][taken] : 0;
-            order = rank(head);
-        }
+        if (lane == who) order = ++taken < a.beams ? order_of[lane][taken] : 0;
     }
+    int token = -1, marked = 0, h0 = -1, h1 = -1;
+    float score = kNegInf;
     if (lane >= a.beams) return;
     const int64_t to = row0 + lane;
     if (from >= 0) {
+        token = key_token(best[from][place]);
+        score = static_cast<float>(__builtin_bit_cast(double, won >> 63 ? won & ~(UINT64_C(1) << 63) : ~won));
         marked = done[from] || token == a.end;
         h0 = last[from][0];
         h1 = last[from][1];
@@ -419,7 +478,7 @@ int ngram_beam_step(const void* logits, int32_t dtype, int64_t batch, int32_t be
         if (dtype == NGRAM_F32) hipLaunchKernelGGL(beam_scan_kernel<true>, grid, dim3(64 * kScanWaves), 0, stream, a);
         else hipLaunchKernelGGL(beam_scan_kernel<false>, grid, dim3(64 * kScanWaves), 0, stream, a);
     }
-    const int waves = std::min(beams, kJoinWaves), room = waves * a.lists * beams * 8;
+    const int row_room = std::min(a.lists, beams) * beams * 8, waves = std::min(beams, kJoinWaves), room = waves * row_room;
     for (a.first = 0; a.first < batch; a.first += most_groups(64 * waves))
         hipLaunchKernelGGL(beam_join_kernel, dim3(static_cast<uint32_t>(std::min(most_groups(64 * waves), batch - a.first))),
                            dim3(64 * waves), room, stream, a);
