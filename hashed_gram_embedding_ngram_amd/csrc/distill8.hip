@@ -628,6 +628,7 @@ DistillArgs device_args(const ngram_distill_args* p) {
     const int64_t e = p->dtype == NGRAM_F32 ? 4 : 8, vectors = (p->V + e - 1) / e;
     a.per = static_cast<int32_t>((vectors + a.chunks - 1) / a.chunks);
     a.per = (a.per + 7) / 8 * 8;                                            // whole words of marks
+    a.chunks = static_cast<int32_t>((vectors + a.per - 1) / a.per);         // which may leave fewer: a row's last chunk has its last vector
     return a;
 }
 

@@ -120,6 +120,21 @@ def test_loss_and_gradient(n, V, k, dtype, rest):
     assert torch.equal(both.loss, one.loss) and torch.equal(inplace, one.dlogits)
 
 
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("n,V,k,dtype", [(2, 153897, 5, F32), (1, 153897, 200, F32), (1, 307793, 200, BF), (2, 307793, 5, BF)])
+def test_long_rows_in_many_parts(n, V, k, dtype, rest):
+    """Rows whose parts, rounded up to whole words of marks, are fewer than were asked for; the last vector is no whole one."""
+    say(f"distill parts {n} x {V}, {k} listed, {dtype} rest={rest}")
+    a = inputs(np.random.default_rng(n + V + k), n, V, k, dtype, None, rest, 1.5)
+    g = gpu(a, dtype, dtype)
+    kw = dict(temperature=1.5, teacher_lse=g["lse"])
+    one = ng.ngram_distill(g["z"], g["t"], g["ids"], grad=True, weight=g["weight"], keep_stats=True, **kw)
+    check(a, dtype, one.loss, one.dlogits, one.stats)
+    inplace = g["z"].clone()
+    both = ng.ngram_distill(inplace, g["t"], g["ids"], weight=g["weight"], dlogits_out=inplace, **kw)
+    assert torch.equal(both.loss, one.loss) and torch.equal(inplace, one.dlogits)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_strided_and_unaligned_rows(dtype):
     say(f"distill strides {dtype}")
