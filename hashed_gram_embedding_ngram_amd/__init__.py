@@ -1202,9 +1202,21 @@ def ngram_beam_step(logits, scores, beams: int, tokens=None, history=None, finis
     return out
 
 
+def _apart(states, rows):
+    """Refuse (address, bytes of a row, distance of rows) of which two share bytes; rows that interleave do not."""
+    begun = []
+    for at, row, stride in sorted(s for s in states if s[1] > 0 and rows > 0):
+        begun = [b for b in begun if b[0] + (rows - 1) * b[2] + b[1] > at]
+        for first, size, step in begun:
+            off = (at - first) % stride
+            if step != stride or off < size or stride - off < row:
+                raise NgramError("two states overlap")
+        begun.append((at, row, stride))
+
+
 class BeamStates:
     """The tensors that ngram_beam_reorder moves: each has the rows of all beams as its first dimension (at any distance),
-    and contiguous rows.  The list names memory, and keeps that memory."""
+    and contiguous rows; no two share memory.  The list names memory, and keeps that memory."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)
@@ -1225,6 +1237,7 @@ class BeamStates:
             if stride < row:
                 raise NgramError(f"state {i}: its rows overlap")
             c.append(_BeamState(t.data_ptr(), row, stride))
+        _apart([(s.data, s.row_bytes, s.stride) for s in c], self.rows)
         self.count = len(c)
         self.c = (_BeamState * max(self.count, 1))(*c)
         self.storages = [t.untyped_storage() for t in self.tensors]

@@ -197,6 +197,16 @@ OTHER = Dev(torch.zeros(8), device=1)
 STREAM1 = type("S", (), {"device_index": 1, "cuda_stream": 0})()
 
 
+def test_beam_states_overlap(no_launch):
+    t = torch.zeros(8, 6)
+    for pair in ([t, t], [t[:, :4], t[:, 3:]], [t, t[1:].view(7, 6)[:, :2]], [t[:, 2:], t[:, :3]], [t, t.view(4, 12)], [t, t.view(8, 2, 3)]):
+        rows = min(p.shape[0] for p in pair)
+        with pytest.raises(ng.NgramError, match="overlap"):
+            ng.BeamStates([Dev(p[:rows]) for p in pair])
+    for pair in ([t[:, :4], t[:, 4:]], [t[:4], t[4:]], [t[:0], t[:0]], [t[:, :2], t[:, 4:], t[:, 2:4]], [t[:1], t[1:2]], [t[:, :0], t]):
+        assert ng.BeamStates([Dev(p) for p in pair]).count == len(pair)
+
+
 @pytest.mark.parametrize("call,match", [
     (lambda: ng.ngram_project_int4(f32(4, 72), w4()), "columns"),
     (lambda: ng.ngram_project_int4(torch.zeros(4, 64), w4()), "device tensor"),
