@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(THREADS) distill_row_kernel(const DistillArgs 
 // of 512 vectors and more.
 int chunks_of(int64_t n, int64_t v, int dtype) {
     const int64_t e = dtype == NGRAM_F32 ? 4 : 8, vectors = (v + e - 1) / e;
-    const int64_t want = 1024 / std::max<int64_t>(n, 1);
+    const int64_t want = 512 / std::max<int64_t>(n, 1);
     return static_cast<int>(std::max<int64_t>((vectors + kBitVectors - 1) / kBitVectors, std::min<int64_t>(want, vectors / 512)));
 }
 
@@ -659,7 +659,7 @@ void launch_grad(const DistillArgs& a, bool f32, hipStream_t st) {
 }
 
 // Rows in one workgroup each: enough of them to fill the card, short enough for the marks.
-bool whole_rows(const DistillArgs& a) { return a.n >= 256 && a.v <= kRowMarks; }
+bool whole_rows(const DistillArgs& a, int64_t e) { return a.v <= kRowMarks && (a.v <= 8192 * e || a.n >= 128); }
 
 template <bool F32, bool REST, bool STREAM, int THREADS, int NV>
 void launch_row(const DistillArgs& a, hipStream_t st) {
@@ -732,7 +732,7 @@ int ngram_distill(const ngram_distill_args* p, float* loss_out, float* stats_out
     a.stats = stats_out ? stats_out : reinterpret_cast<float*>(at + room.stats);
     a.weight = weight; a.scale = static_cast<float>(static_cast<double>(scale) * p->temperature); a.dz = dlogits_out; a.dld = dld;
     const bool f32 = p->dtype == NGRAM_F32;
-    if (dlogits_out && whole_rows(a)) {
+    if (dlogits_out && whole_rows(a, f32 ? 4 : 8)) {
         if (f32 && a.teacher_lse) launch_rows<true, true>(a, stream);
         else if (f32) launch_rows<true, false>(a, stream);
         else if (a.teacher_lse) launch_rows<false, true>(a, stream);

@@ -70,7 +70,20 @@ __device__ __forceinline__ uint32_t div_units(const QuantArgs& a, uint32_t t) {
     return a.units == 1 ? t : static_cast<uint32_t>((static_cast<uint64_t>(t) * a.magic) >> 32) >> a.shift;
 }
 
-template <bool F32, bool ASYM>
+// a / b correctly rounded from y = 1 / b, which is: a product, and twice the remainder times y.  The first
+// makes the quotient one of the two fp32 numbers around the true one, and from such a one and a correctly
+// rounded y the second gives the nearest (Markstein's theorem).  Where a and b have eight bits once is enough:
+// a / b then is an fp32 number or 2^-9 of a step and more from the middle of two (a whole number over b's, 2^-24
+// and 2^-8), and the first leaves an error below 2^-22 of a step before it rounds.
+template <bool TWICE>
+__device__ __forceinline__ float quotient(float a, float b, float y) {
+    float v = a * y;
+    v = __builtin_fmaf(__builtin_fmaf(-v, b, a), y, v);
+    if (TWICE) v = __builtin_fmaf(__builtin_fmaf(-v, b, a), y, v);
+    return v;
+}
+
+template <bool F32, bool ASYM, bool SF32>
 __global__ void __launch_bounds__(256) quant_int4_kernel(const QuantArgs a) {
     const uint32_t t = blockIdx.x * 256 + threadIdx.x;
     const bool on = t < a.count;                            // whole groups are on or off
@@ -92,35 +105,27 @@ __global__ void __launch_bounds__(256) quant_int4_kernel(const QuantArgs a) {
     const int lanes = a.group / kVec;
     lo = min_lanes(lo, lanes);
     nhi = min_lanes(nhi, lanes);
-    float s;
-    if (ASYM) s = (-nhi - lo) / 15.0f;
-    else s = fmaxf(-lo, -nhi) / 7.0f;
-    if (!a.sf32) s = __uint_as_float(bf16_pair(s, s) << 16);
+    constexpr float steps = ASYM ? 15.0f : 7.0f, one = 1.0f / steps;
+    const float range = ASYM ? -nhi - lo : fmaxf(-lo, -nhi);
+    float s = quotient<true>(range, steps, one);
+    if (__builtin_expect(__ballot(!(range > 0x1p-90f && range < 0x1p90f)) != 0, 0)) s = range / steps;
+    if (!SF32) s = __uint_as_float(bf16_pair(s, s) << 16);
     // a group with a value that is not finite, or too wide for a finite scale, is NaN throughout
     const uint64_t odd = __ballot(!(bad == 0.0f));
     const int first = (threadIdx.x & 63) & ~(lanes - 1);
     const bool nan = ((odd >> first) & ((1u << lanes) - 1)) != 0 || !(s < __uint_as_float(kInfBits));
     if (s == 0.0f) s = 1.0f;
-    float z = 8.0f;
-    if (ASYM) z = fminf(fmaxf(rintf(-lo / s), 0.0f), 15.0f);
-    // w / s correctly rounded from y = 1 / s, which is: a product, and twice the remainder times y.  The first
-    // makes the quotient one of the two fp32 numbers around the true one, and from such a one and a correctly
-    // rounded y the second gives the nearest (Markstein's theorem).  A division for each of 151936 x 2560
-    // weights takes 325 us, this way 255.  (Dividing only
-    // where a quotient lies near a half saves nothing: bf16 weights over bf16 scales lie on halves often.)
     const float y = 1.0f / s;
-    float q[8];
+    float z = 8.0f, q[8];
+    if (ASYM) z = rintf(quotient<F32 || SF32>(-lo, s, y));
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float v = w[k] * y;
-        v = __builtin_fmaf(__builtin_fmaf(-v, s, w[k]), y, v);
-        v = __builtin_fmaf(__builtin_fmaf(-v, s, w[k]), y, v);
-        q[k] = rintf(v);
-    }
+    for (int k = 0; k < 8; ++k) q[k] = rintf(quotient<F32 || SF32>(w[k], s, y));
     if (__builtin_expect(__ballot(!(s > 0x1p-100f && s < 0x1p100f)) != 0, 0)) {     // where 1 / s or a remainder leaves the range
+        if (ASYM) z = rintf(-lo / s);
 #pragma unroll
         for (int k = 0; k < 8; ++k) q[k] = rintf(w[k] / s);
     }
+    if (ASYM) z = fminf(fmaxf(z, 0.0f), 15.0f);
     // four codes in a whole number below 2^16, Horner's way, the zero added to all of them at once
     float half[2];
 #pragma unroll
@@ -143,13 +148,13 @@ __global__ void __launch_bounds__(256) quant_int4_kernel(const QuantArgs a) {
     if (4 * static_cast<int64_t>(u) < a.ld) reinterpret_cast<uint32_t*>(a.codes + row * a.ld)[u] = code;
     if ((u & (lanes - 1)) == 0) {
         const int64_t at = row * a.sld + u / lanes;
-        if (a.sf32) static_cast<float*>(a.scales)[at] = s;
+        if (SF32) static_cast<float*>(a.scales)[at] = s;
         else static_cast<uint16_t*>(a.scales)[at] = static_cast<uint16_t>(__float_as_uint(s) >> 16);
         if (ASYM) a.zeros[at] = static_cast<uint8_t>(z);
         // the places past the last group, to whole fours: scale 1, zero 8
         if (u + lanes == a.units) {
             for (int64_t e = at + 1; e < (row + 1) * a.sld; ++e) {
-                if (a.sf32) static_cast<float*>(a.scales)[e] = 1.0f;
+                if (SF32) static_cast<float*>(a.scales)[e] = 1.0f;
                 else static_cast<uint16_t*>(a.scales)[e] = 0x3F80;
                 if (ASYM) a.zeros[e] = 8;
             }
@@ -715,10 +720,14 @@ __global__ void __launch_bounds__(64 * kTileWaves) project_int4_tile_kernel(cons
 
 template <int MT, int GROUP, bool F32>
 int launch_product(ProductArgs a, hipStream_t st) {
-    const bool split = a.o < 128 * 256;
+    const int64_t mtiles = (a.n + 16 * MT - 1) / (16 * MT), tiles = (a.o + 16 * kTileWaves - 1) / (16 * kTileWaves);
+    // Tiles of 128 weight rows where there are enough of them (us, split and tile): 100 x 2560 x 4096 bf16 22 and 38,
+    // x 8192 37 and 39, x 12288 52 and 40, x 16384 68 and 41, 200 x 2560 x 8192 69 and 39; fp32 20 x 2560 x 12288
+    // 28 and 35, 40 x 2560 x 12288 50 and 37, 40 x 1032 x 12288 21 and 17.
+    const bool split = tiles * mtiles < 192;
     const int threads = split ? 64 * kSplitWaves : 64 * kTileWaves;
-    a.otiles = split ? (a.o + 15) / 16 : (a.o + 16 * kTileWaves - 1) / (16 * kTileWaves);
-    const int64_t mtiles = (a.n + 16 * MT - 1) / (16 * MT), most = most_groups(threads) / a.otiles;
+    a.otiles = split ? (a.o + 15) / 16 : tiles;
+    const int64_t most = most_groups(threads) / a.otiles;
     for (a.first = 0; a.first < mtiles; a.first += most) {
         const dim3 grid(static_cast<uint32_t>(std::min(most, mtiles - a.first) * a.otiles));
         if (split) hipLaunchKernelGGL((project_int4_split_kernel<MT, GROUP, F32>), grid, dim3(threads), 0, st, a);
@@ -745,12 +754,17 @@ int launch_rows(const ProductArgs& a, hipStream_t st) {
 
 template <int GROUP, bool F32>
 int launch_group(const ProductArgs& a, hipStream_t st) {
+    // x in registers where they hold it and, but for the last, where that is faster (us, so and without): bf16 1 x
+    // 2560 x 2560 4.5 and 4.8, 16 x 2560 x 151936 60 and 102, 16 x 6144 x 5120 13 and 22, 32 x 1536 x 40000 18 and 26,
+    // 48 x 2560 x 8192 19 and 20, 64 x 2560 x 16384 27 and 44; but 64 x 1032 x 4096 8.5 and 6.0, 40 x 2560 x 4096 14 and 10;
+    // fp32 16 x 1536 x 40000 18 and 25, 11 x 1032 x 151936 48 and 51; two chunks a wavefront lose, 16 x 2560 x 151936
+    // 130 and 113.
     int rc = 1;
     if (a.n <= 16) {
         if (a.chunks <= 12) rc = launch_rows<1, GROUP, F32, 1, 12>(a, st);
-        else if (a.chunks <= 24) rc = launch_rows<1, GROUP, F32, 2, 12>(a, st);
+        else if (!F32 && a.chunks <= 24) rc = launch_rows<1, GROUP, false, 2, 12>(a, st);
         else if (!F32 && a.chunks <= 48) rc = launch_rows<1, GROUP, false, 4, 12>(a, st);
-    } else if (!F32 && a.n <= 64) {
+    } else if (!F32 && (a.n <= 32 || (a.n <= 64 && a.chunks > 12 && a.o >= 8192))) {
         if (a.chunks <= 12) rc = launch_rows<2, GROUP, false, 1, 12>(a, st);
         else if (a.chunks <= 24) rc = launch_rows<2, GROUP, false, 2, 12>(a, st);
     }
@@ -803,12 +817,15 @@ int ngram_quant_int4(const void* x, int32_t x_dtype, int64_t n, int32_t d, const
     a.units = static_cast<uint32_t>(int4_groups(d, q->group) * (q->group / kVec));
     a.cols = d; a.group = q->group; a.sf32 = q->scale_dtype == NGRAM_F32;
     const bool f32 = x_dtype == NGRAM_F32, asym = q->zeros != nullptr;
-    return in_rows(a, n, [&](const QuantArgs& b, dim3 grid) {
-        if (f32 && asym) hipLaunchKernelGGL((quant_int4_kernel<true, true>), grid, dim3(256), 0, stream, b);
-        else if (f32) hipLaunchKernelGGL((quant_int4_kernel<true, false>), grid, dim3(256), 0, stream, b);
-        else if (asym) hipLaunchKernelGGL((quant_int4_kernel<false, true>), grid, dim3(256), 0, stream, b);
-        else hipLaunchKernelGGL((quant_int4_kernel<false, false>), grid, dim3(256), 0, stream, b);
-    }, "ngram_quant_int4");
+    const auto launch = [&](auto kernel) {
+        return in_rows(a, n, [&](const QuantArgs& b, dim3 grid) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, b); }, "ngram_quant_int4");
+    };
+    if (f32) {
+        if (asym) return a.sf32 ? launch(quant_int4_kernel<true, true, true>) : launch(quant_int4_kernel<true, true, false>);
+        return a.sf32 ? launch(quant_int4_kernel<true, false, true>) : launch(quant_int4_kernel<true, false, false>);
+    }
+    if (asym) return a.sf32 ? launch(quant_int4_kernel<false, true, true>) : launch(quant_int4_kernel<false, true, false>);
+    return a.sf32 ? launch(quant_int4_kernel<false, false, true>) : launch(quant_int4_kernel<false, false, false>);
 }
 
 int ngram_dequant_int4(const ngram_int4* q, void* y, int32_t y_dtype, ngram_stream_t stream) {
