@@ -130,7 +130,7 @@ __device__ __forceinline__ bool alive(const StepArgs& a, int64_t row) { return a
 
 constexpr int kScanWaves = 4;
 constexpr int kAhead = 4;           // vectors of a lane at a time
-constexpr int kRoom = 640;          // keys of a wavefront's buffer: below 128 kept plus 512 of one vector
+constexpr int kRoom = 640;          // keys of a wavefront's buffer: below 64 kept plus 512 of one vector
 
 // The 64 largest keys of buf[0 .. count), lane l the l-th; 0 past the last.
 __device__ __forceinline__ uint64_t largest(const uint64_t* buf, int count, int lane) {
@@ -159,6 +159,11 @@ __device__ __forceinline__ void compress(uint64_t* buf, int count, int keep, int
 // it fills, which raises the threshold.  A wavefront's steps go upwards, so an
 // element equal to the threshold has a higher token than those kept; within a step
 // vectors go upwards too.
+//
+// Bound by memory where rows are many: 512 rows of 151936 fp32 take 60 us, 5.2
+// TB/s.  Cutting by sorts of 64 keys:
+// rounds of maxima, one for each beam, took 41 us against 23 for 176 rows of 109117 bf16
+// with 16 beams.  Four rows of 151936 bf16: 8.4 us of loads that wait, sorts and the launch.
 template <bool F32>
 __global__ void __launch_bounds__(64 * kScanWaves) beam_scan_kernel(const StepArgs a) {
     constexpr int E = Row<F32>::E;
@@ -251,7 +256,9 @@ __global__ void __launch_bounds__(64 * kScanWaves) beam_scan_kernel(const StepAr
 // A sequence's lists joined.  A wavefront a beam: the `beams`th largest of its
 // lists' heads bounds its largest keys from below, so `beams` lists at most hold
 // keys that reach it; those are gathered and sorted.  Then one wavefront merges the
-// beams by score, each lane at the next place of one beam's list.
+// beams by score, each lane at the next place of one beam's list.  One sequence of
+// four beams 5.6 us, 11 of 16 beams 11, 64 of eight 8: bound by dependent steps (loads,
+// sorts, an fp64 logarithm, a maximum over lanes for each place).
 constexpr int kJoinWaves = 16;
 
 __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(const StepArgs a) {
@@ -356,6 +363,8 @@ __global__ void __launch_bounds__(64 * kJoinWaves) beam_join_kernel(const StepAr
 
 // Workgroups a row: enough rows fill the card with one each; few rows are cut,
 // to 16 parts at most (64 lists, one a lane of the join) of 4096 elements and more.
+// 1024 workgroups and more: 64 x 8 x 151936 fp32 70 us (512: 92), 11 x 16 x 109117 bf16 37 (42).  4096 elements:
+// 8 x 4 x 50257 11.7 us (8192: 12.5), 1 x 8 x 5003 11.8 (13.2); 2048 changes nothing.
 int chunks_of(int64_t rows, int64_t v) {
     const int64_t want = (1024 + rows - 1) / std::max<int64_t>(rows, 1);
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, 16, (v + 4095) / 4096})));
@@ -371,7 +380,8 @@ int64_t step_bytes(int64_t rows, int lists, int beams) { return rows * lists * (
 // Reordering.  A thread owns one column of 16, 4 or 1 bytes of a sequence's
 // rows: it reads what every row that changes takes, then writes those
 // rows, so nothing is read after it was overwritten and rows that stay move
-// no bytes.
+// no bytes.  24 states of 128 rows of 256 KB: 237 us, a copy's rate (5.0 TB/s); with
+// addresses in registers of each lane instead of uniform ones 378.
 constexpr int kStates = 64;
 
 struct ReorderArgs {

@@ -15,7 +15,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kBitVectors = 16384;      // vectors of a chunk at most: 16 KB of marks
 constexpr int kScan = 128;              // places of a short list
 // Gradients above this size are stored past the caches' usual keeping (1021 x 32003 fp32, forward and
-// backward: 83 us against 97; 4096 x 151936 bf16 497 against 523); smaller ones are read next where they lie.
+// backward: 84 us against 97; 4096 x 151936 bf16 498 against 523); smaller ones are read next where they lie.
 constexpr int64_t kStreamFrom = int64_t{64} << 20;
 
 struct Sums;
@@ -246,7 +246,8 @@ __device__ __forceinline__ void mark_listed(const DistillArgs& a, int64_t row, i
 template <int E>
 __device__ __forceinline__ uint32_t marks_of(const uint32_t* marks, int vector) { return marks[(vector * E) >> 5] >> ((vector * E) & 31); }
 
-// The sums of a chunk of a row; the row's loss where it is one chunk.
+// The sums of a chunk of a row; the row's loss where it is one chunk.  1021 x
+// 32003 fp32 with the rest: 29 us, 4.5 TB/s, bound by memory and the marks in LDS.
 template <bool F32, bool REST>
 __global__ void __launch_bounds__(kThreads) distill_stats_kernel(const DistillArgs a) {
     constexpr int E = Row<F32>::E;
@@ -392,7 +393,9 @@ __device__ __forceinline__ Slope slope_of(const DistillArgs& a, float gs, const 
 // The gradient of a chunk of a row, from the forward's statistics or from the
 // chunks' sums (then the row's first workgroup writes its loss): a q
 // everywhere, then the listed tokens once more.  Their logits are read before anything is
-// written, since dz may be z.
+// written, since dz may be z.  1021 x 32003 fp32 with the rest: 47 to 52 us, 5.2 TB/s,
+// bound by memory; of few rows (24 x 151936 bf16, 8 us) by the teacher's fp64 side,
+// which every chunk computes.
 template <bool F32, bool REST, bool STREAM>
 __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArgs a) {
     constexpr int E = Row<F32>::E;
@@ -493,8 +496,9 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
 // wavefronts a compute unit: 4096 x 151936 bf16 took 546 us with all of a row in
 // registers (512 threads, 38 vectors each), 560 as one stream that asks for the next row as it stores this
 // one, 586 with nothing kept (read twice, from the last-level cache the second time); 1024 threads with 14
-// vectors each and the rest read again 497.  Rows of up to 6144 vectors fit whole: 512 threads, two or three
-// workgroups a unit.
+// vectors each and the rest read again 498.  Rows of up to 6144 vectors fit whole: 512 threads, two or three
+// workgroups a unit (4096 x 32003 bf16 143 us, with 1024 threads 198); up to 2048 with a third of the registers
+// (4096 x 5003 bf16 46 us, 61 with all).
 constexpr int kRowMarks = 1 << 18;      // tokens of a row at most
 
 // The teacher's side is one wavefront's work while the row's loads are on
@@ -584,7 +588,8 @@ __global__ void __launch_bounds__(THREADS) distill_row_kernel(const DistillArgs 
 }
 
 // Workgroups a row: one where rows fill the card; few rows are cut into parts
-// of 512 vectors and more.
+// of 512 vectors and more, for 512 workgroups.  (24 x 151936 bf16 with the gradient 15.7 us, for 1024 workgroups 20.0,
+// for 256 15.2; 96 rows 24, 29 and 26.  Parts of 256 vectors: 16 rows 16.4 against 14.2.)
 int chunks_of(int64_t n, int64_t v, int dtype) {
     const int64_t e = dtype == NGRAM_F32 ? 4 : 8, vectors = (v + e - 1) / e;
     const int64_t want = 512 / std::max<int64_t>(n, 1);
@@ -658,7 +663,10 @@ void launch_grad(const DistillArgs& a, bool f32, hipStream_t st) {
     else launch_grad_of<false, false>(a, st);
 }
 
-// Rows in one workgroup each: enough of them to fill the card, short enough for the marks.
+// Rows in one workgroup each, loss and gradient in one launch: short ones, or enough of them to fill the card, and
+// short enough for the marks.  us, so and apart: 1 x 1001 bf16 6.8 and 13.3, 1 x 32003 fp32 10.4 and 11.9, 256 x 32003
+// bf16 14.7 and 27, 200 x 151936 bf16 36 and 46, 128 x 151936 fp32 40, 120 of them apart 42; but 24 x 151936 bf16 22
+// and 16, 96 of them 27 and 24.
 bool whole_rows(const DistillArgs& a, int64_t e) { return a.v <= kRowMarks && (a.v <= 8192 * e || a.n >= 128); }
 
 template <bool F32, bool REST, bool STREAM, int THREADS, int NV>
