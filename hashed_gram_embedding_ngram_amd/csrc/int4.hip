@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(64 * kSplitWaves) project_int4_split_kernel(co
 //
 // 32 x 2560 x 151936 bf16: 70 to 73 us, 3.2 TB/s; the chain of load, LDS read,
 // widening, products and barrier of each 16 weight rows bounds it, on 10
-// wavefronts a unit (x in registers and 12 KB of LDS a wavefront allow no more).
+// wavefronts a unit (x in registers and 12 KB of LDS a wavefront allow no more; 16 x 2560 x 151936 60 us, 4 x 1032 x 151936 29).
 // Codes straight to registers instead 180 us, two tiles a turn 90.
 template <int MT, int GROUP, bool F32, bool SF32, int PER>
 struct RowsShape {
@@ -469,11 +469,12 @@ struct RowsShape {
     static constexpr int SL = (16 * SD + 63) / 64, ZL = (16 * ZD + 63) / 64;                        // loads of them
     static constexpr int Slot = PER * 1024 + (SL + ZL) * 256;
     static constexpr int Part = MT * 1024;
+    static constexpr int Simd = PER * MT * PARTS == 1 ? 6 : PER * MT * PARTS <= 3 ? 4 : 3;      // wavefronts a SIMD that registers allow
     static constexpr int bytes(int waves) { return waves * (SLOTS * Slot + 2 * Part); }
 };
 
 template <int MT, int GROUP, bool F32, bool SF32, int PER, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES) project_int4_rows_kernel(const ProductArgs a) {
+__global__ void __launch_bounds__(64 * WAVES, (RowsShape<MT, GROUP, F32, SF32, PER>::Simd)) project_int4_rows_kernel(const ProductArgs a) {
     typedef RowsShape<MT, GROUP, F32, SF32, PER> S;
     constexpr int G = S::G, PARTS = S::PARTS, F = S::F, SLOTS = S::SLOTS;
     extern __shared__ __attribute__((aligned(1024))) uint8_t lds[];
@@ -753,11 +754,15 @@ int launch_product(ProductArgs a, hipStream_t st) {
 
 template <int MT, int GROUP, bool F32, bool SF32, int PER, int WAVES>
 int launch_rows_of(ProductArgs a, hipStream_t st) {
-    const int waves = (a.chunks + PER - 1) / PER, lds = RowsShape<MT, GROUP, F32, SF32, PER>::bytes(waves);
+    typedef RowsShape<MT, GROUP, F32, SF32, PER> S;
+    const int waves = (a.chunks + PER - 1) / PER, lds = S::bytes(waves);
     if (lds > 160 * 1024) return 1;             // the caller takes another kernel
     const auto kernel = project_int4_rows_kernel<MT, GROUP, F32, SF32, PER, WAVES>;
     a.otiles = (a.o + 15) / 16;
-    const int64_t at_once = 256 * std::max(1, std::min(12 / waves, 160 * 1024 / lds));
+    // workgroups a unit: two, whose barriers are not each other's, or 12 wavefronts (4 x 1032 x 151936 bf16 29 us, with 12
+    // wavefronts 43; 8 x 2048 x 40000 14.8 and 16.4; but 4 x 512 x 151936 with 24 wavefronts 19.1, with 12 16.3)
+    const int fit = std::min(4 * S::Simd / waves, 160 * 1024 / lds);
+    const int64_t at_once = 256 * std::max(1, std::min(fit, std::max(12 / waves, 2)));
     const dim3 grid(static_cast<uint32_t>(std::min(a.otiles, at_once))), block(64 * waves);
     for (a.first = 0; a.first * 16 * MT < a.n; ++a.first) hipLaunchKernelGGL(kernel, grid, block, lds, st, a);
     return hip_status("ngram_project_int4");
