@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(64 * kSplitWaves) project_int4_split_kernel(co
 template <int MT, int GROUP, bool F32, bool SF32, int PER>
 struct RowsShape {
     static constexpr int G = kChunk / GROUP, PARTS = F32 ? 3 : 1, F = GROUP / 32;
-    static constexpr int SLOTS = PER == 4 ? 2 : PER == 2 ? 3 : 4;
+    static constexpr int SLOTS = PER == 4 ? 2 : PER == 2 || MT * PARTS == 1 ? 3 : 4;       // of one chunk and 16 bf16 rows 3 let two workgroups fit
     static constexpr int SD = PER * G * (SF32 ? 4 : 2) < 4 ? 1 : PER * G * (SF32 ? 4 : 2) / 4;      // words of scales a row
     static constexpr int ZD = PER * G < 4 ? 1 : PER * G / 4;                                        // words of zeros a row
     static constexpr int SL = (16 * SD + 63) / 64, ZL = (16 * ZD + 63) / 64;                        // loads of them
@@ -759,10 +759,11 @@ int launch_rows_of(ProductArgs a, hipStream_t st) {
     if (lds > 160 * 1024) return 1;             // the caller takes another kernel
     const auto kernel = project_int4_rows_kernel<MT, GROUP, F32, SF32, PER, WAVES>;
     a.otiles = (a.o + 15) / 16;
-    // workgroups a unit: two, whose barriers are not each other's, or 12 wavefronts (4 x 1032 x 151936 bf16 29 us, with 12
-    // wavefronts 43; 8 x 2048 x 40000 14.8 and 16.4; but 4 x 512 x 151936 with 24 wavefronts 19.1, with 12 16.3)
+    // workgroups a unit: two, whose barriers are not each other's, or 16 wavefronts (4 x 1032 x 151936 bf16 29 us, one
+    // workgroup 43; 8 x 2048 x 40000 14.8 and 16.4; 8 x 1536 x 40000 13.0 and 15.4; but 4 x 512 x 151936 with 24 wavefronts
+    // 19.1, with 16 15.1, with 12 16.3)
     const int fit = std::min(4 * S::Simd / waves, 160 * 1024 / lds);
-    const int64_t at_once = 256 * std::max(1, std::min(fit, std::max(12 / waves, 2)));
+    const int64_t at_once = 256 * std::max(1, std::min(fit, std::max(16 / waves, 2)));
     const dim3 grid(static_cast<uint32_t>(std::min(a.otiles, at_once))), block(64 * waves);
     for (a.first = 0; a.first * 16 * MT < a.n; ++a.first) hipLaunchKernelGGL(kernel, grid, block, lds, st, a);
     return hip_status("ngram_project_int4");
