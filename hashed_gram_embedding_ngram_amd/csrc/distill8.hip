@@ -38,6 +38,7 @@ struct DistillArgs {
     int32_t per;            // vectors of a chunk
     float scale;            // of the gradient, without the row's weight and T
     float c;                // log2(e) / T
+    float floor;            // -2^20 / c
     double inv_t, t2;       // 1 / T, T^2
 };
 
@@ -54,34 +55,38 @@ __device__ __forceinline__ double wave_sum_f64(double x) {
 
 // ---------------------------------------------------------------------------
 // Sums of exp.  With c = log2(e) / T a set of logits is (m, s): m its largest
-// and s the sum of 2^(x c - R), R = m c rounded to fp32.  One fused multiply-add and
-// one exp2 an element: R is a reference like any other, so its rounding costs nothing as long as
-// whoever uses s takes the same R, and x c - R is rounded once, relative to its own size.
-// Where x c leaves fp32's range (logits beyond 1e30, c beyond 1e7; a set of masked logits among
-// them), s is the sum of 2^((x - m) c) instead.
-constexpr float kFloor = -1e30f;        // m of the empty set
-
+// and s the sum of 2^((x - m) c).
+//
+// A pass over a row holds s as the sum of 2^(x c - R), R = m c rounded to fp32: one
+// fused multiply-add and one exp2 an element, each rounded relative to its own size, and 2^(R - m c)
+// at the end takes R's rounding off (settled).  That rounding is an exponent of the
+// largest element, so m c has to stay small: a thread starts at m = -2^20 / c (the
+// floor), so that |m c| is at most 2^20 and the rounding 2^-4 in every thread of a row whose
+// largest logit lies within 2^19 / c; a logit below the floor (a masked one of -1e9, say) adds
+// exactly 0 to such a row.  Other rows (logits of hundreds of thousands and more
+// times T, masked throughout among them) are summed once more by (x - m) c.  Without the floor a thread
+// whose first vector is masked by -1e10 would hold infinity, to be multiplied with 0 later.
 struct Sums {
     float m, s, off;                    // off: the unlisted tokens' part of s
 };
 
-__device__ __forceinline__ bool usual(float m, float c) { return fabsf(m) < 1e30f && c < 1e7f; }
-// What a sum at `from` is multiplied with to be one at `to`.
-__device__ __forceinline__ float rescale(float from, float to, float c) {
-    return usual(from, c) && usual(to, c) ? exp2_fast(from * c - to * c) : exp2_fast((from - to) * c);
-}
+__device__ __forceinline__ bool usual(float m, float floor) { return fabsf(m) <= -0.5f * floor; }
+// What a sum at `from` is multiplied with to be one at `to`; USUAL: at its R.
+template <bool USUAL>
+__device__ __forceinline__ float rescale(float from, float to, float c) { return USUAL ? exp2_fast(from * c - to * c) : exp2_fast((from - to) * c); }
+template <bool USUAL>
 __device__ __forceinline__ Sums join(const Sums& x, const Sums& y, float c) {
-    const float m = fmaxf(x.m, y.m), f = rescale(x.m, m, c), g = rescale(y.m, m, c);
+    const float m = fmaxf(x.m, y.m), f = rescale<USUAL>(x.m, m, c), g = rescale<USUAL>(y.m, m, c);
     return {m, x.s * f + y.s * g, x.off * f + y.off * g};
 }
+template <bool USUAL>
 __device__ __forceinline__ Sums join_wave(const Sums& x, float c) {
-    const float m = wave_max(x.m), f = rescale(x.m, m, c);
+    const float m = wave_max(x.m), f = rescale<USUAL>(x.m, m, c);
     return {m, wave_sum(x.s * f), wave_sum(x.off * f)};
 }
-// log of the sum of exp((x - m) / T)
-__device__ __forceinline__ double log_of(float s, float m, float c) {
-    const double l = log(static_cast<double>(s));
-    return usual(m, c) ? l + (static_cast<double>(m * c) - static_cast<double>(m) * c) * 0.69314718055994530942 : l;
+__device__ __forceinline__ Sums settled(const Sums& t, float c) {
+    const float f = exp2_fast(__builtin_fmaf(-t.m, c, t.m * c));
+    return {t.m, t.s * f, t.off * f};
 }
 
 // Adds the elements of G vectors; `listed` has a bit for each listed one.  USUAL:
@@ -123,14 +128,14 @@ __device__ __forceinline__ void add_vector(Sums& t, const u32x4& v, uint32_t lis
 }
 
 // A workgroup's sums joined, in every thread.
-template <int WAVES>
+template <int WAVES, bool USUAL>
 __device__ __forceinline__ Sums join_group(const Sums& x, Sums* room, int lane, int wave, float c) {
-    const Sums w = join_wave(x, c);
+    const Sums w = join_wave<USUAL>(x, c);
     if (lane == 0) room[wave] = w;
     __syncthreads();
     Sums t = room[0];
 #pragma unroll
-    for (int h = 1; h < WAVES; ++h) t = join(t, room[h], c);
+    for (int h = 1; h < WAVES; ++h) t = join<USUAL>(t, room[h], c);
     return t;
 }
 
@@ -192,7 +197,7 @@ __device__ __forceinline__ Teacher teacher_of(const DistillArgs& a, int64_t row,
 // Loss and statistics of a row, by one wavefront.  z(j): the student's logit of place j.
 template <typename T, typename On, typename Z>
 __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, const Sums& s, const Teacher& teacher, int lane, T t, On on, Z z) {
-    const double log_s = log_of(s.s, s.m, a.c);                 // log q = (z - m) / T - log_s
+    const double log_s = log(static_cast<double>(s.s));         // log q = (z - m) / T - log_s
     double sum = 0, mass = 0, log_rest = 0;
     for (int j = lane; j < a.k; j += 64) {
         if (!on(j)) continue;
@@ -268,14 +273,16 @@ __global__ void __launch_bounds__(kThreads) distill_stats_kernel(const DistillAr
             if (id >= 0 && id < a.v && id / E >= from && id / E < to) a.z_at[row * a.k + j] = r.element(id);
         }
     }
-    Sums t{kFloor, 0.0f, 0.0f};
+    Sums t{a.floor, 0.0f, 0.0f};
     mine.each([&](const u32x4& v, int i) { add_vector<F32, REST, true>(t, v, REST ? marks_of<E>(marks, i - from) : 0, a.c); });
-    t = join_group<kWaves>(t, room[0], lane, wave, a.c);
-    if (!usual(t.m, a.c) || t.m == kFloor) {
+    t = join_group<kWaves, true>(t, room[0], lane, wave, a.c);
+    if (usual(t.m, a.floor)) {
+        t = settled(t, a.c);
+    } else {
         t = {kLowest, 0.0f, 0.0f};
         Vectors<F32> again(r, from, to);
         again.each([&](const u32x4& v, int i) { add_vector<F32, REST, false>(t, v, REST ? marks_of<E>(marks, i - from) : 0, a.c); });
-        t = join_group<kWaves>(t, room[1], lane, wave, a.c);
+        t = join_group<kWaves, false>(t, room[1], lane, wave, a.c);
     }
     if (wave != 0) return;
     if (a.chunks == 1) write_loss_of<F32>(a, row, t, lane);
@@ -284,8 +291,8 @@ __global__ void __launch_bounds__(kThreads) distill_stats_kernel(const DistillAr
 
 __device__ __forceinline__ Sums join_chunks(const DistillArgs& a, int64_t row, int lane) {
     Sums t{kLowest, 0.0f, 0.0f};
-    for (int c = lane; c < a.chunks; c += 64) t = join(t, a.part[row * a.chunks + c], a.c);
-    return join_wave(t, a.c);
+    for (int c = lane; c < a.chunks; c += 64) t = join<false>(t, a.part[row * a.chunks + c], a.c);
+    return join_wave<false>(t, a.c);
 }
 
 template <bool F32>
@@ -309,9 +316,9 @@ struct Gradient {
     float m, c, L, K, factor;
     uint32_t sign;
     bool zero, wide;
-    __device__ __forceinline__ Gradient(const Slope& s, float c_) : m(s.m), c(c_), L(s.L), factor(s.gs * s.off) {
+    __device__ __forceinline__ Gradient(const Slope& s, float c_, float floor) : m(s.m), c(c_), L(s.L), factor(s.gs * s.off) {
         // the logarithm of a factor that is neither finite nor positive is no exponent
-        wide = F32 || !usual(s.m, c) || !(fabsf(factor) > 1e-30f && fabsf(factor) < 1e30f);
+        wide = F32 || !usual(s.m, floor) || !(fabsf(factor) > 1e-30f && fabsf(factor) < 1e30f);
         K = m * c + (L - __builtin_amdgcn_logf(fabsf(factor)));
         sign = factor < 0.0f ? 0x80008000u : 0;
         zero = s.gs == 0.0f;
@@ -382,7 +389,6 @@ __device__ __forceinline__ float off_list(float rest, float ratio) { return rest
 template <bool REST>
 __device__ __forceinline__ Slope slope_of(const DistillArgs& a, float gs, const Sums& t, double mass) {
     Slope s{t.m, __builtin_amdgcn_logf(t.s), gs, static_cast<float>(mass), static_cast<float>(mass)};
-    if (usual(t.m, a.c)) s.L += __builtin_fmaf(-t.m, a.c, t.m * a.c);       // the rounding of R
     if (REST) {
         s.on = 1.0f;
         s.off = off_list(static_cast<float>(1 - mass), static_cast<float>((1 - mass) * (static_cast<double>(t.s) / t.off)));
@@ -433,7 +439,7 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
         if (a.part) {
             sums = join_chunks(a, row, lane);
             s.m = sums.m;
-            s.L = static_cast<float>(log_of(sums.s, sums.m, a.c) * 1.4426950408889634074);
+            s.L = static_cast<float>(log(static_cast<double>(sums.s)) * 1.4426950408889634074);
             s.off = static_cast<float>(static_cast<double>(sums.s) / sums.off);     // 1 / Q for now
         } else {
             s.m = a.stats[3 * row];
@@ -477,7 +483,7 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
         for (int e = 0; e < static_cast<int>(threadIdx.x); ++e)
             if (id_of[e] == id_of[threadIdx.x]) twice = 1;
     }
-    const Gradient<F32> g(s, a.c);
+    const Gradient<F32> g(s, a.c, a.floor);
     mine.each([&](const u32x4& v, int i) { w.template put<STREAM>(i, g.of(v)); });
     // what was stored above has arrived before it is written over
     __builtin_amdgcn_s_waitcnt(0);
@@ -555,21 +561,23 @@ __global__ void __launch_bounds__(THREADS) distill_row_kernel(const DistillArgs 
             mass_ = mass;
         }
     }
-    Sums t{kFloor, 0.0f, 0.0f};
+    Sums t{a.floor, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
         if (tid < whole - j * THREADS) add_vector<F32, REST, true>(t, raw[j], REST ? marks_of<E>(marks, tid + j * THREADS) : 0, a.c);
     Vectors<F32, THREADS> beyond(r, NV * THREADS, vectors);
     beyond.each([&](const u32x4& v, int i) { add_vector<F32, REST, true>(t, v, REST ? marks_of<E>(marks, i) : 0, a.c); });
-    t = join_group<THREADS / 64>(t, room[0], lane, wave, a.c);
-    if (!usual(t.m, a.c) || t.m == kFloor) {
+    t = join_group<THREADS / 64, true>(t, room[0], lane, wave, a.c);
+    if (usual(t.m, a.floor)) {
+        t = settled(t, a.c);
+    } else {
         t = {kLowest, 0.0f, 0.0f};
         for (int i = tid; i < vectors; i += THREADS) add_vector<F32, REST, false>(t, r.load(i), REST ? marks_of<E>(marks, i) : 0, a.c);
-        t = join_group<THREADS / 64>(t, room[1], lane, wave, a.c);
+        t = join_group<THREADS / 64, false>(t, room[1], lane, wave, a.c);
     }
     if (wave == 0) write_loss(a, row, t, teacher_, lane, t_at, on, [&](int j) { return z_of[j]; });
     const Slope s = slope_of<REST>(a, row_factor(a, row), t, mass_);
-    const Gradient<F32> g(s, a.c);
+    const Gradient<F32> g(s, a.c, a.floor);
     if (!F32 && g.wide) {                               // rare, and short
         for (int i = tid; i < min(whole, NV * THREADS); i += THREADS) w.store_whole(i, g.of_wide(r.load_whole(i)));
     } else {
@@ -629,6 +637,7 @@ DistillArgs device_args(const ngram_distill_args* p) {
     a.inv_t = 1.0 / p->temperature;
     a.t2 = static_cast<double>(p->temperature) * p->temperature;
     a.c = static_cast<float>(1.4426950408889634074 * a.inv_t);
+    a.floor = static_cast<float>(-std::min(0x1p20 / a.c, static_cast<double>(kLowest) * -1));
     a.chunks = chunks_of(p->n, p->V, p->dtype);
     const int64_t e = p->dtype == NGRAM_F32 ? 4 : 8, vectors = (p->V + e - 1) / e;
     a.per = static_cast<int32_t>((vectors + a.chunks - 1) / a.chunks);
