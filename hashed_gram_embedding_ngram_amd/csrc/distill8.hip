@@ -303,9 +303,10 @@ __global__ void __launch_bounds__(256) distill_finish_kernel(const DistillArgs a
 }
 
 // ---------------------------------------------------------------------------
-// The gradient: gs (a q - p), gs the row's factor.  q = 2^(x c - K), K = m c +
-// log2 of the sum: for bf16, whose result rounds by 2^-9, K as one fp32 number that takes the factor
-// too; for fp32 as 2^((x - m) c - L), which loses nothing to K's size.
+// The gradient: gs (a q - p), gs the row's factor.  q = 2^((x - m) c - L), L = log2
+// of the sum.  For bf16, whose result rounds by 2^-9, as 2^(x c - K) where |K| < 2^12: K = m c + L as one
+// fp32 number, which takes the factor too, and whose rounding of 2^-13 at most is 2^-13.5
+// of the result (at 2^16 it would be more than bf16's).
 struct Slope {
     float m, L;             // L = log2 of the sum of 2^((x - m) c)
     float gs, on, off;      // the row's factor; a of listed and of other tokens
@@ -316,10 +317,10 @@ struct Gradient {
     float m, c, L, K, factor;
     uint32_t sign;
     bool zero, wide;
-    __device__ __forceinline__ Gradient(const Slope& s, float c_, float floor) : m(s.m), c(c_), L(s.L), factor(s.gs * s.off) {
+    __device__ __forceinline__ Gradient(const Slope& s, float c_) : m(s.m), c(c_), L(s.L), factor(s.gs * s.off) {
+        K = __builtin_fmaf(m, c, L - __builtin_amdgcn_logf(fabsf(factor)));
         // the logarithm of a factor that is neither finite nor positive is no exponent
-        wide = F32 || !usual(s.m, floor) || !(fabsf(factor) > 1e-30f && fabsf(factor) < 1e30f);
-        K = m * c + (L - __builtin_amdgcn_logf(fabsf(factor)));
+        wide = F32 || !(fabsf(K) < 4096.0f) || !(fabsf(factor) > 1e-30f && fabsf(factor) < 1e30f);
         sign = factor < 0.0f ? 0x80008000u : 0;
         zero = s.gs == 0.0f;
     }
@@ -483,7 +484,7 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
         for (int e = 0; e < static_cast<int>(threadIdx.x); ++e)
             if (id_of[e] == id_of[threadIdx.x]) twice = 1;
     }
-    const Gradient<F32> g(s, a.c, a.floor);
+    const Gradient<F32> g(s, a.c);
     mine.each([&](const u32x4& v, int i) { w.template put<STREAM>(i, g.of(v)); });
     // what was stored above has arrived before it is written over
     __builtin_amdgcn_s_waitcnt(0);
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(THREADS) distill_row_kernel(const DistillArgs 
     }
     if (wave == 0) write_loss(a, row, t, teacher_, lane, t_at, on, [&](int j) { return z_of[j]; });
     const Slope s = slope_of<REST>(a, row_factor(a, row), t, mass_);
-    const Gradient<F32> g(s, a.c, a.floor);
+    const Gradient<F32> g(s, a.c);
     if (!F32 && g.wide) {                               // rare, and short
         for (int i = tid; i < min(whole, NV * THREADS); i += THREADS) w.store_whole(i, g.of_wide(r.load_whole(i)));
     } else {

@@ -703,7 +703,8 @@ int ngram_beam_reorder(const ngram_beam_state* states, int32_t count, const int3
  * is -inf throughout, or holds a NaN or +inf, gives NaN.
  * z is finite of any size (mask fills of -1e9 or the type's lowest number among them), or -inf.
  * Roundings: exp and sums in fp32, relative to the row's largest logit, sums of a fixed order, results
- * of exp below 2^-126 are 0; the teacher's side and the loss in float64, rounded once.
+ * of exp below 2^-126 are 0, a bf16 gradient's exp is off by up to 2^-13 of itself before it is rounded to
+ * 2^-9; the teacher's side and the loss in float64, rounded once.
  * Per row: loss_out; stats_out[n][3]: the largest logit m, log sum exp((z - m) / T),
  * and log Q (0 without teacher_lse), which ngram_distill_grad reads; each fp32, 4-byte aligned, NULL
  * if not wanted.  dlogits_out[n][V] (z's type, distance dld, may be z itself):

@@ -4,7 +4,9 @@ runs of tokens and rows far from zero, through every kernel, against float64.
 Tolerances are test_gpu_distill's, whose derivation does not use the logits' size: only differences to the
 row's largest logit enter it, and a fill adds 0 to the sums on both sides.  A result below 2^-126 may be 0,
 since exp2 gives no subnormal numbers: q is off by up to 2^-126 more, and the gradient by weight * scale * T * |a|
-times that (or by 2^-126, where the factor is part of the exponent)."""
+times that (or by 2^-126, where the factor is part of the exponent).  A bf16 gradient's exponent x c - K takes K =
+m c + L below 2^12, rounded to fp32 once: half a step below 2^12 is 2^-13, and 2^(2^-13) - 1 is below 2^-13 (2^-13
+ln 2 and a part in 10^4), so a q is off by 2^-13 of itself more."""
 import numpy as np
 import pytest
 
@@ -72,6 +74,7 @@ def check_all(a, dtype, loss, grad, stats, scale=0.5):
         want = ref.distill(a["z"], a["t"], a["ids"], a["T"], a["lse"], a["weight"], scale)
         w = a["weight"][:, None] * scale * a["T"]
         gb = bounds(a, scale, dtype == BF, want)[1] + 2.0 ** -126 * np.maximum(1, w * np.abs(want[3]["a"]))
+        gb = gb + (2.0 ** -13 * w * np.abs(want[3]["a"]) * want[3]["q"] if dtype == BF else 0)
         err = np.abs(grad.double().cpu().numpy() - want[2])
         assert grad.dtype == dtype and np.all(err <= gb), (err / gb).max()
 
@@ -117,3 +120,15 @@ def test_rows_far_from_zero(shape, T, rest):
     say(f"distill far {V} {dtype} T={T} rest={rest}")
     a = shifted(np.random.default_rng(V + 1), V, 9, dtype, T, rest)
     all_calls(a, dtype, n, lambda loss, grad, stats: check_all(a, dtype, loss, grad if dtype == F32 else None, stats))
+
+
+@pytest.mark.parametrize("shape,T,rest", [k for k in KINDS if k[0][0] == BF])
+def test_bf16_gradients_far_from_zero(shape, T, rest):
+    """Element by element: a gradient's exponent holds differences to the largest logit, whatever that is."""
+    dtype, V, n = shape
+    say(f"distill far gradient {V} {dtype} T={T} rest={rest}")
+    a = shifted(np.random.default_rng(V + 2), V, 9, dtype, T, rest)
+    # steps of bf16 at 2^12 T / log2 e are 16 and more; finer ones below
+    for i, x in enumerate((1000, 2000, 2500, 2839, 2840, 3000, 5000, 20000)):
+        a["z"][i] = rounded(x * T + 10 * np.random.default_rng(i).normal(size=V), dtype)
+    all_calls(a, dtype, n, lambda loss, grad, stats: check_all(a, dtype, loss, grad, stats))
