@@ -18,7 +18,7 @@ constexpr int kScan = 128;              // places of a short list
 // backward: 84 us against 97; 4096 x 151936 bf16 498 against 523); smaller ones are read next where they lie.
 constexpr int64_t kStreamFrom = int64_t{64} << 20;
 
-struct Sums;
+struct RowSums;
 
 struct DistillArgs {
     const void* z;
@@ -29,7 +29,7 @@ struct DistillArgs {
     float* stats;           // written by the forward, read by the gradient
     const float* weight;
     void* dz;
-    Sums* part;             // [n][chunks], or NULL: statistics are given
+    RowSums* part;          // [n][chunks], or NULL: statistics are given
     int64_t n, v, ld, dld;
     float* z_at;            // [n][k]: listed tokens' logits for a loss that is written beside the gradient, or NULL
     int64_t first;          // the launch's first row
@@ -66,8 +66,15 @@ __device__ __forceinline__ double wave_sum_f64(double x) {
 // exactly 0 to such a row.  Other rows (logits of hundreds of thousands and more
 // times T, masked throughout among them) are summed once more by (x - m) c.  Without the floor a thread
 // whose first vector is masked by -1e10 would hold infinity, to be multiplied with 0 later.
+//
+// With the teacher's rest the pass leaves listed tokens out and takes the unlisted ones'
+// sum about their own largest logit, however far that lies below the row's (in a sum about
+// the row's they would be 0 from 87 T on, and log Q -infinity); the listed tokens, a few, are added afterwards.
 struct Sums {
-    float m, s, off;                    // off: the unlisted tokens' part of s
+    float m, s;
+};
+struct RowSums {
+    Sums all, off;                      // of all tokens; of the unlisted ones, with the rest
 };
 
 __device__ __forceinline__ bool usual(float m, float floor) { return fabsf(m) <= -0.5f * floor; }
@@ -77,19 +84,18 @@ __device__ __forceinline__ float rescale(float from, float to, float c) { return
 template <bool USUAL>
 __device__ __forceinline__ Sums join(const Sums& x, const Sums& y, float c) {
     const float m = fmaxf(x.m, y.m), f = rescale<USUAL>(x.m, m, c), g = rescale<USUAL>(y.m, m, c);
-    return {m, x.s * f + y.s * g, x.off * f + y.off * g};
+    return {m, x.s * f + y.s * g};
 }
 template <bool USUAL>
 __device__ __forceinline__ Sums join_wave(const Sums& x, float c) {
     const float m = wave_max(x.m), f = rescale<USUAL>(x.m, m, c);
-    return {m, wave_sum(x.s * f), wave_sum(x.off * f)};
+    return {m, wave_sum(x.s * f)};
 }
 __device__ __forceinline__ Sums settled(const Sums& t, float c) {
-    const float f = exp2_fast(__builtin_fmaf(-t.m, c, t.m * c));
-    return {t.m, t.s * f, t.off * f};
+    return {t.m, t.s * exp2_fast(__builtin_fmaf(-t.m, c, t.m * c))};
 }
 
-// Adds the elements of G vectors; `listed` has a bit for each listed one.  USUAL:
+// Adds the elements of G vectors, with REST but for those that have a bit in `listed`.  USUAL:
 // x c - R, else (x - m) c.  One rescaling for all of them, and sums by pairs, so
 // that few of the instructions wait for each other.
 template <bool F32, bool REST, bool USUAL, int G>
@@ -100,22 +106,13 @@ __device__ __forceinline__ void add_vectors(Sums& t, const u32x4 (&v)[G], const 
 #pragma unroll
     for (int k = 0; k < G * E; ++k) {
         x[k] = Row<F32>::at(v[k / E], k % E);
+        if (REST) x[k] = listed[k / E] & (1u << (k % E)) ? kNegInf : x[k];
         top = fmaxf(top, x[k]);
     }
     const float R = top * c, f = USUAL ? exp2_fast(t.m * c - R) : exp2_fast((t.m - top) * c);
     t.m = top;
 #pragma unroll
     for (int k = 0; k < G * E; ++k) x[k] = USUAL ? exp2_fast(__builtin_fmaf(x[k], c, -R)) : exp2_fast((x[k] - top) * c);
-    if (REST) {
-        float y[G * E];
-#pragma unroll
-        for (int k = 0; k < G * E; ++k) y[k] = listed[k / E] & (1u << (k % E)) ? 0.0f : x[k];
-#pragma unroll
-        for (int n = G * E / 2; n > 0; n /= 2)
-#pragma unroll
-            for (int k = 0; k < n; ++k) y[k] += y[k + n];
-        t.off = __builtin_fmaf(t.off, f, y[0]);
-    }
 #pragma unroll
     for (int n = G * E / 2; n > 0; n /= 2)
 #pragma unroll
@@ -137,6 +134,22 @@ __device__ __forceinline__ Sums join_group(const Sums& x, Sums* room, int lane, 
 #pragma unroll
     for (int h = 1; h < WAVES; ++h) t = join<USUAL>(t, room[h], c);
     return t;
+}
+// A row's (or its part's) sums, in every thread: t from the pass over its vectors, or again() of a second
+// pass by differences; with REST `on` has this thread's listed tokens, `places` of them in the list.
+template <int WAVES, bool REST, typename Again>
+__device__ __forceinline__ RowSums finish_sums(const DistillArgs& a, Sums t, Sums on, int places, Sums (*room)[WAVES], int lane, int wave, Again again) {
+    if (REST) {
+        const Sums w = join_wave<false>(on, a.c);
+        if (lane == 0) room[2][wave] = w;
+    }
+    t = join_group<WAVES, true>(t, room[0], lane, wave, a.c);
+    if (usual(t.m, a.floor)) t = settled(t, a.c);
+    else t = join_group<WAVES, false>(again(), room[1], lane, wave, a.c);
+    if (!REST) return {t, {kLowest, 0.0f}};
+    on = room[2][0];
+    for (int h = 1; h < min(WAVES, (places + 63) / 64); ++h) on = join<false>(on, room[2][h], a.c);
+    return {join<false>(on, t, a.c), t};
 }
 
 // This thread's vectors of from .. to - 1, kAhead loads at a time in flight;
@@ -196,7 +209,8 @@ __device__ __forceinline__ Teacher teacher_of(const DistillArgs& a, int64_t row,
 
 // Loss and statistics of a row, by one wavefront.  z(j): the student's logit of place j.
 template <typename T, typename On, typename Z>
-__device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, const Sums& s, const Teacher& teacher, int lane, T t, On on, Z z) {
+__device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, const RowSums& sums, const Teacher& teacher, int lane, T t, On on, Z z) {
+    const Sums s = sums.all, off = sums.off;
     const double log_s = log(static_cast<double>(s.s));         // log q = (z - m) / T - log_s
     double sum = 0, mass = 0, log_rest = 0;
     for (int j = lane; j < a.k; j += 64) {
@@ -208,7 +222,7 @@ __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, co
     sum = wave_sum_f64(sum);
     if (a.teacher_lse) {
         const double rest = 1 - wave_sum_f64(mass);
-        log_rest = log(static_cast<double>(s.off)) - log(static_cast<double>(s.s));
+        log_rest = (static_cast<double>(off.m) - s.m) * a.inv_t + (log(static_cast<double>(off.s)) - log_s);
         if (!(rest <= 0)) sum += rest * (log(rest) - log_rest);
     }
     if (lane == 0) {
@@ -222,7 +236,7 @@ __device__ __forceinline__ void write_loss(const DistillArgs& a, int64_t row, co
     }
 }
 template <bool F32>
-__device__ void write_loss_of(const DistillArgs& a, int64_t row, const Sums& s, int lane) {
+__device__ void write_loss_of(const DistillArgs& a, int64_t row, const RowSums& s, int lane) {
     const Row<F32> r(a.z, row * a.ld, a.v);
     const int32_t* const ids = a.ids + row * a.k;
     const auto t = [&](int j) { return teacher_at(a, row * a.k + j); };
@@ -248,6 +262,12 @@ __device__ __forceinline__ void mark_listed(const DistillArgs& a, int64_t row, i
     }
     __syncthreads();
 }
+// Whether the token of place j has a place before it.
+__device__ __forceinline__ bool listed_before(const int32_t* ids, int j) {
+    for (int e = 0; e < j; ++e)
+        if (ids[e] == ids[j]) return true;
+    return false;
+}
 template <int E>
 __device__ __forceinline__ uint32_t marks_of(const uint32_t* marks, int vector) { return marks[(vector * E) >> 5] >> ((vector * E) & 31); }
 
@@ -256,7 +276,7 @@ __device__ __forceinline__ uint32_t marks_of(const uint32_t* marks, int vector) 
 template <bool F32, bool REST>
 __global__ void __launch_bounds__(kThreads) distill_stats_kernel(const DistillArgs a) {
     constexpr int E = Row<F32>::E;
-    __shared__ Sums room[2][kWaves];
+    __shared__ Sums room[3][kWaves];
     __shared__ uint32_t marks[REST ? kBitVectors * E / 32 : 1];
     __shared__ int twice;
     const int lane = threadIdx.x & 63;
@@ -267,39 +287,48 @@ __global__ void __launch_bounds__(kThreads) distill_stats_kernel(const DistillAr
     const int from = chunk * a.per, to = min(r.vectors(), from + a.per);
     Vectors<F32> mine(r, from, to);
     if (REST) mark_listed<E>(a, row, from, to, marks, &twice);
-    if (a.z_at) {                       // the gradient may take the logits' place
+    Sums on{kLowest, 0.0f};
+    if (REST || a.z_at) {               // z_at: the gradient may take the logits' place
+        const int32_t* const ids = a.ids + row * a.k;
         for (int j = threadIdx.x; j < a.k; j += kThreads) {
-            const int id = a.ids[row * a.k + j];
-            if (id >= 0 && id < a.v && id / E >= from && id / E < to) a.z_at[row * a.k + j] = r.element(id);
+            const int id = ids[j];
+            if (id < 0 || id >= a.v || id / E < from || id / E >= to) continue;
+            const float z = r.element(id);
+            if (a.z_at) a.z_at[row * a.k + j] = z;
+            if (REST && !(twice && listed_before(ids, j))) on = join<false>(on, {z, 1.0f}, a.c);
         }
     }
-    Sums t{a.floor, 0.0f, 0.0f};
+    Sums t{a.floor, 0.0f};
     mine.each([&](const u32x4& v, int i) { add_vector<F32, REST, true>(t, v, REST ? marks_of<E>(marks, i - from) : 0, a.c); });
-    t = join_group<kWaves, true>(t, room[0], lane, wave, a.c);
-    if (usual(t.m, a.floor)) {
-        t = settled(t, a.c);
-    } else {
-        t = {kLowest, 0.0f, 0.0f};
+    const RowSums sums = finish_sums<kWaves, REST>(a, t, on, a.k, room, lane, wave, [&] {
+        Sums u{kLowest, 0.0f};
         Vectors<F32> again(r, from, to);
-        again.each([&](const u32x4& v, int i) { add_vector<F32, REST, false>(t, v, REST ? marks_of<E>(marks, i - from) : 0, a.c); });
-        t = join_group<kWaves, false>(t, room[1], lane, wave, a.c);
-    }
+        again.each([&](const u32x4& v, int i) { add_vector<F32, REST, false>(u, v, REST ? marks_of<E>(marks, i - from) : 0, a.c); });
+        return u;
+    });
     if (wave != 0) return;
-    if (a.chunks == 1) write_loss_of<F32>(a, row, t, lane);
-    else if (lane == 0) a.part[row * a.chunks + chunk] = t;
+    if (a.chunks == 1) write_loss_of<F32>(a, row, sums, lane);
+    else if (lane == 0) a.part[row * a.chunks + chunk] = sums;
 }
 
-__device__ __forceinline__ Sums join_chunks(const DistillArgs& a, int64_t row, int lane) {
-    Sums t{kLowest, 0.0f, 0.0f};
-    for (int c = lane; c < a.chunks; c += 64) t = join<false>(t, a.part[row * a.chunks + c], a.c);
-    return join_wave<false>(t, a.c);
+template <bool REST>
+__device__ __forceinline__ RowSums join_chunks(const DistillArgs& a, int64_t row, int lane) {
+    RowSums t{{kLowest, 0.0f}, {kLowest, 0.0f}};
+    for (int c = lane; c < a.chunks; c += 64) {
+        const RowSums p = a.part[row * a.chunks + c];
+        t.all = join<false>(t.all, p.all, a.c);
+        if (REST) t.off = join<false>(t.off, p.off, a.c);
+    }
+    t.all = join_wave<false>(t.all, a.c);
+    if (REST) t.off = join_wave<false>(t.off, a.c);
+    return t;
 }
 
 template <bool F32>
 __global__ void __launch_bounds__(256) distill_finish_kernel(const DistillArgs a) {
     const int lane = threadIdx.x & 63;
     const int64_t row = a.first + static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (row < a.n) write_loss_of<F32>(a, row, join_chunks(a, row, lane), lane);
+    if (row < a.n) write_loss_of<F32>(a, row, a.teacher_lse ? join_chunks<true>(a, row, lane) : join_chunks<false>(a, row, lane), lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -307,9 +336,13 @@ __global__ void __launch_bounds__(256) distill_finish_kernel(const DistillArgs a
 // of the sum.  For bf16, whose result rounds by 2^-9, as 2^(x c - K) where |K| < 2^12: K = m c + L as one
 // fp32 number, which takes the factor too, and whose rounding of 2^-13 at most is 2^-13.5
 // of the result (at 2^16 it would be more than bf16's).
+//
+// Off the list with the teacher's rest a = 1 - P / Q (1 where P or Q is 0), and a q is (Q - P) times the
+// unlisted tokens' own softmax, which stands where Q is too small for a number.
 struct Slope {
-    float m, L;             // L = log2 of the sum of 2^((x - m) c)
-    float gs, on, off;      // the row's factor; a of listed and of other tokens
+    float m, L;                     // L = log2 of the sum of 2^((x - m) c)
+    float gs, on;                   // the row's factor; a of listed tokens
+    float off_m, off_L, factor;     // of other tokens: factor 2^((x - off_m) c - off_L)
 };
 
 template <bool F32>
@@ -317,7 +350,7 @@ struct Gradient {
     float m, c, L, K, factor;
     uint32_t sign;
     bool zero, wide;
-    __device__ __forceinline__ Gradient(const Slope& s, float c_) : m(s.m), c(c_), L(s.L), factor(s.gs * s.off) {
+    __device__ __forceinline__ Gradient(const Slope& s, float c_) : m(s.off_m), c(c_), L(s.off_L), factor(s.factor) {
         K = __builtin_fmaf(m, c, L - __builtin_amdgcn_logf(fabsf(factor)));
         // the logarithm of a factor that is neither finite nor positive is no exponent
         wide = F32 || !(fabsf(K) < 4096.0f) || !(fabsf(factor) > 1e-30f && fabsf(factor) < 1e30f);
@@ -383,16 +416,39 @@ __device__ __forceinline__ void write_listed(const Row<F32>& w, const Slope& s, 
     put_listed<F32>(w, s, c, id, p, z);
 }
 
-// a of the tokens off the list: `ratio` = P / Q
-__device__ __forceinline__ float off_list(float rest, float ratio) { return rest > 0.0f && ratio < __builtin_inff() ? 1.0f - ratio : 1.0f; }
+// Q - P, or Q where there is nothing to share out: no rest, or nobody to take it.
+__device__ __forceinline__ float share(float q, double rest, bool nobody) { return rest <= 0 || nobody ? q : static_cast<float>(q - rest); }
 
 // From a row's sums; mass = sum of p.
 template <bool REST>
-__device__ __forceinline__ Slope slope_of(const DistillArgs& a, float gs, const Sums& t, double mass) {
-    Slope s{t.m, __builtin_amdgcn_logf(t.s), gs, static_cast<float>(mass), static_cast<float>(mass)};
+__device__ __forceinline__ Slope slope_of(const DistillArgs& a, float gs, const RowSums& t, double mass) {
+    Slope s{t.all.m, __builtin_amdgcn_logf(t.all.s), gs, static_cast<float>(mass), 0, 0, 0};
+    s.off_m = s.m;
+    s.off_L = s.L;
+    s.factor = gs * s.on;
     if (REST) {
+        const bool nobody = t.off.s == 0.0f;
         s.on = 1.0f;
-        s.off = off_list(static_cast<float>(1 - mass), static_cast<float>((1 - mass) * (static_cast<double>(t.s) / t.off)));
+        s.off_m = t.off.m;
+        s.off_L = nobody ? 0.0f : __builtin_amdgcn_logf(t.off.s);
+        s.factor = gs * share(t.off.s / t.all.s * rescale<false>(t.off.m, t.all.m, a.c), 1 - mass, nobody);
+    }
+    return s;
+}
+// From the forward's statistics: the unlisted tokens' softmax about the row's largest logit, which loses log Q's
+// rounding and its own, as much as log Q is large; from kFar on the row is summed once more.
+constexpr float kFar = -64.0f;
+__device__ __forceinline__ bool far_rest(float log_q) { return log_q < kFar && log_q > kNegInf; }
+template <bool REST>
+__device__ __forceinline__ Slope slope_given(float m, float log_s, float log_q, float q, float gs, double mass) {
+    Slope s{m, log_s * kLog2e, gs, static_cast<float>(mass), m, 0, 0};
+    s.off_L = s.L;
+    s.factor = gs * s.on;
+    if (REST) {
+        const bool nobody = log_q == kNegInf;
+        s.on = 1.0f;
+        s.off_L = nobody ? 0.0f : static_cast<float>((static_cast<double>(log_s) + log_q) * 1.4426950408889634074);
+        s.factor = gs * share(q, 1 - mass, nobody);
     }
     return s;
 }
@@ -412,14 +468,15 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
     __shared__ int twice;
     __shared__ Teacher teacher_;
     __shared__ double mass_;
-    __shared__ Slope slope_;
-    __shared__ Sums sums_;
+    __shared__ RowSums sums_;
+    __shared__ float stats_[4];                 // with Q
+    __shared__ Sums room[kWaves];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t row = a.first + blockIdx.x / a.chunks;
     const int chunk = static_cast<int>(blockIdx.x % a.chunks);
     const Row<F32> r(a.z, row * a.ld, a.v), w(a.dz, row * a.dld, a.v);
-    const int from = chunk * a.per, to = min(w.vectors(), from + a.per);
+    int from = chunk * a.per, to = min(w.vectors(), from + a.per);
     Vectors<F32> mine(r, from, to);
     const int32_t* const ids = a.ids + row * a.k;
     const auto t_at = [&](int j) { return teacher_at(a, row * a.k + j); };
@@ -435,21 +492,13 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
             mass_ = mass;
         }
     } else if (wave == 1) {
-        Slope s{0, 0, row_factor(a, row), 0, 0};
-        Sums sums{0, 0, 0};
         if (a.part) {
-            sums = join_chunks(a, row, lane);
-            s.m = sums.m;
-            s.L = static_cast<float>(log(static_cast<double>(sums.s)) * 1.4426950408889634074);
-            s.off = static_cast<float>(static_cast<double>(sums.s) / sums.off);     // 1 / Q for now
-        } else {
-            s.m = a.stats[3 * row];
-            s.L = a.stats[3 * row + 1] * kLog2e;
-            s.off = static_cast<float>(exp(-static_cast<double>(a.stats[3 * row + 2])));
-        }
-        if (lane == 0) {
-            slope_ = s;
-            sums_ = sums;
+            const RowSums sums = join_chunks<REST>(a, row, lane);
+            if (lane == 0) sums_ = sums;
+        } else if (lane < 3) {
+            const float x = a.stats[3 * row + lane];
+            stats_[lane] = x;
+            if (REST && lane == 2) stats_[3] = static_cast<float>(exp(static_cast<double>(x)));
         }
     }
     if (a.k > kScan) {
@@ -458,10 +507,14 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
         if (threadIdx.x == 0) twice = 0;
         __syncthreads();
     }
-    Slope s = slope_;
-    s.on = static_cast<float>(mass_);
-    s.off = REST ? off_list(static_cast<float>(1 - mass_), static_cast<float>((1 - mass_) * s.off)) : s.on;
-    if (REST) s.on = 1.0f;
+    const float gs = row_factor(a, row);
+    Slope s = a.part ? slope_of<REST>(a, gs, sums_, mass_) : slope_given<REST>(stats_[0], stats_[1], stats_[2], stats_[3], gs, mass_);
+    const bool far = REST && !a.part && far_rest(stats_[2]);
+    if (far) {                                  // the row is its first workgroup's: others must not write what that one reads
+        if (chunk != 0) return;
+        from = 0;
+        to = w.vectors();
+    }
     const Teacher teacher = teacher_;
     // this thread's listed tokens
     constexpr int PER = kMaxK / kThreads;
@@ -484,8 +537,26 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
         for (int e = 0; e < static_cast<int>(threadIdx.x); ++e)
             if (id_of[e] == id_of[threadIdx.x]) twice = 1;
     }
-    const Gradient<F32> g(s, a.c);
-    mine.each([&](const u32x4& v, int i) { w.template put<STREAM>(i, g.of(v)); });
+    if (far) {
+        Sums t{kLowest, 0.0f};
+        for (int at = 0; at < to; at += kBitVectors) {
+            const int end = min(to, at + kBitVectors);
+            __syncthreads();                    // marks and `twice` of before are read
+            mark_listed<E>(a, row, at, end, marks, &twice);
+            for (int i = at + static_cast<int>(threadIdx.x); i < end; i += kThreads)
+                add_vector<F32, true, false>(t, r.load(i), marks_of<E>(marks, i - at), a.c);
+        }
+        t = join_group<kWaves, false>(t, room, lane, wave, a.c);
+        s.off_m = t.m;
+        s.off_L = __builtin_amdgcn_logf(t.s);
+        if (threadIdx.x == 0) twice = 1;        // in one of the ranges or not
+        const Gradient<F32> g(s, a.c);
+        Vectors<F32> all(r, from, to);
+        all.each([&](const u32x4& v, int i) { w.template put<STREAM>(i, g.of(v)); });
+    } else {
+        const Gradient<F32> g(s, a.c);
+        mine.each([&](const u32x4& v, int i) { w.template put<STREAM>(i, g.of(v)); });
+    }
     // what was stored above has arrived before it is written over
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
@@ -514,7 +585,7 @@ template <bool F32, bool REST, bool STREAM, int THREADS, int NV>
 __global__ void __launch_bounds__(THREADS) distill_row_kernel(const DistillArgs a) {
     constexpr int E = Row<F32>::E;
     extern __shared__ uint32_t marks[];                 // v / 32 + 1
-    __shared__ Sums room[2][THREADS / 64];
+    __shared__ Sums room[3][THREADS / 64];
     __shared__ int32_t id_of[kMaxK];
     __shared__ float t_of[kMaxK], z_of[kMaxK], p_of[kMaxK];
     __shared__ int twice;
@@ -562,22 +633,23 @@ __global__ void __launch_bounds__(THREADS) distill_row_kernel(const DistillArgs 
             mass_ = mass;
         }
     }
-    Sums t{a.floor, 0.0f, 0.0f};
+    Sums t{a.floor, 0.0f}, listed{kLowest, 0.0f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
         if (tid < whole - j * THREADS) add_vector<F32, REST, true>(t, raw[j], REST ? marks_of<E>(marks, tid + j * THREADS) : 0, a.c);
     Vectors<F32, THREADS> beyond(r, NV * THREADS, vectors);
     beyond.each([&](const u32x4& v, int i) { add_vector<F32, REST, true>(t, v, REST ? marks_of<E>(marks, i) : 0, a.c); });
-    t = join_group<THREADS / 64, true>(t, room[0], lane, wave, a.c);
-    if (usual(t.m, a.floor)) {
-        t = settled(t, a.c);
-    } else {
-        t = {kLowest, 0.0f, 0.0f};
-        for (int i = tid; i < vectors; i += THREADS) add_vector<F32, REST, false>(t, r.load(i), REST ? marks_of<E>(marks, i) : 0, a.c);
-        t = join_group<THREADS / 64, false>(t, room[1], lane, wave, a.c);
+    if (REST) {
+        for (int j = tid; j < a.k; j += THREADS)
+            if (on(j) && !(twice && listed_before(id_of, j))) listed = join<false>(listed, {z_of[j], 1.0f}, a.c);
     }
-    if (wave == 0) write_loss(a, row, t, teacher_, lane, t_at, on, [&](int j) { return z_of[j]; });
-    const Slope s = slope_of<REST>(a, row_factor(a, row), t, mass_);
+    const RowSums sums = finish_sums<THREADS / 64, REST>(a, t, listed, a.k, room, lane, wave, [&] {
+        Sums u{kLowest, 0.0f};
+        for (int i = tid; i < vectors; i += THREADS) add_vector<F32, REST, false>(u, r.load(i), REST ? marks_of<E>(marks, i) : 0, a.c);
+        return u;
+    });
+    if (wave == 0) write_loss(a, row, sums, teacher_, lane, t_at, on, [&](int j) { return z_of[j]; });
+    const Slope s = slope_of<REST>(a, row_factor(a, row), sums, mass_);
     const Gradient<F32> g(s, a.c);
     if (!F32 && g.wide) {                               // rare, and short
         for (int i = tid; i < min(whole, NV * THREADS); i += THREADS) w.store_whole(i, g.of_wide(r.load_whole(i)));
@@ -712,7 +784,7 @@ Room room_of(int64_t n, int64_t v, int64_t k, int dtype) {
     const auto round = [](int64_t b) { return (b + 15) / 16 * 16; };
     const int64_t chunks = chunks_of(n, v, dtype);
     r.part = 0;
-    r.stats = chunks > 1 ? round(n * chunks * static_cast<int64_t>(sizeof(Sums))) : 0;
+    r.stats = chunks > 1 ? round(n * chunks * static_cast<int64_t>(sizeof(RowSums))) : 0;
     r.z_at = r.stats + round(n * 12);
     r.total = r.z_at + (chunks > 1 ? round(n * k * 4) : 0);
     return r;
@@ -746,7 +818,7 @@ int ngram_distill(const ngram_distill_args* p, float* loss_out, float* stats_out
         return fail(NGRAM_EINVAL, "workspace must hold %lld bytes, 16-byte aligned", (long long)room.total);
     char* const at = static_cast<char*>(workspace);
     a.loss = loss_out;
-    a.part = reinterpret_cast<Sums*>(at + room.part);
+    a.part = reinterpret_cast<RowSums*>(at + room.part);
     a.stats = stats_out ? stats_out : reinterpret_cast<float*>(at + room.stats);
     a.weight = weight; a.scale = static_cast<float>(static_cast<double>(scale) * p->temperature); a.dz = dlogits_out; a.dld = dld;
     const bool f32 = p->dtype == NGRAM_F32;

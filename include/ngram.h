@@ -702,11 +702,13 @@ int ngram_beam_reorder(const ngram_beam_state* states, int32_t count, const int3
  * student that gives a token of p > 0 no chance has an infinite loss; a row of z that
  * is -inf throughout, or holds a NaN or +inf, gives NaN.
  * z is finite of any size (mask fills of -1e9 or the type's lowest number among them), or -inf.
+ * log Q and a q off the list, (Q - P) times the unlisted tokens' own softmax, stand however small Q is.
  * Roundings: exp and sums in fp32, relative to the row's largest logit, sums of a fixed order, results
  * of exp below 2^-126 are 0, a bf16 gradient's exp is off by up to 2^-13 of itself before it is rounded to
  * 2^-9; the teacher's side and the loss in float64, rounded once.
  * Per row: loss_out; stats_out[n][3]: the largest logit m, log sum exp((z - m) / T),
- * and log Q (0 without teacher_lse), which ngram_distill_grad reads; each fp32, 4-byte aligned, NULL
+ * and log Q (0 without teacher_lse), which ngram_distill_grad reads (it sums a row once more where log Q
+ * is below -64, which an fp32 log Q would show in the unlisted tokens' gradient); each fp32, 4-byte aligned, NULL
  * if not wanted.  dlogits_out[n][V] (z's type, distance dld, may be z itself):
  * weight[i] * scale * dloss/dz (weight NULL: 1), for a loss that is the sum of
  * weight[i] * scale * loss[i]; a row with weight * scale 0 gets zeros, whatever its logits hold.
