@@ -695,11 +695,24 @@ int check_args(const ngram_distill_args* p) {
     return NGRAM_OK;
 }
 
+// Whether rows of dz share bytes with rows of z: two ranges that meet share some unless their rows lie as far apart, each
+// in the gaps of the other's.
+bool overlap(const ngram_distill_args* p, const void* dz, int64_t dld) {
+    const __int128 e = p->dtype == NGRAM_F32 ? 4 : 2, row = p->V * e, ld = p->ld * e, dl = dld * e, n = p->n;
+    const __int128 off = static_cast<__int128>(reinterpret_cast<uintptr_t>(dz)) - static_cast<__int128>(reinterpret_cast<uintptr_t>(p->logits));
+    if (off >= (n - 1) * ld + row || -off >= (n - 1) * dl + row) return false;
+    if (n == 1 || ld != dl) return true;
+    const __int128 at = (off % ld + ld) % ld;
+    return at < row || ld - at < row;
+}
+
 int check_grad(const ngram_distill_args* p, const float* weight, float scale, const void* dz, int64_t dld) {
     if (dld < p->V) return fail(NGRAM_EINVAL, "dld=%lld is below V=%lld", (long long)dld, (long long)p->V);
     if (dz && dz == p->logits && dld != p->ld) return fail(NGRAM_EINVAL, "dlogits_out takes logits' place, but dld=%lld is not ld=%lld", (long long)dld, (long long)p->ld);
     if (!std::isfinite(scale)) return fail(NGRAM_EINVAL, "scale=%g must be finite", scale);
     if (!aligned(dz, p->dtype == NGRAM_F32 ? 4 : 2) || !aligned(weight, 4)) return fail(NGRAM_EALIGN, "dlogits_out or weight is not aligned to its elements");
+    // workgroups read a row while others write theirs
+    if (p->n > 0 && dz && dz != p->logits && overlap(p, dz, dld)) return fail(NGRAM_EINVAL, "dlogits_out overlaps logits without being logits");
     return NGRAM_OK;
 }
 

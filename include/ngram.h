@@ -709,7 +709,8 @@ int ngram_beam_reorder(const ngram_beam_state* states, int32_t count, const int3
  * Per row: loss_out; stats_out[n][3]: the largest logit m, log sum exp((z - m) / T),
  * and log Q (0 without teacher_lse), which ngram_distill_grad reads (it sums a row once more where log Q
  * is below -64, which an fp32 log Q would show in the unlisted tokens' gradient); each fp32, 4-byte aligned, NULL
- * if not wanted.  dlogits_out[n][V] (z's type, distance dld, may be z itself):
+ * if not wanted.  dlogits_out[n][V] (z's type, distance dld, may be z itself
+ * with the same distance, else shares no byte with it: refused):
  * weight[i] * scale * dloss/dz (weight NULL: 1), for a loss that is the sum of
  * weight[i] * scale * loss[i]; a row with weight * scale 0 gets zeros, whatever its logits hold.
  * z: any distance ld >= V elements between rows, element-aligned; t [n][k]
