@@ -136,9 +136,9 @@ __device__ __forceinline__ Sums join_group(const Sums& x, Sums* room, int lane, 
     return t;
 }
 // A row's (or its part's) sums, in every thread: t from the pass over its vectors, or again() of a second
-// pass by differences; with REST `on` has this thread's listed tokens, `places` of them in the list.
+// pass by differences; with REST `on` has this thread's listed tokens (listed_sums).
 template <int WAVES, bool REST, typename Again>
-__device__ __forceinline__ RowSums finish_sums(const DistillArgs& a, Sums t, Sums on, int places, Sums (*room)[WAVES], int lane, int wave, Again again) {
+__device__ __forceinline__ RowSums finish_sums(const DistillArgs& a, Sums t, Sums on, bool twice, Sums (*room)[WAVES], int lane, int wave, Again again) {
     if (REST) {
         const Sums w = join_wave<false>(on, a.c);
         if (lane == 0) room[2][wave] = w;
@@ -148,7 +148,8 @@ __device__ __forceinline__ RowSums finish_sums(const DistillArgs& a, Sums t, Sum
     else t = join_group<WAVES, false>(again(), room[1], lane, wave, a.c);
     if (!REST) return {t, {kLowest, 0.0f}};
     on = room[2][0];
-    for (int h = 1; h < min(WAVES, (places + 63) / 64); ++h) on = join<false>(on, room[2][h], a.c);
+    const int holding = twice ? WAVES : min(WAVES, (a.k + 63) / 64);        // wavefronts that hold listed tokens
+    for (int h = 1; h < holding; ++h) on = join<false>(on, room[2][h], a.c);
     return {join<false>(on, t, a.c), t};
 }
 
@@ -262,14 +263,23 @@ __device__ __forceinline__ void mark_listed(const DistillArgs& a, int64_t row, i
     }
     __syncthreads();
 }
-// Whether the token of place j has a place before it.
-__device__ __forceinline__ bool listed_before(const int32_t* ids, int j) {
-    for (int e = 0; e < j; ++e)
-        if (ids[e] == ids[j]) return true;
-    return false;
-}
 template <int E>
 __device__ __forceinline__ uint32_t marks_of(const uint32_t* marks, int vector) { return marks[(vector * E) >> 5] >> ((vector * E) & 31); }
+
+// This thread's share of the listed tokens' sum.  Places hold a token each and z(j) is that of
+// place j; where some token has several, marked tokens are taken in their order, each once.
+template <bool F32, typename On, typename Z>
+__device__ __forceinline__ Sums listed_sums(const DistillArgs& a, const Row<F32>& r, const uint32_t* marks, int words, int first, bool twice, On on, Z z) {
+    Sums t{kLowest, 0.0f};
+    if (!twice) {
+        for (int j = threadIdx.x; j < a.k; j += blockDim.x)
+            if (on(j)) t = join<false>(t, {z(j), 1.0f}, a.c);
+        return t;
+    }
+    for (int i = threadIdx.x; i < words; i += blockDim.x)
+        for (uint32_t bits = marks[i]; bits != 0; bits &= bits - 1) t = join<false>(t, {r.element(first + 32 * i + __builtin_ctz(bits)), 1.0f}, a.c);
+    return t;
+}
 
 // The sums of a chunk of a row; the row's loss where it is one chunk.  1021 x
 // 32003 fp32 with the rest: 29 us, 4.5 TB/s, bound by memory and the marks in LDS.
@@ -278,6 +288,7 @@ __global__ void __launch_bounds__(kThreads) distill_stats_kernel(const DistillAr
     constexpr int E = Row<F32>::E;
     __shared__ Sums room[3][kWaves];
     __shared__ uint32_t marks[REST ? kBitVectors * E / 32 : 1];
+    __shared__ float z_of[REST ? kMaxK : 1];
     __shared__ int twice;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -287,28 +298,35 @@ __global__ void __launch_bounds__(kThreads) distill_stats_kernel(const DistillAr
     const int from = chunk * a.per, to = min(r.vectors(), from + a.per);
     Vectors<F32> mine(r, from, to);
     if (REST) mark_listed<E>(a, row, from, to, marks, &twice);
-    Sums on{kLowest, 0.0f};
-    if (REST || a.z_at) {               // z_at: the gradient may take the logits' place
-        const int32_t* const ids = a.ids + row * a.k;
+    const int32_t* const ids = a.ids + row * a.k;
+    const auto on = [&](int j) { return ids[j] >= 0 && ids[j] < a.v; };
+    const auto here = [&](int j) { return on(j) && ids[j] / E >= from && ids[j] / E < to; };
+    Sums t{a.floor, 0.0f}, listed{kLowest, 0.0f};
+    mine.each([&](const u32x4& v, int i) { add_vector<F32, REST, true>(t, v, REST ? marks_of<E>(marks, i - from) : 0, a.c); });
+    if (REST || a.z_at) {               // behind the loop: the caches have them now.  z_at: the gradient may take the logits' place
         for (int j = threadIdx.x; j < a.k; j += kThreads) {
-            const int id = ids[j];
-            if (id < 0 || id >= a.v || id / E < from || id / E >= to) continue;
-            const float z = r.element(id);
+            if (!here(j)) continue;
+            const float z = r.element(ids[j]);
             if (a.z_at) a.z_at[row * a.k + j] = z;
-            if (REST && !(twice && listed_before(ids, j))) on = join<false>(on, {z, 1.0f}, a.c);
+            if (REST) z_of[j] = z;
         }
     }
-    Sums t{a.floor, 0.0f};
-    mine.each([&](const u32x4& v, int i) { add_vector<F32, REST, true>(t, v, REST ? marks_of<E>(marks, i - from) : 0, a.c); });
-    const RowSums sums = finish_sums<kWaves, REST>(a, t, on, a.k, room, lane, wave, [&] {
+    if (REST) listed = listed_sums(a, r, marks, ((to - from) * E + 31) / 32, from * E, twice, here, [&](int j) { return z_of[j]; });
+    const RowSums sums = finish_sums<kWaves, REST>(a, t, listed, REST && twice, room, lane, wave, [&] {
         Sums u{kLowest, 0.0f};
         Vectors<F32> again(r, from, to);
         again.each([&](const u32x4& v, int i) { add_vector<F32, REST, false>(u, v, REST ? marks_of<E>(marks, i - from) : 0, a.c); });
         return u;
     });
     if (wave != 0) return;
-    if (a.chunks == 1) write_loss_of<F32>(a, row, sums, lane);
-    else if (lane == 0) a.part[row * a.chunks + chunk] = sums;
+    if (a.chunks > 1) {
+        if (lane == 0) a.part[row * a.chunks + chunk] = sums;
+    } else if (REST) {
+        const auto t_at = [&](int j) { return teacher_at(a, row * a.k + j); };
+        write_loss(a, row, sums, teacher_of(a, row, lane, t_at, on), lane, t_at, on, [&](int j) { return z_of[j]; });
+    } else {
+        write_loss_of<F32>(a, row, sums, lane);
+    }
 }
 
 template <bool REST>
@@ -639,11 +657,8 @@ __global__ void __launch_bounds__(THREADS) distill_row_kernel(const DistillArgs 
         if (tid < whole - j * THREADS) add_vector<F32, REST, true>(t, raw[j], REST ? marks_of<E>(marks, tid + j * THREADS) : 0, a.c);
     Vectors<F32, THREADS> beyond(r, NV * THREADS, vectors);
     beyond.each([&](const u32x4& v, int i) { add_vector<F32, REST, true>(t, v, REST ? marks_of<E>(marks, i) : 0, a.c); });
-    if (REST) {
-        for (int j = tid; j < a.k; j += THREADS)
-            if (on(j) && !(twice && listed_before(id_of, j))) listed = join<false>(listed, {z_of[j], 1.0f}, a.c);
-    }
-    const RowSums sums = finish_sums<THREADS / 64, REST>(a, t, listed, a.k, room, lane, wave, [&] {
+    if (REST) listed = listed_sums(a, r, marks, static_cast<int>(a.v) / 32 + 1, 0, twice, on, [&](int j) { return z_of[j]; });
+    const RowSums sums = finish_sums<THREADS / 64, REST>(a, t, listed, REST && twice, room, lane, wave, [&] {
         Sums u{kLowest, 0.0f};
         for (int i = tid; i < vectors; i += THREADS) add_vector<F32, REST, false>(u, r.load(i), REST ? marks_of<E>(marks, i) : 0, a.c);
         return u;
