@@ -132,3 +132,30 @@ def test_bf16_gradients_far_from_zero(shape, T, rest):
     for i, x in enumerate((1000, 2000, 2500, 2839, 2840, 3000, 5000, 20000)):
         a["z"][i] = rounded(x * T + 10 * np.random.default_rng(i).normal(size=V), dtype)
     all_calls(a, dtype, n, lambda loss, grad, stats: check_all(a, dtype, loss, grad, stats))
+
+
+@pytest.mark.parametrize("dtype,V,n", [(BF, 5003, 0), (BF, 70001, 0), (F32, 5003, 0), (F32, 33001, 0), (F32, 60001, 130)])
+@pytest.mark.parametrize("T", [2.0 ** -120, 1e-20, 1e-6, 1e-3, 1e3, 1e20, 1e37])
+def test_extreme_temperatures(T, dtype, V, n):
+    """log2 e / T over fp32's whole range: all of q on the largest logits, or none anywhere.  The loss carries T^2: above fp32's
+    largest number (2^128 less half a step of 2^104) it rounds to infinity, and below 2^-126 its half step is 2^-150."""
+    T = float(np.float32(T))
+    say(f"distill T={T} {V} {dtype}")
+    rng = np.random.default_rng(V + 3)
+    a = rows_of(rng, rng.normal(size=(6, V)) * 2, 9, dtype, T, False)
+    a["z"][1, :V // 3] = rounded(-1e10, dtype)
+    a["z"][2] = rounded(1e10 + 1e9 * rng.normal(size=V), dtype)
+    a["z"][3] = rounded(1e-3 * rng.normal(size=V), dtype)
+    a["z"][4], a["t"][4] = 0.0, 0.0
+    a["weight"][:] = np.float32(min(1.0, 1 / T))
+    want = ref.distill(a["z"], a["t"], a["ids"], T, None, a["weight"], 0.5)
+    lb = bounds(a, 0.5, dtype == BF, want)[0] + 2.0 ** -150
+
+    def see(loss, grad, stats):
+        got, most = loss.double().cpu().numpy(), 2.0 ** 128 - 2.0 ** 103
+        sure = np.abs(want[0] - most) > lb
+        assert np.array_equal(np.isposinf(got)[sure], want[0][sure] >= most)
+        fine = np.isfinite(got)
+        assert np.all(np.abs(got[fine] - want[0][fine]) <= lb[fine])
+        check_all(a, dtype, None, grad, stats)
+    all_calls(a, dtype, n, see)
