@@ -630,7 +630,8 @@ int ngram_dequant_int4(const ngram_int4* q, void* y, int32_t y_dtype, ngram_stre
  * 2^-24 (156 (group + 1) sum over groups of scale sum |x| + 2 (groups + 10) sum |x w|)
  * of the exact sum, and its rounding (that the bound has to allow for every
  * rounding in one direction makes it wide: fp32 results of 32 x 2560 x 151936
- * are 2e-7 of their norm off).  A row of x that holds an infinity or a NaN, or values above 2^115,
+ * are 2e-7 of their norm off).  fp32 x counts in steps of 2^-133, bf16's smallest, which numbers below 2^-110 notice: up
+ * to 31 scale 2^-133 more for each.  A row of x that holds an infinity or a NaN, or values above 2^115,
  * gives NaN or infinities; other rows are not touched by it.  n = 0 launches nothing. */
 int ngram_project_int4(const void* x, int32_t x_dtype, int64_t n, const ngram_int4* W, void* y, int32_t y_dtype,
                        ngram_stream_t stream);
