@@ -1,5 +1,6 @@
 // Beam search for MI355X (gfx950): ngram_beam_step, ngram_beam_reorder.  The
-// formulas are in include/ngram.h.
+// formulas are in include/ngram.h.  Times in comments are on the
+// card: of one kernel, or of a call replayed in a graph.
 #include "rows8.h"
 
 #include <algorithm>

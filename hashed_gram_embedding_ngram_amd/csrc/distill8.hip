@@ -1,5 +1,6 @@
 // Distillation from a teacher's top logits for MI355X (gfx950): ngram_distill
-// and ngram_distill_grad.  The formulas are in include/ngram.h.
+// and ngram_distill_grad.  The formulas are in include/ngram.h.  Times in comments are on the
+// card: of one kernel, or of a call replayed in a graph.
 #include "rows8.h"
 
 #include <algorithm>
@@ -64,8 +65,9 @@ __device__ __forceinline__ double wave_sum_f64(double x) {
 // floor), so that |m c| is at most 2^20 and the rounding 2^-4 in every thread of a row whose
 // largest logit lies within 2^19 / c; a logit below the floor (a masked one of -1e9, say) adds
 // exactly 0 to such a row.  Other rows (logits of hundreds of thousands and more
-// times T, masked throughout among them) are summed once more by (x - m) c.  Without the floor a thread
-// whose first vector is masked by -1e10 would hold infinity, to be multiplied with 0 later.
+// times T, masked throughout among them) are summed once more by (x - m) c: 4096 x 151936 bf16 with the
+// gradient and the rest 521 us, 826 where all rows are.  Without the floor a thread whose
+// first vector is masked by -1e10 would hold infinity, to be multiplied with 0 later.
 //
 // With the teacher's rest the pass leaves listed tokens out and takes the unlisted ones'
 // sum about their own largest logit, however far that lies below the row's (in a sum about
@@ -282,7 +284,7 @@ __device__ __forceinline__ Sums listed_sums(const DistillArgs& a, const Row<F32>
 }
 
 // The sums of a chunk of a row; the row's loss where it is one chunk.  1021 x
-// 32003 fp32 with the rest: 29 us, 4.5 TB/s, bound by memory and the marks in LDS.
+// 32003 fp32 with the rest: 28 us, 4.6 TB/s, bound by memory and the marks in LDS.
 template <bool F32, bool REST>
 __global__ void __launch_bounds__(kThreads) distill_stats_kernel(const DistillArgs a) {
     constexpr int E = Row<F32>::E;
@@ -454,7 +456,8 @@ __device__ __forceinline__ Slope slope_of(const DistillArgs& a, float gs, const 
     return s;
 }
 // From the forward's statistics: the unlisted tokens' softmax about the row's largest logit, which loses log Q's
-// rounding and its own, as much as log Q is large; from kFar on the row is summed once more.
+// rounding and its own, as much as log Q is large; from kFar on the row is summed once more, by one
+// workgroup (1021 x 32003 fp32 70 us against 44, 24 x 151936 bf16 39 against 8).
 constexpr float kFar = -64.0f;
 __device__ __forceinline__ bool far_rest(float log_q) { return log_q < kFar && log_q > kNegInf; }
 template <bool REST>
@@ -474,7 +477,7 @@ __device__ __forceinline__ Slope slope_given(float m, float log_s, float log_q, 
 // The gradient of a chunk of a row, from the forward's statistics or from the
 // chunks' sums (then the row's first workgroup writes its loss): a q
 // everywhere, then the listed tokens once more.  Their logits are read before anything is
-// written, since dz may be z.  1021 x 32003 fp32 with the rest: 47 to 52 us, 5.2 TB/s,
+// written, since dz may be z.  1021 x 32003 fp32 with the rest: 47 to 53 us, 5.2 TB/s,
 // bound by memory; of few rows (24 x 151936 bf16, 8 us) by the teacher's fp64 side,
 // which every chunk computes.
 template <bool F32, bool REST, bool STREAM>
@@ -592,9 +595,9 @@ __global__ void __launch_bounds__(kThreads) distill_grad_kernel(const DistillArg
 // wavefronts a compute unit: 4096 x 151936 bf16 took 546 us with all of a row in
 // registers (512 threads, 38 vectors each), 560 as one stream that asks for the next row as it stores this
 // one, 586 with nothing kept (read twice, from the last-level cache the second time); 1024 threads with 14
-// vectors each and the rest read again 498.  Rows of up to 6144 vectors fit whole: 512 threads, two or three
-// workgroups a unit (4096 x 32003 bf16 143 us, with 1024 threads 198); up to 2048 with a third of the registers
-// (4096 x 5003 bf16 46 us, 61 with all).
+// vectors each and the rest read again 496.  Rows of up to 6144 vectors fit whole: 512 threads, two or three
+// workgroups a unit (4096 x 32003 bf16 140 us, with 1024 threads 198); up to 2048 with a third of the registers
+// (4096 x 5003 bf16 43 us, 61 with all).
 constexpr int kRowMarks = 1 << 18;      // tokens of a row at most
 
 // The teacher's side is one wavefront's work while the row's loads are on
@@ -684,7 +687,7 @@ __global__ void __launch_bounds__(THREADS) distill_row_kernel(const DistillArgs 
 }
 
 // Workgroups a row: one where rows fill the card; few rows are cut into parts
-// of 512 vectors and more, for 512 workgroups.  (24 x 151936 bf16 with the gradient 15.7 us, for 1024 workgroups 20.0,
+// of 512 vectors and more, for 512 workgroups.  (24 x 151936 bf16 with the gradient, 15.1 us now, was 15.7, for 1024 workgroups 20.0,
 // for 256 15.2; 96 rows 24, 29 and 26.  Parts of 256 vectors: 16 rows 16.4 against 14.2.)
 int chunks_of(int64_t n, int64_t v, int dtype) {
     const int64_t e = dtype == NGRAM_F32 ? 4 : 8, vectors = (v + e - 1) / e;
@@ -774,9 +777,9 @@ void launch_grad(const DistillArgs& a, bool f32, hipStream_t st) {
 }
 
 // Rows in one workgroup each, loss and gradient in one launch: short ones, or enough of them to fill the card, and
-// short enough for the marks.  us, so and apart: 1 x 1001 bf16 6.8 and 13.3, 1 x 32003 fp32 10.4 and 11.9, 256 x 32003
-// bf16 14.7 and 27, 200 x 151936 bf16 36 and 46, 128 x 151936 fp32 40, 120 of them apart 42; but 24 x 151936 bf16 22
-// and 16, 96 of them 27 and 24.
+// short enough for the marks.  us, so and apart: 1 x 1001 bf16 6.2 and 13.3, 1 x 32003 fp32 9.2 and 11.9, 256 x 32003
+// bf16 14.0 and 27, 200 x 151936 bf16 36 and 46, 128 x 151936 fp32 37, 120 of them apart 41; but 24 x 151936 bf16 22
+// and 15, 96 of them 27 and 23.
 bool whole_rows(const DistillArgs& a, int64_t e) { return a.v <= kRowMarks && (a.v <= 8192 * e || a.n >= 128); }
 
 template <bool F32, bool REST, bool STREAM, int THREADS, int NV>

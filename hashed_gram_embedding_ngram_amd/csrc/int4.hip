@@ -1,6 +1,7 @@
 // Weights in 4 bits with a scale (and a zero) for each group of columns, for
 // MI355X (gfx950): ngram_quant_int4, ngram_dequant_int4 and the product
-// ngram_project_int4.  The formats and formulas are in include/ngram.h.
+// ngram_project_int4.  The formats and formulas are in include/ngram.h.  Times in comments are on the
+// card: of one kernel, or of a call replayed in a graph.
 #include "common8.h"
 
 #include <algorithm>
